@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
-SOURCES = ["kvq_append.cu", "kvq_dequant.cu", "kvq_decode.cu", "kvq_decode_test_wait.cu", "kvq_decode_tc.cu", "kvq_merge.cu", "kvq_decode_api.cu", "kvq_sweep.cu", "kvq_prefill.cu", "kvq_replay.cu"]
+SOURCES = ["kvq_append.cu", "kvq_dequant.cu", "kvq_decode.cu", "kvq_decode_test_wait.cu", "kvq_decode_tc.cu", "kvq_merge.cu", "kvq_decode_api.cu", "kvq_sweep.cu", "kvq_prefill.cu", "kvq_replay.cu",
+           "kvq_rope_append.cu", "kvq_block8_dequant.cu", "kvq_block8_decode.cu", "kvq_block8_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177"]
@@ -37,7 +38,8 @@ def _stale(lib: str) -> bool:
         return True
     t = os.path.getmtime(lib)
     inputs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
-        os.path.join(HERE, "..", "include", "kvq.h"), os.path.abspath(__file__)]
+        os.path.join(HERE, "..", "include", "kvq.h"), os.path.join(HERE, "..", "include", "kvq_fp8_block.h"),
+        os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in inputs if os.path.exists(p))
 
 

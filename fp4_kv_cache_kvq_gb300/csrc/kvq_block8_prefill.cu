@@ -1,0 +1,834 @@
+// kvq_block8_prefill.cu -- chunked-prefill attention over the 8-bit block
+// cache on the 5th-generation tensor cores (tcgen05, accumulators in TMEM),
+// and its C entry points.
+//
+// Mathematics.  Query token i of n sits at position T - n + i and attends
+// 0 .. T - n + i.  With one K and one V scale per 16 positions,
+//   S = q . code_K,  y = S (softmax_scale log2 e sK),  P = 2^(y - m),
+//   O = sum P (sV / sV_ref) code_V,  out = sV_ref O / sum P.
+// S takes the cached K codes as they are: q, scaled per row by a power of two
+// to [2^7, 2^8), is the sum of two E4M3 values hi = RNE(q) and lo = q - hi
+// (a bf16 value has 8 significant bits and an E4M3 value 4; lo is exact down
+// to 2^-10 of the row's largest element and off by at most 2^-18 of it under
+// that), so S = hi . K + lo . K are two fp8 products, which together cost one
+// f16 product and need no expansion of K.  V is expanded to f16 with sV/sV_ref
+// (sV_ref the largest V scale of the CTA's positions: the ratio is a power of
+// two <= 1, so the product is exact down to 2^-24), and P is rounded to f16
+// (2^-11 relative): f16 keeps the weights finer than an fp8 P could.
+// Accumulation, maxima and sums are fp32.
+//
+// What bounds it: the tensor pipe, 4 Hq d flop per attended pair.  Work split:
+// a CTA takes 256 query rows (G heads x 256/G tokens) of one kv head as two
+// 128-row tiles that share each 128-position cache tile; when few rows would
+// leave SMs idle, the positions are split over several CTAs too and a second
+// launch joins their partials.
+// Fourteen warps: softmax (2 x 4, thread = row), V expansion (4), loader (1),
+// MMA issue (1 thread), joined by mbarriers (every wait bounded):
+//   loader    bulk copies of K codes, V codes and scales into rings of 3 tiles;
+//             the pool's K layout is the tensor core's operand layout
+//   MMA       S_X(j) = Qhi_X K(j)^T + Qlo_X K(j)^T   kind::f8f6f4
+//             O_X += P_X(j) V^(j)                    kind::f16, P_X from TMEM
+//             in the order O_A(j), S_A(j+1), O_B(j), S_B(j+1)
+#include "kvq_block8.cuh"
+#include "kvq_common.cuh"
+#include "kvq_host.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kT = 128;         // cache positions per tile
+constexpr int kRows = 128;      // rows of one query tile (the MMA's M)
+constexpr int kXTiles = 2;      // query tiles per CTA
+constexpr int kCtaRows8 = kXTiles * kRows;
+constexpr int kSmWarps = 4 * kXTiles;
+constexpr int kExpWarps = 4;
+constexpr int kLdWarp = kSmWarps + kExpWarps;
+constexpr int kMWarp = kLdWarp + 1;
+constexpr int kP8Threads = 32 * (kMWarp + 1);
+constexpr int kOCol8 = kXTiles * kT;  // TMEM: S_X (then P_X) at [128 X, +128), O_X at [256 + 128 X, +d)
+constexpr int kTmem8 = 512;
+constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
+constexpr float kSlack8 = 8.0f;
+constexpr uint32_t kPoll8 = 20000;
+constexpr int kScaleBytes = 128;  // scales of one tile: up to 8 groups of 16 bytes
+
+enum : int {
+  kKFull = 0,                      // [kKRing] K codes and scales landed
+  kKEmpty = kKFull + kKRing,       // [kKRing] S products done (commit), softmax warps have the scales
+  kV8Full = kKEmpty + kKRing,      // [kVRing] V codes and scales landed
+  kV8Empty = kV8Full + kVRing,     // [kVRing] expanded (one arrival per warp)
+  kVFull = kV8Empty + kVRing,      // [kVSlots8] V^ slot written
+  kVEmpty = kVFull + kVSlots8,     // [kVSlots8] O products done with it (commit)
+  kSFull = kVEmpty + kVSlots8,     // [kXTiles] S_X in TMEM
+  kPFull = kSFull + kXTiles,       // [kXTiles] P_X in TMEM, O_X rescaled
+  kPvDone = kPFull + kXTiles,      // [kXTiles] O_X += P_X V^ done
+  kBars8 = kPvDone + kXTiles
+};
+
+struct Prefill8Params {
+  const int32_t* lens;
+  const int32_t* chunk_lens;
+  kvq_cache c;
+  const uint16_t* q;
+  void* out;
+  float* part_o;   // [splits][batch * chunk * hq][D] when splits > 1
+  float* part_ml;  // [splits][batch * chunk * hq][2]
+  int32_t* flag;
+  int32_t batch, hkv, g, hq, chunk, splits, qpb, nqb, out_bf16;
+  float qk_log2;
+};
+
+template <int D>
+struct P8Geo {
+  static constexpr int kQBytes = kRows * D;              // one tile of hi or lo
+  static constexpr int kQ = 0;                           // [tile][hi, lo]
+  static constexpr int kK = kQ + 2 * kXTiles * kQBytes;  // [kKRing][128 positions][D]
+  static constexpr int kV8 = kK + kKRing * kT * D;       // [kVRing]
+  static constexpr int kV = kV8 + kVRing * kT * D;       // [kVSlots8][D][128] f16
+  static constexpr int kKS = kV + kVSlots8 * kT * D * 2;
+  static constexpr int kVS = kKS + kKRing * kScaleBytes;
+  static constexpr int kBar = kVS + kVRing * kScaleBytes;
+  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, sV_ref bits, masks
+  static constexpr int kUsed = kMisc + 4 * (3 + kKRing + kVRing) + 128;
+  // at least half an SM's shared memory, so that one CTA (holding all 512
+  // TMEM columns) runs per SM
+  static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
+  static_assert(kBar % 8 == 0 && kBytes <= 227 * 1024, "shared-memory layout");
+};
+
+__device__ __forceinline__ bool pwait8(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (mbar_try_wait_hint(bar, parity, kPoll8)) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// one outcome for the whole warp (TMEM accesses are warp-collective)
+__device__ __forceinline__ bool wwait8(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, pwait8(bar, parity, abort));
+}
+
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// D[tmem] (+)= A[desc] * B[desc]^T, E4M3 operands, fp32 accumulator.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Scale pair of 16-position block i of a tile staged by groups of GT tokens.
+template <int GT>
+__device__ __forceinline__ uint32_t scale_at(uint32_t base, int i) {
+  return base + (GT == 16 ? 16 * i : 8 * i);
+}
+
+// The largest |score * csk| of 16 scores of a block, masked from lim on.
+template <bool FAST>
+__device__ __forceinline__ float block_max(const uint32_t* v, int c0, int lim, float csk, float m) {
+  float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (FAST || c0 + 2 * i < lim) a = fmaxf(a, __uint_as_float(v[2 * i]));
+    if (FAST || c0 + 2 * i + 1 < lim) b = fmaxf(b, __uint_as_float(v[2 * i + 1]));
+  }
+  a = fmaxf(a, b);
+  if (FAST) return fmaxf(m, a * csk);
+  return a == -INFINITY ? m : fmaxf(m, a * csk);
+}
+
+// P = 2^(S csk - m) for 16 scores as 8 f16 pairs, their sum into l2.
+template <bool FAST>
+__device__ __forceinline__ void block_p(const uint32_t* v, uint32_t* w, int c0, int lim, float csk, uint64_t nref2,
+                                        uint64_t (&l2)[2]) {
+  const uint64_t cs2 = pk2(csk, csk);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float y0, y1;
+    upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cs2, nref2), y0, y1);
+    float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+    if (!FAST) {
+      if (c0 + 2 * i >= lim) e0 = 0.0f;
+      if (c0 + 2 * i + 1 >= lim) e1 = 0.0f;
+    }
+    l2[i & 1] = add2(l2[i & 1], pk2(e0, e1));
+    w[i] = pack_f16x2(e0, e1);
+  }
+}
+
+template <int D, int GT>
+__global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Prefill8Params p) {
+  using G = P8Geo<D>;
+  constexpr int kGroups = kT / GT;
+  constexpr int kGroupBytes = 2 * GT * D + (GT >= 32 ? GT / 2 : 16);
+  constexpr int kGroupScale = GT >= 32 ? GT / 2 : 16;
+  extern __shared__ uint8_t p8_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p8_raw) + 127) & ~uintptr_t(127));
+  const uint32_t sb = smem_addr(base);
+  const uint32_t bars = sb + G::kBar;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
+  uint32_t* tslot = misc;
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
+  uint32_t* vref_bits = misc + 2;
+  volatile uint32_t* kgood = misc + 3;             // [kKRing] bit i: block i of the tile lies in a valid page
+  volatile uint32_t* vgood = misc + 3 + kKRing;    // [kVRing]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int sp = (int)(blockIdx.x % (unsigned)p.splits);
+  const int rest = (int)(blockIdx.x / (unsigned)p.splits);
+  const int qb = p.nqb - 1 - rest % p.nqb;  // the longest first
+  const int bh = rest / p.nqb;
+  const int h = bh % p.hkv, b = bh / p.hkv;
+  const int32_t T = __ldg(p.lens + b);
+  const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
+  if (n < 0 || n > p.chunk || T < 0) {
+    if (tid == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
+    if (n < 0 || n > p.chunk) return;
+  }
+  if (qb * p.qpb >= n) return;  // padding only
+  const int ti = qb * p.qpb + tid / p.g;  // softmax threads: the row's query token and head
+  const int hh = h * p.g + tid % p.g;
+  const int X = tid / kRows;
+  const bool row_ok = tid < p.qpb * p.g && ti < n;
+  const int64_t row = ((int64_t)b * p.chunk + ti) * p.hq + hh;
+  const int64_t rows_all = (int64_t)p.batch * p.chunk * p.hq;
+  if (T < n) {  // the chunk's own tokens must be in the cache
+    if (tid == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
+    if (row_ok) {
+      if (p.splits > 1) {
+        *(reinterpret_cast<float2*>(p.part_ml) + sp * rows_all + row) = make_float2(-INFINITY, 0.0f);
+      } else {
+        for (int c = 0; c < D; c += 8) {
+          if (p.out_bf16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c) = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + c);
+            o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      }
+    }
+    return;
+  }
+  const int64_t first = (int64_t)T - n;             // position of the chunk's token 0
+  const int64_t pos_min = first + qb * p.qpb;       // last position that every row of the CTA attends
+  const int last_ti = min(n, (qb + 1) * p.qpb) - 1;
+  const int64_t cap = (int64_t)p.c.max_pages_per_seq * p.c.page_size;
+  const int64_t limit = min(first + last_ti + 1, cap);  // positions read
+  if (tid == 0 && first + last_ti + 1 > cap) set_flag(p.flag, KVQ_FLAG_PAGE_OOB);
+  const int tiles = (int)((limit + kT - 1) / kT);
+  const int per = (tiles + p.splits - 1) / p.splits;
+  const int j0 = min(tiles, sp * per), ntiles = min(tiles, j0 + per) - j0;
+  const int rows_used = (last_ti - qb * p.qpb + 1) * p.g;
+  const int nx = rows_used > kRows ? 2 : 1;         // query tiles with rows
+  if (ntiles <= 0) {                                // a split without positions
+    if (row_ok) *(reinterpret_cast<float2*>(p.part_ml) + sp * rows_all + row) = make_float2(-INFINITY, 0.0f);
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kKRing; ++i) {
+      mbar_init(bars + 8 * (kKFull + i), 1);
+      mbar_init(bars + 8 * (kKEmpty + i), 1 + 4 * nx);
+    }
+    for (int i = 0; i < kVRing; ++i) {
+      mbar_init(bars + 8 * (kV8Full + i), 1);
+      mbar_init(bars + 8 * (kV8Empty + i), kExpWarps);
+    }
+    for (int i = 0; i < kVSlots8; ++i) {
+      mbar_init(bars + 8 * (kVFull + i), 32 * kExpWarps);
+      mbar_init(bars + 8 * (kVEmpty + i), 1);
+    }
+    for (int i = 0; i < kXTiles; ++i) {
+      mbar_init(bars + 8 * (kSFull + i), 1);
+      mbar_init(bars + 8 * (kPFull + i), 32 * 4);
+      mbar_init(bars + 8 * (kPvDone + i), 1);
+    }
+    *abort = 0;
+    *vref_bits = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
+  __syncthreads();
+
+  // sV_ref: the largest V scale of the positions this CTA reads
+  const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
+  const Block8Layout L(D, p.c.page_size);
+  {
+    uint32_t best = 0u;
+    const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
+    for (int64_t gi = g0 + tid; gi < g1; gi += kP8Threads) {
+      const int64_t phys = block8_page(p.c, b, gi * GT, p.flag);
+      if (phys < 0) continue;
+      const uint8_t* grp = pool + block8_group_offset(L, phys, p.hkv, h, (int)((gi * GT) & (p.c.page_size - 1)));
+#pragma unroll
+      for (int k = 0; k < GT / 16; ++k) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(grp + L.scale(k, 1)));
+        if (gi * GT + 16 * k < limit && v < 0x7F800000u) best = max(best, v);
+      }
+    }
+    best = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (lane == 0 && best != 0u) atomicMax(vref_bits, best);
+  }
+
+  // query rows: power-of-two prescale, hi and lo E4M3 parts in operand layout
+  float cs = 0.0f;
+  if (warp < kSmWarps) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
+    uint32_t amax = 0u;
+    if (row_ok) {
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 w = __ldg(src + i);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max((ws[k] << 16) & 0x7FFF0000u, ws[k] & 0x7FFF0000u));
+      }
+    }
+    int k = 0;
+    if (amax > 0u && amax < 0x7F800000u) k = min(100, max(-120, 7 - ((int)(amax >> 23) - 127)));
+    const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+    const uint32_t dst = sb + G::kQ + X * 2 * G::kQBytes + (uint32_t)(((tid % kRows) >> 3) * 8 * D + (tid & 7) * 16);
+#pragma unroll 2
+    for (int c16 = 0; c16 < D / 16; ++c16) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (row_ok) w = __ldg(src + 2 * c16 + half);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t hp[4], lp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = bf16_lo(ws[i]) * up, x1 = bf16_hi(ws[i]) * up;
+          hp[i] = e4m3x2_from_f32(x0, x1);
+          const float2 f = f16x2_to_float2(f16x2_from_e4m3x2(hp[i]));
+          lp[i] = e4m3x2_from_f32(x0 - f.x, x1 - f.y);
+        }
+        hi[2 * half] = hp[0] | (hp[1] << 16);
+        hi[2 * half + 1] = hp[2] | (hp[3] << 16);
+        lo[2 * half] = lp[0] | (lp[1] << 16);
+        lo[2 * half + 1] = lp[2] | (lp[3] << 16);
+      }
+      sts128(dst + 128 * c16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sts128(dst + G::kQBytes + 128 * c16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
+    cs = p.qk_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+    if (amax >= 0x7F800000u) cs = __uint_as_float(0x7FC00000u);  // Inf or NaN query: the row is NaN
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
+  const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
+
+  if (warp < kSmWarps) {
+    // ---------------------------------------------------------------- softmax
+    if (X < nx) {
+      const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t sp_col = t_lane + (uint32_t)(X * kT);
+      const uint32_t op = t_lane + (uint32_t)(kOCol8 + X * kT);
+      const uint32_t s_full = bars + 8 * (kSFull + X), p_full = bars + 8 * (kPFull + X);
+      const uint32_t pv_done = bars + 8 * (kPvDone + X);
+      const int64_t pos_r = first + ti;  // last position this row attends
+      float m_run = -INFINITY, l_run = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < ntiles; ++j) {
+        const int ks = j % kKRing;
+        if (!(ok = wwait8(s_full, (uint32_t)j & 1u, abort))) break;
+        // the tile's K scales (landed before S could be formed; this wait makes
+        // the copy visible to this thread)
+        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kKRing) & 1u, abort))) break;
+        tc_fence_after();
+        float csk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          csk[i] = cs * __uint_as_float(lds32(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, i)));
+        const uint32_t good = kgood[ks];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
+        const int64_t p0 = (int64_t)(j0 + j) * kT;
+        const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
+        const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
+        // the tile in two halves of 64 scores, each read from TMEM once: the
+        // maximum against the lazy reference, then P over the same registers.
+        // A raise of the reference shrinks what was accumulated against the
+        // old one: l, O and, in the second half, the first half's P.
+        uint64_t l2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t va[32], vb[32];
+          tmem_ld32_async(sp_col + (uint32_t)(64 * hf), va);
+          tmem_ld32_async(sp_col + (uint32_t)(64 * hf + 32), vb);
+          tmem_wait_ld(va);
+          tmem_wait_ld(vb);
+          float mt = -INFINITY;
+          int lb[4];  // masked from here on, per block
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lb[i] = ((good >> (4 * hf + i)) & 1u) ? lim : 0;
+          if (fast) {
+            mt = block_max<true>(va, 0, 0, csk[4 * hf], mt);
+            mt = block_max<true>(va + 16, 0, 0, csk[4 * hf + 1], mt);
+            mt = block_max<true>(vb, 0, 0, csk[4 * hf + 2], mt);
+            mt = block_max<true>(vb + 16, 0, 0, csk[4 * hf + 3], mt);
+          } else {
+            mt = block_max<false>(va, 64 * hf, lb[0], csk[4 * hf], mt);
+            mt = block_max<false>(va + 16, 64 * hf + 16, lb[1], csk[4 * hf + 1], mt);
+            mt = block_max<false>(vb, 64 * hf + 32, lb[2], csk[4 * hf + 2], mt);
+            mt = block_max<false>(vb + 16, 64 * hf + 48, lb[3], csk[4 * hf + 3], mt);
+          }
+          float al = 1.0f;
+          if (mt > m_run + kSlack8) {
+            if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
+            m_run = mt;
+          }
+          if (__any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
+            if (hf == 1) {
+              const uint32_t al2 = pack_f16x2(al, al);
+              tmem_wait_st();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t pw[16];
+                tmem_ld16(sp_col + (uint32_t)(16 * k), pw);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pw[i] = hmul2_u32(pw[i], al2);
+                tmem_st16_async(sp_col + (uint32_t)(16 * k), pw);
+              }
+            }
+            {
+              float a0, a1, b0, b1;
+              upk2(l2[0], a0, a1);
+              upk2(l2[1], b0, b1);
+              l2[0] = pk2(a0 * al, a1 * al);
+              l2[1] = pk2(b0 * al, b1 * al);
+            }
+            if (j > 0) {  // O: once O_X += P_X V^ of the previous tile is done
+              if (!(ok = wwait8(pv_done, (uint32_t)(j - 1) & 1u, abort))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(op + (uint32_t)c0, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st16_async(op + (uint32_t)c0, o);
+              }
+            }
+          }
+          l_run *= al;
+          const float nref = m_run == -INFINITY ? 0.0f : -m_run;
+          const uint64_t nref2 = pk2(nref, nref);
+          uint32_t w[16];
+          if (fast) {
+            block_p<true>(va, w, 0, 0, csk[4 * hf], nref2, l2);
+            block_p<true>(va + 16, w + 8, 0, 0, csk[4 * hf + 1], nref2, l2);
+            tmem_st16_async(sp_col + (uint32_t)(32 * hf), w);
+            block_p<true>(vb, w, 0, 0, csk[4 * hf + 2], nref2, l2);
+            block_p<true>(vb + 16, w + 8, 0, 0, csk[4 * hf + 3], nref2, l2);
+            tmem_st16_async(sp_col + (uint32_t)(32 * hf + 16), w);
+          } else {
+            block_p<false>(va, w, 64 * hf, lb[0], csk[4 * hf], nref2, l2);
+            block_p<false>(va + 16, w + 8, 64 * hf + 16, lb[1], csk[4 * hf + 1], nref2, l2);
+            tmem_st16_async(sp_col + (uint32_t)(32 * hf), w);
+            block_p<false>(vb, w, 64 * hf + 32, lb[2], csk[4 * hf + 2], nref2, l2);
+            block_p<false>(vb + 16, w + 8, 64 * hf + 48, lb[3], csk[4 * hf + 3], nref2, l2);
+            tmem_st16_async(sp_col + (uint32_t)(32 * hf + 16), w);
+          }
+        }
+        if (!ok) break;
+        tmem_wait_st();
+        {
+          float a0, a1, b0, b1;
+          upk2(l2[0], a0, a1);
+          upk2(l2[1], b0, b1);
+          l_run += (a0 + a1) + (b0 + b1);
+        }
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      // the result once the last O_X += P_X V^ is done
+      if (ok) ok = wwait8(pv_done, (uint32_t)(ntiles - 1) & 1u, abort);
+      if (ok) {
+        tc_fence_after();
+        const bool part = p.splits > 1;
+        const float f = part ? vref : (l_run > 0.0f || l_run != l_run ? vref / l_run : 0.0f);
+        float* of = part ? p.part_o + (sp * rows_all + row) * D : static_cast<float*>(p.out) + row * D;
+        uint16_t* ob = static_cast<uint16_t*>(p.out) + row * D;
+        if (part && row_ok) *(reinterpret_cast<float2*>(p.part_ml) + sp * rows_all + row) = make_float2(m_run, l_run);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(op + (uint32_t)c0, o);
+          if (!row_ok) continue;
+          if (p.out_bf16 && !part) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = bf16x2_of(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+              *reinterpret_cast<uint4*>(ob + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(of + c0 + i) =
+                  make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f,
+                              __uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
+          }
+        }
+      }
+    }
+  } else if (warp < kSmWarps + kExpWarps) {
+    // ------------------------------------------------------------ V expansion
+    // item (channel c, 16-position block): one 16-byte row of codes to two
+    // 16-byte rows of f16; lanes take consecutive channels, so loads and
+    // stores touch 128 contiguous bytes per eight lanes
+    const int dt = tid - 32 * kSmWarps;
+    const float vinv = vref > 0.0f ? 1.0f / vref : 0.0f;
+    for (int j = 0; j < ntiles; ++j) {
+      const int s = j % kVRing, slot = j % kVSlots8;
+      const uint32_t codes = sb + G::kV8 + s * kT * D, dst = sb + G::kV + slot * kT * D * 2;
+      const int valid = (int)min((int64_t)kT, limit - (int64_t)(j0 + j) * kT);
+      if (!wwait8(bars + 8 * (kV8Full + s), (uint32_t)(j / kVRing) & 1u, abort)) break;
+      if (j >= kVSlots8 && !wwait8(bars + 8 * (kVEmpty + slot), (uint32_t)(j / kVSlots8 - 1) & 1u, abort)) break;
+      const uint32_t good = vgood[s];
+      const bool whole = valid == kT && good == 0xFFu;
+#pragma unroll 2
+      for (int it = dt; it < D * (kT / 16); it += 32 * kExpWarps) {
+        const int c = it % D, blk = it / D;
+        uint4 w = lds128(codes + (uint32_t)((blk * D + c) * 16));
+        const float r = __uint_as_float(lds32(scale_at<GT>(sb + G::kVS + s * kScaleBytes, blk) + 4)) * vinv;
+        uint32_t r2 = pack_f16x2(r, r);
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        if (!whole) {  // positions that are not attended: zero codes and a finite factor
+          const int left = ((good >> blk) & 1u) ? valid - 16 * blk : 0;
+          if (left <= 0) r2 = 0u;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            ws[t] &= (2 * t < left ? 0x000000FFu : 0u) | (2 * t + 1 < left ? 0x0000FF00u : 0u) |
+                     (2 * t + 8 < left ? 0x00FF0000u : 0u) | (2 * t + 9 < left ? 0xFF000000u : 0u);
+        }
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          lo[t] = hmul2_u32(f16x2_from_e4m3x2(ws[t] & 0xFFFFu), r2);
+          hi[t] = hmul2_u32(f16x2_from_e4m3x2(ws[t] >> 16), r2);
+        }
+        const uint32_t at = dst + core_offset((uint32_t)c, (uint32_t)(16 * blk), D);
+        sts128(at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        sts128(at + (D / 8) * 128, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kV8Empty + s));
+      fence_async_smem();
+      mbar_arrive(bars + 8 * (kVFull + slot));
+    }
+  } else if (warp == kLdWarp) {
+    // ------------------------------------------------------------ bulk copies
+    // lane i < kGroups copies group i of each tile: K codes and scales, then V
+    // codes and scales
+    int kiss = 0, viss = 0;
+    for (int j = 0; j < ntiles; ++j) {
+      const int ks = j % kKRing, vs = j % kVRing;
+      const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
+      const uint8_t* src = nullptr;
+      if (lane < kGroups && pos < limit) {
+        const int64_t phys = block8_page(p.c, b, pos, p.flag);
+        if (phys >= 0) {
+          const int64_t off = block8_group_offset(L, phys, p.hkv, h, (int)(pos & (p.c.page_size - 1)));
+          if (KVQ_IN(off >= 0 && off + kGroupBytes <= p.c.num_pages * (int64_t)p.hkv * L.page_bytes(), p.flag))
+            src = pool + off;
+        }
+      }
+      const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
+      uint32_t good = 0u;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
+      const uint32_t bytes = (uint32_t)__popc(got) * (uint32_t)(GT * D + kGroupScale);
+      if (j >= kKRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kKRing - 1) & 1u, abort)) break;
+      if (lane == 0) {
+        kgood[ks] = good;
+        mbar_arrive_expect_tx(bars + 8 * (kKFull + ks), bytes);
+      }
+      __syncwarp();
+      if (src != nullptr) {
+        bulk_g2s(sb + G::kK + ks * kT * D + lane * GT * D, src, GT * D, bars + 8 * (kKFull + ks));
+        bulk_g2s(sb + G::kKS + ks * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
+                 bars + 8 * (kKFull + ks));
+      }
+      kiss = j + 1;
+      if (j >= kVRing && !wwait8(bars + 8 * (kV8Empty + vs), (uint32_t)(j / kVRing - 1) & 1u, abort)) break;
+      if (lane == 0) {
+        vgood[vs] = good;
+        mbar_arrive_expect_tx(bars + 8 * (kV8Full + vs), bytes);
+      }
+      __syncwarp();
+      if (src != nullptr) {
+        bulk_g2s(sb + G::kV8 + vs * kT * D + lane * GT * D, src + GT * D, GT * D, bars + 8 * (kV8Full + vs));
+        bulk_g2s(sb + G::kVS + vs * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
+                 bars + 8 * (kV8Full + vs));
+      }
+      viss = j + 1;
+    }
+    if (*abort) {  // copies still in flight land before the shared memory goes away
+      const auto drain = [&](int bar, int ring, int issued) {
+        for (int j = max(0, issued - ring); j < issued; ++j) {
+          const uint64_t t0 = global_ns();
+          while (!mbar_try_wait_hint(bars + 8 * (bar + j % ring), (uint32_t)(j / ring) & 1u, kPoll8) &&
+                 global_ns() - t0 < 20000000ull) {
+          }
+        }
+      };
+      drain(kKFull, kKRing, kiss);
+      drain(kV8Full, kVRing, viss);
+    }
+  } else if (lane == 0) {
+    // ----------------------------------------------------------- tensor cores
+    constexpr uint32_t kIdS = idesc_f16_f32(kRows, kT);  // E4M3 is type 0 of kind::f8f6f4, as f16 is of kind::f16
+    constexpr uint32_t kIdO = idesc_f16_f32(kRows, D);
+    uint32_t last_bar = 0, last_par = 0;
+    const auto issue_s = [&](int j, int x) {
+      const uint64_t dk = smem_desc(sb + G::kK + (j % kKRing) * kT * D, 128, 8 * D);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const uint64_t dq = smem_desc(sb + G::kQ + (2 * x + part) * G::kQBytes, 128, 8 * D);
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s)
+          tc_mma_f8(tmem + (uint32_t)(x * kT), dq + (uint64_t)(16 * s), dk + (uint64_t)(16 * s), kIdS, part + s > 0);
+      }
+      tc_commit(bars + 8 * (kSFull + x));
+      last_bar = bars + 8 * (kSFull + x);
+      last_par = (uint32_t)j & 1u;
+    };
+    bool ok = pwait8(bars + 8 * kKFull, 0u, abort);
+    if (ok) {
+      tc_fence_after();
+      for (int x = 0; x < nx; ++x) issue_s(0, x);
+      tc_commit(bars + 8 * kKEmpty);
+    }
+    for (int j = 0; j < ntiles && ok; ++j) {
+      if (!(ok = pwait8(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
+      const uint64_t dv = smem_desc(sb + G::kV + (j % kVSlots8) * kT * D * 2, (D / 8) * 128, 128);
+      for (int x = 0; x < nx; ++x) {
+        if (!(ok = pwait8(bars + 8 * (kPFull + x), (uint32_t)j & 1u, abort))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < kT / 16; ++s)
+          tc_mma_f16_ta(tmem + (uint32_t)(kOCol8 + x * kT), tmem + (uint32_t)(x * kT + s * 8),
+                        dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, j > 0 || s > 0);
+        tc_commit(bars + 8 * (kPvDone + x));
+        last_bar = bars + 8 * (kPvDone + x);
+        last_par = (uint32_t)j & 1u;
+        if (x == nx - 1) tc_commit(bars + 8 * (kVEmpty + j % kVSlots8));
+        if (j + 1 < ntiles) {
+          const int jn = j + 1;
+          if (x == 0 && !(ok = pwait8(bars + 8 * (kKFull + jn % kKRing), (uint32_t)(jn / kKRing) & 1u, abort))) break;
+          // P_X lives in S_X's columns: the next scores follow the product that reads it
+          if (!(ok = pwait8(bars + 8 * (kPvDone + x), (uint32_t)j & 1u, abort))) break;
+          tc_fence_after();
+          issue_s(jn, x);
+          if (x == nx - 1) tc_commit(bars + 8 * (kKEmpty + jn % kKRing));
+        }
+      }
+    }
+    if (*abort && last_bar != 0) {  // MMAs still running when the CTA gave up
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait_hint(last_bar, last_par, kPoll8) && global_ns() - t0 < 20000000ull) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *abort) set_flag(p.flag, KVQ_FLAG_TIMEOUT);
+  if (warp == 0) tmem_dealloc(tmem, kTmem8);
+}
+
+// Joins the splits' partials of one query row per D/4 threads.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const Prefill8Params p) {
+  grid_dependency_wait();
+  const int64_t rows = (int64_t)p.batch * p.chunk * p.hq;
+  const int64_t i = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  const int c4 = threadIdx.x % (D / 4);
+  if (i >= rows) return;
+  const int64_t tok = i / p.hq;
+  const int b = (int)(tok / p.chunk), ti = (int)(tok % p.chunk);
+  const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
+  if (n < 0 || n > p.chunk || ti >= n) return;
+  float mx = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + s * rows + i);
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // no position of this row
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + (s * rows + i) * D) + c4);
+    const float mn = fmaxf(mx, ml.x);
+    const float ref = mn == -INFINITY ? 0.0f : mn;
+    const float a = mx == -INFINITY ? 0.0f : fast_exp2(mx - ref);
+    const float f = ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - ref);
+    o = make_float4(fmaf(f, x.x, o.x * a), fmaf(f, x.y, o.y * a), fmaf(f, x.z, o.z * a), fmaf(f, x.w, o.w * a));
+    l = fmaf(f, ml.y, l * a);
+    mx = mn;
+  }
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (p.out_bf16)
+    *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + i * D) + c4) =
+        make_uint2(bf16x2_of(o.x, o.y), bf16x2_of(o.z, o.w));
+  else
+    *(reinterpret_cast<float4*>(static_cast<float*>(p.out) + i * D) + c4) = o;
+}
+
+// ------------------------------------------------------------------ host side
+constexpr int kMaxSplits = 32;
+
+// CTAs that share the positions of one block of query rows: as many as keep
+// the whole grid within one CTA per SM.
+int prefill_splits(int64_t ctas, int sms) {
+  const int64_t s = sms / (ctas > 0 ? ctas : 1);
+  return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+}
+
+size_t split_bytes(int64_t splits, int64_t rows, int d) {
+  return splits > 1 ? (size_t)splits * (size_t)rows * (size_t)(d + 2) * sizeof(float) : 16;
+}
+
+template <int D, int GT>
+kvq_status launch_prefill8(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
+  static DeviceOnce attr_set;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (attr_set.pending(dev)) {
+    if (cudaFuncSetAttribute(prefill_block8_kernel<D, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             P8Geo<D>::kBytes) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    attr_set.mark(dev);
+  }
+  prefill_block8_kernel<D, GT><<<grid, kP8Threads, P8Geo<D>::kBytes, s>>>(pp);
+  const kvq_status st = launch_status();
+  if (st != KVQ_OK || pp.splits == 1) return st;
+  const int64_t rows = (int64_t)pp.batch * pp.chunk * pp.hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + 256 / (D / 4) - 1) / (256 / (D / 4))));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, pp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+template <int D>
+kvq_status launch_prefill8_d(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
+  switch (pp.c.page_size) {
+    case 16: return launch_prefill8<D, 16>(pp, s, grid);
+    case 32: return launch_prefill8<D, 32>(pp, s, grid);
+    default: return launch_prefill8<D, 64>(pp, s, grid);
+  }
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" size_t kvq_fp8_block_prefill_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                        int32_t head_dim, int32_t chunk) {
+  if (batch < 1 || chunk < 1 || num_kv_heads < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > kCtaRows8 || head_dim < 16)
+    return 0;
+  const int sms = device_sm_count();
+  if (sms <= 0) return 0;
+  const int qpb = kCtaRows8 / (num_q_heads / num_kv_heads);
+  const int64_t ctas = ((int64_t)chunk + qpb - 1) / qpb * batch * num_kv_heads;
+  return split_bytes(prefill_splits(ctas, sms), (int64_t)batch * chunk * num_q_heads, head_dim);
+}
+
+extern "C" kvq_status kvq_fp8_block_prefill_attn(const kvq_cache* cache, int32_t batch, int32_t num_q_heads,
+                                                 int32_t chunk, const int32_t* d_seq_lens, const int32_t* d_chunk_lens,
+                                                 const void* q, float softmax_scale, void* out, int32_t out_dtype,
+                                                 void* workspace, size_t workspace_bytes, int32_t* d_err_flag,
+                                                 kvq_stream stream) {
+  if (batch < 1 || chunk < 1) return KVQ_ERR_INVALID_ARGUMENT;
+  const kvq_status st = check_block8_cache(cache, batch);
+  if (st != KVQ_OK) return st;
+  const int hkv = cache->num_kv_heads, D = cache->head_dim;
+  if (num_q_heads < hkv || num_q_heads % hkv != 0) return KVQ_ERR_INVALID_ARGUMENT;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale < 3.0e38f)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (out_dtype != KVQ_DTYPE_F32 && out_dtype != KVQ_DTYPE_BF16) return KVQ_ERR_INVALID_ARGUMENT;
+  if (d_seq_lens == nullptr || q == nullptr || out == nullptr || workspace == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(workspace, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  const int g = num_q_heads / hkv;
+  if (g > 8) return KVQ_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  const int qpb = kCtaRows8 / g;
+  const int64_t nqb = ((int64_t)chunk + qpb - 1) / qpb;
+  const int64_t ctas = nqb * batch * hkv;
+  if (ctas > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
+  // never more splits than the cache has tiles
+  const int64_t cap_tiles = ((int64_t)cache->max_pages_per_seq * cache->page_size + kT - 1) / kT;
+  int splits = prefill_splits(ctas, sms);
+  const int64_t rows = (int64_t)batch * chunk * num_q_heads;
+  if (workspace_bytes < split_bytes(splits, rows, D)) return KVQ_ERR_WORKSPACE;
+  if (splits > cap_tiles) splits = (int)cap_tiles;
+  Prefill8Params pp = {};
+  pp.lens = d_seq_lens;
+  pp.chunk_lens = d_chunk_lens;
+  pp.c = *cache;
+  pp.q = static_cast<const uint16_t*>(q);
+  pp.out = out;
+  pp.part_o = static_cast<float*>(workspace);
+  pp.part_ml = pp.part_o + (size_t)splits * rows * D;
+  pp.flag = d_err_flag;
+  pp.batch = batch;
+  pp.hkv = hkv;
+  pp.g = g;
+  pp.hq = num_q_heads;
+  pp.chunk = chunk;
+  pp.splits = splits;
+  pp.qpb = qpb;
+  pp.nqb = (int32_t)nqb;
+  pp.out_bf16 = out_dtype == KVQ_DTYPE_BF16;
+  pp.qk_log2 = softmax_scale * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)(ctas * splits);
+  return D == 128 ? launch_prefill8_d<128>(pp, s, grid) : launch_prefill8_d<64>(pp, s, grid);
+}

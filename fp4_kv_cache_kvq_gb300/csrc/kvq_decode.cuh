@@ -41,6 +41,7 @@ struct MergeParams {
   const float* part_ml;
   const int2* unit_rec;
   float* out;
+  uint16_t* out_bf16;  // written instead of `out` when set (no window)
   int32_t* flag;
   // FP8 window (k8 == nullptr: none)
   const uint8_t* k8;
@@ -89,10 +90,11 @@ struct Grp {
 };
 
 
+template <int CHUNK = kChunk>
 __device__ __forceinline__ int fp4_chunks(int32_t T, int window) {
   if (T <= 0) return 0;
   const int w = window > 0 ? min(window, T) : 0;
-  return (T - w + kChunk - 1) / kChunk;
+  return (int)(((uint32_t)(T - w) + (CHUNK - 1)) / CHUNK);
 }
 
 __device__ __forceinline__ int fp4_tokens(int32_t T, int window) {
@@ -109,7 +111,9 @@ struct Walker {
 
 // Every warp computes the same thing: the line's length and where range
 // `idx` of `count` equal ranges starts.  Lanes scan 32 sequences at a time.
-__device__ __forceinline__ void plan(const DecodeParams& p, int idx, int count, int64_t& total, int64_t& v0,
+// CHUNK: tokens per chunk (the 8-bit cache's decode takes shorter ones).
+template <int CHUNK = kChunk, class Params>
+__device__ __forceinline__ void plan(const Params& p, int idx, int count, int64_t& total, int64_t& v0,
                                      int64_t& v1, Walker& wk) {
   const int lane = threadIdx.x & 31;
   int64_t acc = 0;
@@ -117,7 +121,7 @@ __device__ __forceinline__ void plan(const DecodeParams& p, int idx, int count, 
   // pass 1: total
   for (int base = 0; base < p.batch; base += 32) {
     const int bb = base + lane;
-    int64_t x = bb < p.batch ? (int64_t)fp4_chunks(__ldg(p.lens + bb), p.window) * p.hkv : 0;
+    int64_t x = bb < p.batch ? (int64_t)fp4_chunks<CHUNK>(__ldg(p.lens + bb), p.window) * p.hkv : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
     acc += x;
@@ -136,7 +140,7 @@ __device__ __forceinline__ void plan(const DecodeParams& p, int idx, int count, 
   acc = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int bb = base + lane;
-    const int n = bb < p.batch ? fp4_chunks(__ldg(p.lens + bb), p.window) : 0;
+    const int n = bb < p.batch ? fp4_chunks<CHUNK>(__ldg(p.lens + bb), p.window) : 0;
     const int64_t x = (int64_t)n * p.hkv;
     int64_t incl = x;
 #pragma unroll
@@ -161,7 +165,8 @@ __device__ __forceinline__ void plan(const DecodeParams& p, int idx, int count, 
   }
 }
 
-__device__ __forceinline__ void advance(const DecodeParams& p, Walker& wk) {
+template <int CHUNK = kChunk, class Params>
+__device__ __forceinline__ void advance(const Params& p, Walker& wk) {
   ++wk.v;
   if (++wk.c < wk.nch) return;
   wk.c = 0;
@@ -169,7 +174,7 @@ __device__ __forceinline__ void advance(const DecodeParams& p, Walker& wk) {
   wk.h = 0;
   do {
     ++wk.b;
-    wk.nch = wk.b < p.batch ? fp4_chunks(__ldg(p.lens + wk.b), p.window) : 1;
+    wk.nch = wk.b < p.batch ? fp4_chunks<CHUNK>(__ldg(p.lens + wk.b), p.window) : 1;
   } while (wk.nch == 0);
 }
 

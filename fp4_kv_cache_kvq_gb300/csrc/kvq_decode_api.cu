@@ -170,7 +170,7 @@ kvq_status decode_attn(const kvq_cache* global, const kvq_cache* swa, int32_t ba
     st = launch_decode_mma(dp, s, ctas, after_append);
   if (st != KVQ_OK) return st;
 
-  MergeParams mp;
+  MergeParams mp = {};
   mp.lens = d_seq_lens;
   mp.q = dp.q;
   mp.part_o = dp.part_o;

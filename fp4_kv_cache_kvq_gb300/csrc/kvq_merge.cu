@@ -25,7 +25,8 @@ namespace {
 // partials in batches of kMergeBatch whose loads are all in flight at once:
 // two L2 round trips for up to kMergeBatch splits.
 constexpr int kMergeBatch = 8;
-template <int D>
+// BF16: the result is rounded once, to bf16, on its way out.
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kNG * D / 4) merge_splits_kernel(const MergeParams p) {
   grid_dependency_wait();  // the decode grid has finished and its partials are visible
   const int u = blockIdx.x;
@@ -40,10 +41,19 @@ __global__ void __launch_bounds__(kNG * D / 4) merge_splits_kernel(const MergePa
   }
   const int64_t qrow = (int64_t)b * p.hq + (int64_t)h * p.g + r;
   if (!KVQ_IN(b < p.batch, p.flag)) return;
-  float4* dst = reinterpret_cast<float4*>(p.out + qrow * D) + c4;
+  const auto store = [&](float x, float y, float z, float w) {
+    if constexpr (BF16) {
+      uint2 v;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(v.x) : "f"(y), "f"(x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(v.y) : "f"(w), "f"(z));
+      *(reinterpret_cast<uint2*>(p.out_bf16 + qrow * D) + c4) = v;
+    } else {
+      *(reinterpret_cast<float4*>(p.out + qrow * D) + c4) = make_float4(x, y, z, w);
+    }
+  };
   if (T > 0 && !KVQ_IN(rec.x >= 0 && rec.y >= 0 && (int64_t)rec.x + rec.y <= p.n_slots, p.flag)) rec.y = 0;
   if (T == 0) {
-    *dst = make_float4(0.f, 0.f, 0.f, 0.f);
+    store(0.f, 0.f, 0.f, 0.f);
     return;
   }
   // the unit's partials, kMergeBatch at a time with every load of a batch
@@ -83,7 +93,7 @@ __global__ void __launch_bounds__(kNG * D / 4) merge_splits_kernel(const MergePa
     mx = mn;
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  *dst = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  store(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
 // Merge with the FP8 window: CTAs of 256 threads, one per (unit, slice of
@@ -284,10 +294,13 @@ kvq_status launch_window_merge(const MergeParams& mp, cudaStream_t s, int smem, 
 
 kvq_status launch_merge(const MergeParams& mp, int64_t units, cudaStream_t s) {
   if (mp.k8 == nullptr) {
+    const bool bf = mp.out_bf16 != nullptr;
     const cudaError_t e =
         mp.head_dim == 128
-            ? launch_dependent(merge_splits_kernel<128>, dim3((unsigned)units), dim3(kNG * 128 / 4), 0, s, mp)
-            : launch_dependent(merge_splits_kernel<64>, dim3((unsigned)units), dim3(kNG * 64 / 4), 0, s, mp);
+            ? launch_dependent(bf ? merge_splits_kernel<128, true> : merge_splits_kernel<128, false>,
+                               dim3((unsigned)units), dim3(kNG * 128 / 4), 0, s, mp)
+            : launch_dependent(bf ? merge_splits_kernel<64, true> : merge_splits_kernel<64, false>,
+                               dim3((unsigned)units), dim3(kNG * 64 / 4), 0, s, mp);
     return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
   }
   const int wsmem = window_smem_bytes(mp.head_dim, mp.window);

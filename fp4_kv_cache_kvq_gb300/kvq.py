@@ -1,4 +1,5 @@
-"""Thin Python binding of libkvq (the C ABI declared in include/kvq.h).
+"""Thin Python binding of libkvq (the C ABI declared in include/kvq.h and
+include/kvq_fp8_block.h).
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libkvq.so.  PyTorch is used for device memory and streams.  There is no CPU
@@ -6,7 +7,10 @@ fallback -- if libkvq.so is missing, ``load()`` raises.
 
 Names follow the header: ``append`` (kvq_append), ``fp8_set_scales``
 (kvq_fp8_set_scales), ``decode_attn`` (kvq_decode_attn), ``dequant``
-(kvq_dequant), ``decode_workspace_bytes`` (kvq_decode_workspace_bytes).
+(kvq_dequant), ``decode_workspace_bytes`` (kvq_decode_workspace_bytes),
+``rope_append`` (kvq_rope_append).  ``append``, ``decode_attn``,
+``prefill_attn`` and ``dequant`` take an ``Fp8BlockCache`` as well and then call
+kvq_fp8_block_append, _decode_attn, _prefill_attn and _dequant.
 """
 from __future__ import annotations
 
@@ -24,10 +28,12 @@ LIB_PATH = os.path.join(_HERE, "libkvq.so")
 FORMAT_FP4 = 1
 FORMAT_FP8 = 2
 FORMAT_NVFP4 = 3
+FORMAT_FP8_BLOCK = 4
 FLAG_NONFINITE = 0x1
 FLAG_PAGE_OOB = 0x2
 FLAG_TIMEOUT = 0x4
 FLAG_BAD_LENGTH = 0x8
+FLAG_POSITION = 0x20
 LAYOUT_FP8_TENSOR = 1
 LAYOUT_INT_PER_TOKEN = 2
 LAYOUT_INT_PER_CHANNEL = 3
@@ -62,6 +68,7 @@ class KvqCacheStruct(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _CP = ctypes.POINTER(KvqCacheStruct)
+_I32, _I64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
 def load() -> ctypes.CDLL:
@@ -110,6 +117,24 @@ def load() -> ctypes.CDLL:
                                          _P, _P, _P, ctypes.c_size_t, _P]
             L.kvq_fp4_pool_bytes.restype = ctypes.c_size_t
             L.kvq_fp4_pool_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+            L.kvq_fp8_block_pool_bytes.restype = ctypes.c_size_t
+            L.kvq_fp8_block_pool_bytes.argtypes = [_I64, _I32, _I32, _I32]
+            L.kvq_rope_table.restype = ctypes.c_int
+            L.kvq_rope_table.argtypes = [_I64, _I32, ctypes.c_double, _P, _P]
+            L.kvq_rope_append.restype = ctypes.c_int
+            L.kvq_rope_append.argtypes = [_CP, _I32, _I32, _P, _P, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32,
+                                          _I32, _P, _P, _P, _P]
+            L.kvq_fp8_block_append.restype = ctypes.c_int
+            L.kvq_fp8_block_append.argtypes = [_CP, _I32, _I32, _P, _P, _P, _P, _P, _P]
+            L.kvq_fp8_block_dequant.restype = ctypes.c_int
+            L.kvq_fp8_block_dequant.argtypes = L.kvq_dequant.argtypes
+            L.kvq_fp8_block_decode_attn.restype = ctypes.c_int
+            L.kvq_fp8_block_decode_attn.argtypes = [_CP, _I32, _I32, _P, _P, _F, _P, _I32, _P, ctypes.c_size_t, _P, _P]
+            L.kvq_fp8_block_prefill_workspace_bytes.restype = ctypes.c_size_t
+            L.kvq_fp8_block_prefill_workspace_bytes.argtypes = [_I32] * 5
+            L.kvq_fp8_block_prefill_attn.restype = ctypes.c_int
+            L.kvq_fp8_block_prefill_attn.argtypes = [_CP, _I32, _I32, _I32, _P, _P, _P, _F, _P, _I32, _P,
+                                                     ctypes.c_size_t, _P, _P]
             _lib = L
     return _lib
 
@@ -222,18 +247,190 @@ class Fp8WindowCache:
 
 
 
+class Fp8BlockCache:
+    """8-bit paged cache for K and V: FP8 E4M3 codes, one fp32 scale per 16
+    positions of one kv head (K and V apart), head_dim 64 or 128.
+
+    pool  uint8 [num_pages][num_kv_heads][page_size / G][group bytes],
+          G = min(page_size, 64) (the byte layout is documented in
+          include/kvq_fp8_block.h); one given by the caller is used as it is.
+    page_table int32 [batch][max_pages_per_seq] or None (contiguous).
+    """
+
+    def __init__(self, num_kv_heads: int, head_dim: int, page_size: int, num_pages: int, max_pages_per_seq: int,
+                 page_table: Optional[torch.Tensor] = None, device="cuda", pool: Optional[torch.Tensor] = None):
+        self.num_kv_heads, self.head_dim, self.page_size = num_kv_heads, head_dim, page_size
+        self.num_pages, self.max_pages_per_seq = num_pages, max_pages_per_seq
+        self.group = min(page_size, 64)
+        nbytes = load().kvq_fp8_block_pool_bytes(num_pages, num_kv_heads, page_size, head_dim)
+        if nbytes == 0:
+            raise ValueError("invalid 8-bit cache geometry (head_dim 64/128, page_size 16..256)")
+        groups = num_pages * num_kv_heads * (page_size // self.group)
+        shape = (num_pages, num_kv_heads, page_size // self.group, nbytes // groups)
+        if pool is None:
+            pool = torch.zeros(shape, dtype=torch.uint8, device=device)
+        _need(pool, torch.uint8, "pool")
+        if tuple(pool.shape) != shape:
+            raise ValueError(f"pool must have shape {shape}")
+        if page_table is not None:
+            _need_table(page_table, max_pages_per_seq)
+        self.pool, self.page_table = pool, page_table
+
+    def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqCacheStruct:
+        """The kvq_cache description; a page_table argument overrides the
+        cache's own for one call."""
+        pt = self.page_table if page_table is None else page_table
+        return KvqCacheStruct(FORMAT_FP8_BLOCK, self.num_kv_heads, self.head_dim, self.page_size, self.num_pages,
+                              self.max_pages_per_seq, 0, _ptr(pt), _ptr(self.pool), None, None, None)
+
+    @property
+    def nbytes(self) -> int:
+        return self.pool.numel()
+
+
+def _need_table(t: torch.Tensor, max_pages: int) -> None:
+    _need(t, torch.int32, "page_table")
+    if t.dim() != 2 or t.shape[1] != max_pages:
+        raise ValueError("page_table must have shape [batch, max_pages_per_seq]")
+
+
+def _need_here(cache, **tensors) -> None:
+    """Every tensor given lives on the cache's device, which is the current one."""
+    dev = cache.pool.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+
+
+def _need_rows(batch: int, cache, page_table: Optional[torch.Tensor] = None, **per_seq) -> None:
+    """Per-sequence int32 tensors have `batch` entries, and so has the page table."""
+    for name, t in per_seq.items():
+        if t is None:
+            continue
+        _need(t, torch.int32, name)
+        if t.numel() != batch:
+            raise ValueError(f"{name} must hold one value per sequence ({batch})")
+    pt = cache.page_table if page_table is None else page_table
+    if pt is not None and pt.shape[0] < batch:
+        raise ValueError("the page table has fewer rows than sequences")
+
+
+def _need_err(err: Optional[torch.Tensor]) -> None:
+    if err is not None:
+        _need(err, torch.int32, "err")
+        if err.numel() < 1:
+            raise ValueError("err must hold one int32")
+
+
 def append(cache, start_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-           err: Optional[torch.Tensor] = None, stream=None, page_table: Optional[torch.Tensor] = None) -> None:
-    """kvq_append: k, v bf16 [batch][n_new][Hkv][head_dim]; start_pos int32 [batch]."""
+           err: Optional[torch.Tensor] = None, stream=None, page_table: Optional[torch.Tensor] = None,
+           new_lens: Optional[torch.Tensor] = None) -> None:
+    """kvq_append: k, v bf16 [batch][n_new][Hkv][head_dim]; start_pos int32 [batch].
+    An Fp8BlockCache (kvq_fp8_block_append) also takes new_lens, int32 [batch]:
+    sequence b has new_lens[b] <= n_new new tokens."""
     _need(k, torch.bfloat16, "k")
     _need(v, torch.bfloat16, "v")
     _need(start_pos, torch.int32, "start_pos")
     if k.dim() != 4 or k.shape != v.shape:
         raise ValueError("k and v must have shape [batch, n_new, num_kv_heads, head_dim]")
+    if isinstance(cache, Fp8BlockCache):
+        if tuple(k.shape[2:]) != (cache.num_kv_heads, cache.head_dim):
+            raise ValueError("k and v must have the cache's heads and head_dim")
+        if page_table is not None:
+            _need_table(page_table, cache.max_pages_per_seq)
+        _need_rows(k.shape[0], cache, page_table, start_pos=start_pos, new_lens=new_lens)
+        _need_err(err)
+        _need_here(cache, k=k, v=v, start_pos=start_pos, new_lens=new_lens, err=err, page_table=page_table)
+        s = cache.struct(page_table)
+        st = load().kvq_fp8_block_append(ctypes.byref(s), k.shape[0], k.shape[1], _ptr(start_pos), _ptr(new_lens),
+                                         _ptr(k), _ptr(v), _ptr(err), _stream(stream))
+        return _check(st, "kvq_fp8_block_append")
+    if new_lens is not None:
+        raise ValueError("new_lens needs an Fp8BlockCache (or rope_append)")
     s = cache.struct(page_table) if isinstance(cache, Fp4Cache) else cache.struct()
     st = load().kvq_append(ctypes.byref(s), k.shape[0], k.shape[1], _ptr(start_pos), _ptr(k), _ptr(v),
                            _ptr(err), _stream(stream))
     _check(st, "kvq_append")
+
+
+def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:
+    """kvq_rope_table: float32 [num_positions][rotary_dim], of each position
+    the rotary_dim/2 cosines, then the sines."""
+    table = torch.empty((num_positions, rotary_dim), dtype=torch.float32, device=device)
+    if table.device.index != torch.cuda.current_device():
+        raise ValueError(f"device {table.device} is not the current one")
+    _check(load().kvq_rope_table(num_positions, rotary_dim, float(base), _ptr(table), _stream(stream)),
+           "kvq_rope_table")
+    return table
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one token to the next of a bf16 [batch][n][heads][d] tensor
+    whose tokens' values are contiguous and evenly spaced (a contiguous tensor,
+    or a part of a packed projection)."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [batch, n_new, heads, head_dim]")
+    B, n, H, d = t.shape
+    sb, sn, sh, sd = t.stride()
+    step = sn if n > 1 else (sb if B > 1 else H * d)
+    even = (sd == 1 or d == 1) and (H == 1 or sh == d) and (n == 1 or B == 1 or sb == n * sn) and step >= H * d
+    if t.numel() and not even:
+        raise ValueError(f"{name}: the values of a token must be contiguous and the tokens evenly spaced")
+    return step
+
+
+def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                table: Optional[torch.Tensor], interleaved: bool = False, new_lens: Optional[torch.Tensor] = None,
+                q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                err: Optional[torch.Tensor] = None, stream=None,
+                page_table: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """kvq_rope_append: rotate q and k, bf16 [batch][n_new][heads][head_dim], by
+    their positions start_pos[b] + t and append k and v to an Fp4Cache (NVFP4
+    too) or Fp8BlockCache.  Returns the rotated queries (q_out, made when not
+    given; None without q); k_out, when given, receives the rotated keys.  q, k
+    and v may be parts of one packed projection.  table: rope_table(...), its
+    width the rotated channels; None: no rotation.  new_lens, int32 [batch]: the
+    new tokens of each sequence of a padded batch."""
+    if not isinstance(cache, (Fp4Cache, Fp8BlockCache)):
+        raise ValueError("rope_append needs an Fp4Cache or Fp8BlockCache (append k_out to a window ring)")
+    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
+    B, n = k.shape[:2]
+    if k.shape != v.shape or tuple(k.shape[2:]) != (cache.num_kv_heads, cache.head_dim):
+        raise ValueError("k and v must have shape [batch, n_new, num_kv_heads, head_dim]")
+    hq, qs = 0, 0
+    if q is not None:
+        qs, hq = _token_stride(q, "q"), q.shape[2]
+        if tuple(q.shape) != (B, n, hq, cache.head_dim):
+            raise ValueError("q must have shape [batch, n_new, num_q_heads, head_dim]")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        _need(k_out, torch.bfloat16, "k_out")
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+    rows = rd = 0
+    if table is not None:
+        _need(table, torch.float32, "table")
+        rows, rd = table.shape
+    if page_table is not None:
+        _need_table(page_table, cache.max_pages_per_seq)
+    _need_rows(B, cache, page_table, start_pos=start_pos, new_lens=new_lens)
+    _need_err(err)
+    _need_here(cache, q=q, k=k, v=v, table=table, start_pos=start_pos, new_lens=new_lens, q_out=q_out, k_out=k_out,
+               err=err, page_table=page_table)
+    s = cache.struct(page_table)
+    st = load().kvq_rope_append(ctypes.byref(s), B, n, _ptr(start_pos), _ptr(new_lens), hq, _ptr(q), qs, _ptr(k), ks,
+                                _ptr(v), vs, _ptr(table), rows, rd, int(bool(interleaved)), _ptr(q_out), _ptr(k_out),
+                                _ptr(err), _stream(stream))
+    _check(st, "kvq_rope_append")
+    return q_out
 
 
 def fp8_set_scales(cache, k: torch.Tensor, v: torch.Tensor,
@@ -259,9 +456,15 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
                 stream=None, kernel: str = "mma") -> torch.Tensor:
     """kvq_decode_attn: q bf16 [batch][Hq][head_dim] -> out float32 [batch][Hq][head_dim].
     kernel="tcgen05" calls kvq_decode_attn_tc instead (head_dim 128: both
-    products on the tensor-memory MMA; a measured, slower alternative)."""
+    products on the tensor-memory MMA; a measured, slower alternative).
+    An Fp8BlockCache (kvq_fp8_block_decode_attn) takes a float32 or bfloat16
+    out and neither swa nor kernel="tcgen05"."""
     if kernel not in ("mma", "tcgen05"):
         raise ValueError(f"unknown decode kernel {kernel!r}")
+    if isinstance(cache, Fp8BlockCache):
+        if swa is not None or kernel != "mma":
+            raise ValueError("an Fp8BlockCache takes neither swa nor kernel=\"tcgen05\"")
+        return _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, stream)
     _need(q, torch.bfloat16, "q")
     _need(seq_lens, torch.int32, "seq_lens")
     batch, hq, d = q.shape
@@ -280,6 +483,39 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
             float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
             _ptr(err), _stream(stream))
     _check(st, "kvq_decode_attn_tc" if kernel == "tcgen05" else "kvq_decode_attn")
+    return out
+
+
+_OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _attn_args(cache, q, out, softmax_scale):
+    _need(q, torch.bfloat16, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if out.dtype not in _OUT_DTYPES or not out.is_cuda or not out.is_contiguous() or out.shape != q.shape:
+        raise ValueError("out must be a contiguous float32 or bfloat16 CUDA tensor of q's shape")
+    if q.shape[-1] != cache.head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    return out, 1.0 / math.sqrt(cache.head_dim) if softmax_scale is None else float(softmax_scale)
+
+
+def _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, stream) -> torch.Tensor:
+    if q.dim() != 3:
+        raise ValueError("q must have shape [batch, num_q_heads, head_dim]")
+    out, scale = _attn_args(cache, q, out, softmax_scale)
+    B, hq, d = q.shape
+    _need_rows(B, cache, seq_lens=seq_lens)
+    _need_err(err)
+    if workspace is None:
+        workspace = torch.empty(max(16, decode_workspace_bytes(B, hq, cache.num_kv_heads, d)), dtype=torch.uint8,
+                                device=q.device)
+    _need_here(cache, seq_lens=seq_lens, q=q, out=out, workspace=workspace, err=err)
+    s = cache.struct()
+    st = load().kvq_fp8_block_decode_attn(ctypes.byref(s), B, hq, _ptr(seq_lens), _ptr(q), scale, _ptr(out),
+                                          _OUT_DTYPES[out.dtype], _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    _check(st, "kvq_fp8_block_decode_attn")
     return out
 
 
@@ -310,10 +546,46 @@ def append_decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, k_new: torch.Ten
     return out
 
 
-def prefill_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softmax_scale: Optional[float] = None,
-                 out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+def prefill_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, chunk: int) -> int:
+    """kvq_fp8_block_prefill_workspace_bytes."""
+    return int(load().kvq_fp8_block_prefill_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, chunk))
+
+
+def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace) -> torch.Tensor:
+    if q.dim() != 4:
+        raise ValueError("q must have shape [batch, chunk, num_q_heads, head_dim]")
+    if out is None and chunk_lens is not None:  # the padding's rows are not written
+        out = torch.zeros(q.shape, dtype=torch.float32, device=q.device)
+    out, scale = _attn_args(cache, q, out, softmax_scale)
+    B, chunk, hq, d = q.shape
+    _need_rows(B, cache, seq_lens=seq_lens, chunk_lens=chunk_lens)
+    _need_err(err)
+    if workspace is None:
+        workspace = torch.empty(max(16, prefill_workspace_bytes(B, hq, cache.num_kv_heads, d, chunk)),
+                                dtype=torch.uint8, device=q.device)
+    _need_here(cache, seq_lens=seq_lens, chunk_lens=chunk_lens, q=q, out=out, workspace=workspace, err=err)
+    s = cache.struct()
+    st = load().kvq_fp8_block_prefill_attn(ctypes.byref(s), B, hq, chunk, _ptr(seq_lens), _ptr(chunk_lens), _ptr(q),
+                                           scale, _ptr(out), _OUT_DTYPES[out.dtype], _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    _check(st, "kvq_fp8_block_prefill_attn")
+    return out
+
+
+def prefill_attn(cache, seq_lens: torch.Tensor, q: torch.Tensor, softmax_scale: Optional[float] = None,
+                 out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None,
+                 chunk_lens: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """kvq_prefill_attn: q bf16 [batch][chunk][Hq][head_dim] (their keys and
-    values already appended) -> out float32, same shape; causal over the cache."""
+    values already appended) -> out float32, same shape; causal over the cache.
+    An Fp8BlockCache (kvq_fp8_block_prefill_attn) takes a float32 or bfloat16
+    out, a workspace of prefill_workspace_bytes(...) bytes, and chunk_lens, int32
+    [batch]: the chunk's tokens of each sequence of a padded batch, whose other
+    rows of out are left as they were (0 in an out made here)."""
+    if isinstance(cache, Fp8BlockCache):
+        return _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace)
+    if chunk_lens is not None or workspace is not None:
+        raise ValueError("chunk_lens and workspace need an Fp8BlockCache")
     _need(q, torch.bfloat16, "q")
     _need(seq_lens, torch.int32, "seq_lens")
     batch, chunk, hq, d = q.shape
@@ -355,8 +627,14 @@ def swa_replay(w: torch.Tensor, emb: torch.Tensor, n_win: int, want_hidden: bool
 
 def dequant(cache, seq_lens: Optional[torch.Tensor], max_len: int, dtype: torch.dtype = torch.float32,
             err: Optional[torch.Tensor] = None, stream=None):
-    """kvq_dequant: dense K, V [batch][max_len][Hkv][head_dim] (FP8: max_len == window, slot order)."""
-    if isinstance(cache, Fp4Cache):
+    """kvq_dequant: dense K, V [batch][max_len][Hkv][head_dim] (FP8 ring: max_len
+    == window, slot order; Fp8BlockCache: kvq_fp8_block_dequant)."""
+    block8 = isinstance(cache, Fp8BlockCache)
+    if block8:
+        _need_rows(seq_lens.shape[0], cache, seq_lens=seq_lens)
+        _need_err(err)
+        _need_here(cache, seq_lens=seq_lens, err=err)
+    if isinstance(cache, (Fp4Cache, Fp8BlockCache)):
         batch = seq_lens.shape[0]
         s = cache.struct()
         device = cache.pool.device
@@ -368,9 +646,9 @@ def dequant(cache, seq_lens: Optional[torch.Tensor], max_len: int, dtype: torch.
     shape = (batch, max_len, cache.num_kv_heads, cache.head_dim)
     k = torch.empty(shape, dtype=dtype, device=device)
     v = torch.empty(shape, dtype=dtype, device=device)
-    st = load().kvq_dequant(ctypes.byref(s), batch, _ptr(seq_lens), max_len, code, _ptr(k), _ptr(v), _ptr(err),
-                            _stream(stream))
-    _check(st, "kvq_dequant")
+    fn = load().kvq_fp8_block_dequant if block8 else load().kvq_dequant
+    st = fn(ctypes.byref(s), batch, _ptr(seq_lens), max_len, code, _ptr(k), _ptr(v), _ptr(err), _stream(stream))
+    _check(st, "kvq_fp8_block_dequant" if block8 else "kvq_dequant")
     return k, v
 
 

@@ -114,11 +114,14 @@ typedef enum kvq_status {
                                    bounds-checked build of the library
                                    (-DKVQ_DEBUG_BOUNDS), which then skips the
                                    access */
+#define KVQ_FLAG_POSITION 0x20  /* a position past the rows of a rotation table (kvq_rope_append) */
 
 typedef enum kvq_format {
     KVQ_FORMAT_FP4_E2M1_E4M3_G16 = 1,
     KVQ_FORMAT_FP8_E4M3_HEAD = 2,
-    KVQ_FORMAT_NVFP4 = 3
+    KVQ_FORMAT_NVFP4 = 3,
+    KVQ_FORMAT_FP8_E4M3_BLOCK = 4 /* 8-bit paged cache: kvq_fp8_block.h, whose entry points
+                                     alone take it */
 } kvq_format;
 
 typedef struct kvq_stream_opaque *kvq_stream; /* a cudaStream_t */
