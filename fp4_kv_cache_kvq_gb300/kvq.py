@@ -74,6 +74,8 @@ _I32, _I64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 def load() -> ctypes.CDLL:
     """Load libkvq.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -155,8 +157,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a torch.cuda.Stream object around it
+# (0.3 us a call instead of 3).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -277,11 +286,11 @@ class Fp8BlockCache:
         self.pool, self.page_table = pool, page_table
 
     def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqCacheStruct:
-        """The kvq_cache description; a page_table argument overrides the
-        cache's own for one call."""
+        """The kvq_cache description of the cache as it is now; a page_table
+        argument overrides the cache's own for one call."""
         pt = self.page_table if page_table is None else page_table
         return KvqCacheStruct(FORMAT_FP8_BLOCK, self.num_kv_heads, self.head_dim, self.page_size, self.num_pages,
-                              self.max_pages_per_seq, 0, _ptr(pt), _ptr(self.pool), None, None, None)
+                              self.max_pages_per_seq, 0, _ptr(pt), self.pool.data_ptr(), None, None, None)
 
     @property
     def nbytes(self) -> int:
@@ -294,34 +303,47 @@ def _need_table(t: torch.Tensor, max_pages: int) -> None:
         raise ValueError("page_table must have shape [batch, max_pages_per_seq]")
 
 
-def _need_here(cache, **tensors) -> None:
-    """Every tensor given lives on the cache's device, which is the current one."""
-    dev = cache.pool.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+# Checks of the calls on an Fp8BlockCache and of rope_append: a few hundred
+# nanoseconds each, since a decode step makes them once a layer.
+def _device(cache) -> int:
+    """The cache's device, which has to be the current one."""
+    dev = cache.pool.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.pool.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _need_rows(batch: int, cache, page_table: Optional[torch.Tensor] = None, **per_seq) -> None:
-    """Per-sequence int32 tensors have `batch` entries, and so has the page table."""
-    for name, t in per_seq.items():
-        if t is None:
-            continue
-        _need(t, torch.int32, name)
-        if t.numel() != batch:
-            raise ValueError(f"{name} must hold one value per sequence ({batch})")
+def _on(dev: int, t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
+    """t is contiguous, of this type, on the cache's device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of dtype {dtype} on cuda:{dev}")
+
+
+def _per_seq(dev: int, t: torch.Tensor, batch: int, name: str) -> None:
+    _on(dev, t, torch.int32, name)
+    if t.numel() != batch:
+        raise ValueError(f"{name} must hold one value per sequence ({batch})")
+
+
+def _table_rows(dev: int, cache, page_table: Optional[torch.Tensor], batch: int) -> None:
+    """The page table of a call has a row for every sequence."""
+    if page_table is not None:
+        _on(dev, page_table, torch.int32, "page_table")
+        if page_table.dim() != 2 or page_table.shape[1] != cache.max_pages_per_seq:
+            raise ValueError("page_table must have shape [batch, max_pages_per_seq]")
     pt = cache.page_table if page_table is None else page_table
     if pt is not None and pt.shape[0] < batch:
         raise ValueError("the page table has fewer rows than sequences")
 
 
-def _need_err(err: Optional[torch.Tensor]) -> None:
-    if err is not None:
-        _need(err, torch.int32, "err")
-        if err.numel() < 1:
-            raise ValueError("err must hold one int32")
+def _err_ptr(dev: int, err: Optional[torch.Tensor]) -> Optional[int]:
+    if err is None:
+        return None
+    _on(dev, err, torch.int32, "err")
+    if err.numel() < 1:
+        raise ValueError("err must hold one int32")
+    return err.data_ptr()
 
 
 def append(cache, start_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -338,14 +360,17 @@ def append(cache, start_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if isinstance(cache, Fp8BlockCache):
         if tuple(k.shape[2:]) != (cache.num_kv_heads, cache.head_dim):
             raise ValueError("k and v must have the cache's heads and head_dim")
-        if page_table is not None:
-            _need_table(page_table, cache.max_pages_per_seq)
-        _need_rows(k.shape[0], cache, page_table, start_pos=start_pos, new_lens=new_lens)
-        _need_err(err)
-        _need_here(cache, k=k, v=v, start_pos=start_pos, new_lens=new_lens, err=err, page_table=page_table)
+        B = k.shape[0]
+        dev = _device(cache)
+        _on(dev, k, torch.bfloat16, "k")
+        _on(dev, v, torch.bfloat16, "v")
+        _table_rows(dev, cache, page_table, B)
+        _per_seq(dev, start_pos, B, "start_pos")
+        if new_lens is not None:
+            _per_seq(dev, new_lens, B, "new_lens")
         s = cache.struct(page_table)
-        st = load().kvq_fp8_block_append(ctypes.byref(s), k.shape[0], k.shape[1], _ptr(start_pos), _ptr(new_lens),
-                                         _ptr(k), _ptr(v), _ptr(err), _stream(stream))
+        st = load().kvq_fp8_block_append(ctypes.byref(s), B, k.shape[1], _ptr(start_pos), _ptr(new_lens), _ptr(k),
+                                         _ptr(v), _err_ptr(dev, err), _stream(stream))
         return _check(st, "kvq_fp8_block_append")
     if new_lens is not None:
         raise ValueError("new_lens needs an Fp8BlockCache (or rope_append)")
@@ -366,17 +391,19 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, devic
     return table
 
 
-def _token_stride(t: torch.Tensor, name: str) -> int:
+def _token_stride(dev: int, t: torch.Tensor, name: str) -> int:
     """Elements from one token to the next of a bf16 [batch][n][heads][d] tensor
     whose tokens' values are contiguous and evenly spaced (a contiguous tensor,
     or a part of a packed projection)."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [batch, n_new, heads, head_dim]")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.dim() != 4:
+        raise ValueError(f"{name} must be a bfloat16 tensor [batch, n_new, heads, head_dim] on cuda:{dev}")
     B, n, H, d = t.shape
+    if t.is_contiguous():
+        return H * d
     sb, sn, sh, sd = t.stride()
-    step = sn if n > 1 else (sb if B > 1 else H * d)
-    even = (sd == 1 or d == 1) and (H == 1 or sh == d) and (n == 1 or B == 1 or sb == n * sn) and step >= H * d
-    if t.numel() and not even:
+    step = sn if n > 1 else sb
+    if t.numel() and not ((sd == 1 or d == 1) and (H == 1 or sh == d) and step >= H * d and
+                          (n == 1 or B == 1 or sb == n * sn)):
         raise ValueError(f"{name}: the values of a token must be contiguous and the tokens evenly spaced")
     return step
 
@@ -395,40 +422,43 @@ def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: to
     new tokens of each sequence of a padded batch."""
     if not isinstance(cache, (Fp4Cache, Fp8BlockCache)):
         raise ValueError("rope_append needs an Fp4Cache or Fp8BlockCache (append k_out to a window ring)")
-    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
-    B, n = k.shape[:2]
-    if k.shape != v.shape or tuple(k.shape[2:]) != (cache.num_kv_heads, cache.head_dim):
+    dev = _device(cache)
+    ks, vs = _token_stride(dev, k, "k"), _token_stride(dev, v, "v")
+    shape = k.shape
+    B, n, hkv, d = shape
+    if shape != v.shape or hkv != cache.num_kv_heads or d != cache.head_dim:
         raise ValueError("k and v must have shape [batch, n_new, num_kv_heads, head_dim]")
-    hq, qs = 0, 0
+    hq = qs = 0
+    q_ptr = out_ptr = None
     if q is not None:
-        qs, hq = _token_stride(q, "q"), q.shape[2]
-        if tuple(q.shape) != (B, n, hq, cache.head_dim):
+        qs, hq = _token_stride(dev, q, "q"), q.shape[2]
+        if q.shape != (B, n, hq, d):
             raise ValueError("q must have shape [batch, n_new, num_q_heads, head_dim]")
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _need(q_out, torch.bfloat16, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+        else:
+            _on(dev, q_out, torch.bfloat16, "q_out")
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
-        _need(k_out, torch.bfloat16, "k_out")
-        if k_out.shape != k.shape:
+        _on(dev, k_out, torch.bfloat16, "k_out")
+        if k_out.shape != shape:
             raise ValueError("k_out must have k's shape")
     rows = rd = 0
     if table is not None:
-        _need(table, torch.float32, "table")
+        _on(dev, table, torch.float32, "table")
         rows, rd = table.shape
-    if page_table is not None:
-        _need_table(page_table, cache.max_pages_per_seq)
-    _need_rows(B, cache, page_table, start_pos=start_pos, new_lens=new_lens)
-    _need_err(err)
-    _need_here(cache, q=q, k=k, v=v, table=table, start_pos=start_pos, new_lens=new_lens, q_out=q_out, k_out=k_out,
-               err=err, page_table=page_table)
+    _table_rows(dev, cache, page_table, B)
+    _per_seq(dev, start_pos, B, "start_pos")
+    if new_lens is not None:
+        _per_seq(dev, new_lens, B, "new_lens")
     s = cache.struct(page_table)
-    st = load().kvq_rope_append(ctypes.byref(s), B, n, _ptr(start_pos), _ptr(new_lens), hq, _ptr(q), qs, _ptr(k), ks,
-                                _ptr(v), vs, _ptr(table), rows, rd, int(bool(interleaved)), _ptr(q_out), _ptr(k_out),
-                                _ptr(err), _stream(stream))
+    st = load().kvq_rope_append(ctypes.byref(s), B, n, start_pos.data_ptr(), _ptr(new_lens), hq, q_ptr, qs,
+                                k.data_ptr(), ks, v.data_ptr(), vs, _ptr(table), rows, rd, 1 if interleaved else 0,
+                                out_ptr, _ptr(k_out), _err_ptr(dev, err), _stream(stream))
     _check(st, "kvq_rope_append")
     return q_out
 
@@ -489,32 +519,41 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
 _OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _attn_args(cache, q, out, softmax_scale):
-    _need(q, torch.bfloat16, "q")
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    if out.dtype not in _OUT_DTYPES or not out.is_cuda or not out.is_contiguous() or out.shape != q.shape:
-        raise ValueError("out must be a contiguous float32 or bfloat16 CUDA tensor of q's shape")
+def _attn_out(dev: int, cache, q: torch.Tensor, out: Optional[torch.Tensor], padded: bool):
+    """(out, its KVQ_DTYPE_*) of an attention over an Fp8BlockCache."""
+    _on(dev, q, torch.bfloat16, "q")
     if q.shape[-1] != cache.head_dim:
         raise ValueError("q must have the cache's head_dim")
-    return out, 1.0 / math.sqrt(cache.head_dim) if softmax_scale is None else float(softmax_scale)
+    if out is None:  # rows of a padded batch's padding are not written
+        out = (torch.zeros if padded else torch.empty)(q.shape, dtype=torch.float32, device=q.device)
+    code = _OUT_DTYPES.get(out.dtype)
+    if code is None or out.get_device() != dev or not out.is_contiguous() or out.shape != q.shape:
+        raise ValueError("out must be a contiguous float32 or bfloat16 tensor of q's shape on the cache's device")
+    return out, code
+
+
+def _workspace(dev: int, workspace: Optional[torch.Tensor], need, *sizes) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(16, need(*sizes)), dtype=torch.uint8, device=f"cuda:{dev}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace  # its size is checked by the library
 
 
 def _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, stream) -> torch.Tensor:
+    dev = _device(cache)
     if q.dim() != 3:
         raise ValueError("q must have shape [batch, num_q_heads, head_dim]")
-    out, scale = _attn_args(cache, q, out, softmax_scale)
+    out, code = _attn_out(dev, cache, q, out, False)
     B, hq, d = q.shape
-    _need_rows(B, cache, seq_lens=seq_lens)
-    _need_err(err)
-    if workspace is None:
-        workspace = torch.empty(max(16, decode_workspace_bytes(B, hq, cache.num_kv_heads, d)), dtype=torch.uint8,
-                                device=q.device)
-    _need_here(cache, seq_lens=seq_lens, q=q, out=out, workspace=workspace, err=err)
+    _per_seq(dev, seq_lens, B, "seq_lens")
+    _table_rows(dev, cache, None, B)
+    ws = _workspace(dev, workspace, decode_workspace_bytes, B, hq, cache.num_kv_heads, d)
     s = cache.struct()
-    st = load().kvq_fp8_block_decode_attn(ctypes.byref(s), B, hq, _ptr(seq_lens), _ptr(q), scale, _ptr(out),
-                                          _OUT_DTYPES[out.dtype], _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    st = load().kvq_fp8_block_decode_attn(ctypes.byref(s), B, hq, seq_lens.data_ptr(), q.data_ptr(),
+                                          1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
+                                          out.data_ptr(), code, ws.data_ptr(), ws.nbytes, _err_ptr(dev, err),
+                                          _stream(stream))
     _check(st, "kvq_fp8_block_decode_attn")
     return out
 
@@ -552,22 +591,22 @@ def prefill_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, hea
 
 
 def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace) -> torch.Tensor:
+    dev = _device(cache)
     if q.dim() != 4:
         raise ValueError("q must have shape [batch, chunk, num_q_heads, head_dim]")
-    if out is None and chunk_lens is not None:  # the padding's rows are not written
-        out = torch.zeros(q.shape, dtype=torch.float32, device=q.device)
-    out, scale = _attn_args(cache, q, out, softmax_scale)
+    out, code = _attn_out(dev, cache, q, out, chunk_lens is not None)
     B, chunk, hq, d = q.shape
-    _need_rows(B, cache, seq_lens=seq_lens, chunk_lens=chunk_lens)
-    _need_err(err)
-    if workspace is None:
-        workspace = torch.empty(max(16, prefill_workspace_bytes(B, hq, cache.num_kv_heads, d, chunk)),
-                                dtype=torch.uint8, device=q.device)
-    _need_here(cache, seq_lens=seq_lens, chunk_lens=chunk_lens, q=q, out=out, workspace=workspace, err=err)
+    _per_seq(dev, seq_lens, B, "seq_lens")
+    if chunk_lens is not None:
+        _per_seq(dev, chunk_lens, B, "chunk_lens")
+    _table_rows(dev, cache, None, B)
+    ws = _workspace(dev, workspace, prefill_workspace_bytes, B, hq, cache.num_kv_heads, d, chunk)
     s = cache.struct()
-    st = load().kvq_fp8_block_prefill_attn(ctypes.byref(s), B, hq, chunk, _ptr(seq_lens), _ptr(chunk_lens), _ptr(q),
-                                           scale, _ptr(out), _OUT_DTYPES[out.dtype], _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    st = load().kvq_fp8_block_prefill_attn(ctypes.byref(s), B, hq, chunk, seq_lens.data_ptr(), _ptr(chunk_lens),
+                                           q.data_ptr(),
+                                           1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
+                                           out.data_ptr(), code, ws.data_ptr(), ws.nbytes, _err_ptr(dev, err),
+                                           _stream(stream))
     _check(st, "kvq_fp8_block_prefill_attn")
     return out
 
@@ -631,9 +670,10 @@ def dequant(cache, seq_lens: Optional[torch.Tensor], max_len: int, dtype: torch.
     == window, slot order; Fp8BlockCache: kvq_fp8_block_dequant)."""
     block8 = isinstance(cache, Fp8BlockCache)
     if block8:
-        _need_rows(seq_lens.shape[0], cache, seq_lens=seq_lens)
-        _need_err(err)
-        _need_here(cache, seq_lens=seq_lens, err=err)
+        dev = _device(cache)
+        _per_seq(dev, seq_lens, seq_lens.numel(), "seq_lens")
+        _table_rows(dev, cache, None, seq_lens.numel())
+        _err_ptr(dev, err)
     if isinstance(cache, (Fp4Cache, Fp8BlockCache)):
         batch = seq_lens.shape[0]
         s = cache.struct()
