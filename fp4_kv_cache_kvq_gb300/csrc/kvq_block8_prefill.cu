@@ -45,7 +45,12 @@ constexpr int kSmWarps = 4 * kXTiles;
 constexpr int kExpWarps = 4;
 constexpr int kLdWarp = kSmWarps + kExpWarps;
 constexpr int kMWarp = kLdWarp + 1;
-constexpr int kP8Threads = 32 * (kMWarp + 1);
+// four warpgroups, so that registers can move between them: the loader's and
+// the MMA issuer's group (two of its warps idle) and the expansion leave theirs
+// to the softmax, which holds a row's 128 scores at once
+constexpr int kP8Threads = 512;
+constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192 + 72 + 56 = 4 x 128
+static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * 128, "registers of the launch");
 constexpr int kOCol8 = kXTiles * kT;  // TMEM: S_X (then P_X) at [128 X, +128), O_X at [256 + 128 X, +d)
 constexpr int kTmem8 = 512;
 constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
@@ -155,23 +160,40 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t base, int i) {
   return base + (GT == 16 ? 16 * i : 8 * i);
 }
 
-// The largest |score * csk| of 16 scores of a block, masked from lim on.
-template <bool FAST>
-__device__ __forceinline__ float block_max(const uint32_t* v, int c0, int lim, float csk, float m) {
-  float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (FAST || c0 + 2 * i < lim) a = fmaxf(a, __uint_as_float(v[2 * i]));
-    if (FAST || c0 + 2 * i + 1 < lim) b = fmaxf(b, __uint_as_float(v[2 * i + 1]));
-  }
-  a = fmaxf(a, b);
-  if (FAST) return fmaxf(m, a * csk);
-  return a == -INFINITY ? m : fmaxf(m, a * csk);
+// 16 columns of this warp's TMEM lanes and their maximum, without the wait.
+__device__ __forceinline__ void tmem_ld_max16_async(uint32_t taddr, uint32_t (&v)[16], uint32_t& m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, "
+      "[%17];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(m)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_all() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// keeps the uses of v and m behind the wait
+__device__ __forceinline__ void after_wait(uint32_t (&v)[16], uint32_t& m) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(m)
+               :
+               : "memory");
 }
 
-// P = 2^(S csk - m) for 16 scores as 8 f16 pairs, their sum into l2.
-template <bool FAST>
-__device__ __forceinline__ void block_p(const uint32_t* v, uint32_t* w, int c0, int lim, float csk, uint64_t nref2,
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// P = 2^(S csk - m) for the 16 scores of a block as 8 f16 pairs, their sum
+// into l2; MASK: scores from `left` on give 0.
+template <bool MASK>
+__device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, int left, float csk, uint64_t nref2,
                                         uint64_t (&l2)[2]) {
   const uint64_t cs2 = pk2(csk, csk);
 #pragma unroll
@@ -179,9 +201,9 @@ __device__ __forceinline__ void block_p(const uint32_t* v, uint32_t* w, int c0, 
     float y0, y1;
     upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cs2, nref2), y0, y1);
     float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
-    if (!FAST) {
-      if (c0 + 2 * i >= lim) e0 = 0.0f;
-      if (c0 + 2 * i + 1 >= lim) e1 = 0.0f;
+    if (MASK) {
+      if (2 * i >= left) e0 = 0.0f;
+      if (2 * i + 1 >= left) e1 = 0.0f;
     }
     l2[i & 1] = add2(l2[i & 1], pk2(e0, e1));
     w[i] = pack_f16x2(e0, e1);
@@ -273,7 +295,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     }
     for (int i = 0; i < kXTiles; ++i) {
       mbar_init(bars + 8 * (kSFull + i), 1);
-      mbar_init(bars + 8 * (kPFull + i), 32 * 4);
+      mbar_init(bars + 8 * (kPFull + i), 4);
       mbar_init(bars + 8 * (kPvDone + i), 1);
     }
     *abort = 0;
@@ -357,6 +379,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 
   if (warp < kSmWarps) {
     // ---------------------------------------------------------------- softmax
+    reg_inc<kRegsSoftmax>();
     if (X < nx) {
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t sp_col = t_lane + (uint32_t)(X * kT);
@@ -367,12 +390,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       float m_run = -INFINITY, l_run = 0.0f;
       bool ok = true;
       for (int j = 0; j < ntiles; ++j) {
+        // the tile's K scales, ahead of its scores
         const int ks = j % kKRing;
-        if (!(ok = wwait8(s_full, (uint32_t)j & 1u, abort))) break;
-        // the tile's K scales (landed before S could be formed; this wait makes
-        // the copy visible to this thread)
         if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kKRing) & 1u, abort))) break;
-        tc_fence_after();
         float csk[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -383,101 +403,71 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
         const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
-        // the tile in two halves of 64 scores, each read from TMEM once: the
-        // maximum against the lazy reference, then P over the same registers.
-        // A raise of the reference shrinks what was accumulated against the
-        // old one: l, O and, in the second half, the first half's P.
+        if (!(ok = wwait8(s_full, (uint32_t)j & 1u, abort))) break;
+        tc_fence_after();
+        // the row's 128 scores in registers, each block's maximum with them
+        uint32_t v[8][16], vm[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tmem_ld_max16_async(sp_col + (uint32_t)(16 * i), v[i], vm[i]);
+        tmem_wait_ld_all();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) after_wait(v[i], vm[i]);
+        float mt = -INFINITY;
+        if (fast) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mt = fmaxf(mt, __uint_as_float(vm[i]) * csk[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int left = ((good >> i) & 1u) ? lim - 16 * i : 0;
+            float a = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (c < left) a = fmaxf(a, __uint_as_float(v[i][c]));
+            if (left > 0) mt = fmaxf(mt, a * csk[i]);
+          }
+        }
+        // lazy reference: raised only past +8; O and l shrink then
+        float al = 1.0f;
+        if (mt > m_run + kSlack8) {
+          if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
+          m_run = mt;
+        }
+        if (j > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
+          if (!(ok = wwait8(pv_done, (uint32_t)(j - 1) & 1u, abort))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(op + (uint32_t)c0, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st16_async(op + (uint32_t)c0, o);
+          }
+        }
+        const float nref = m_run == -INFINITY ? 0.0f : -m_run;
+        const uint64_t nref2 = pk2(nref, nref);
         uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t va[32], vb[32];
-          tmem_ld32_async(sp_col + (uint32_t)(64 * hf), va);
-          tmem_ld32_async(sp_col + (uint32_t)(64 * hf + 32), vb);
-          tmem_wait_ld(va);
-          tmem_wait_ld(vb);
-          float mt = -INFINITY;
-          int lb[4];  // masked from here on, per block
-#pragma unroll
-          for (int i = 0; i < 4; ++i) lb[i] = ((good >> (4 * hf + i)) & 1u) ? lim : 0;
-          if (fast) {
-            mt = block_max<true>(va, 0, 0, csk[4 * hf], mt);
-            mt = block_max<true>(va + 16, 0, 0, csk[4 * hf + 1], mt);
-            mt = block_max<true>(vb, 0, 0, csk[4 * hf + 2], mt);
-            mt = block_max<true>(vb + 16, 0, 0, csk[4 * hf + 3], mt);
-          } else {
-            mt = block_max<false>(va, 64 * hf, lb[0], csk[4 * hf], mt);
-            mt = block_max<false>(va + 16, 64 * hf + 16, lb[1], csk[4 * hf + 1], mt);
-            mt = block_max<false>(vb, 64 * hf + 32, lb[2], csk[4 * hf + 2], mt);
-            mt = block_max<false>(vb + 16, 64 * hf + 48, lb[3], csk[4 * hf + 3], mt);
-          }
-          float al = 1.0f;
-          if (mt > m_run + kSlack8) {
-            if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
-            m_run = mt;
-          }
-          if (__any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
-            if (hf == 1) {
-              const uint32_t al2 = pack_f16x2(al, al);
-              tmem_wait_st();
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint32_t pw[16];
-                tmem_ld16(sp_col + (uint32_t)(16 * k), pw);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pw[i] = hmul2_u32(pw[i], al2);
-                tmem_st16_async(sp_col + (uint32_t)(16 * k), pw);
-              }
-            }
-            {
-              float a0, a1, b0, b1;
-              upk2(l2[0], a0, a1);
-              upk2(l2[1], b0, b1);
-              l2[0] = pk2(a0 * al, a1 * al);
-              l2[1] = pk2(b0 * al, b1 * al);
-            }
-            if (j > 0) {  // O: once O_X += P_X V^ of the previous tile is done
-              if (!(ok = wwait8(pv_done, (uint32_t)(j - 1) & 1u, abort))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16(op + (uint32_t)c0, o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                tmem_st16_async(op + (uint32_t)c0, o);
-              }
-            }
-          }
-          l_run *= al;
-          const float nref = m_run == -INFINITY ? 0.0f : -m_run;
-          const uint64_t nref2 = pk2(nref, nref);
+        for (int i = 0; i < 8; i += 2) {
           uint32_t w[16];
           if (fast) {
-            block_p<true>(va, w, 0, 0, csk[4 * hf], nref2, l2);
-            block_p<true>(va + 16, w + 8, 0, 0, csk[4 * hf + 1], nref2, l2);
-            tmem_st16_async(sp_col + (uint32_t)(32 * hf), w);
-            block_p<true>(vb, w, 0, 0, csk[4 * hf + 2], nref2, l2);
-            block_p<true>(vb + 16, w + 8, 0, 0, csk[4 * hf + 3], nref2, l2);
-            tmem_st16_async(sp_col + (uint32_t)(32 * hf + 16), w);
+            block_p<false>(v[i], w, 0, csk[i], nref2, l2);
+            block_p<false>(v[i + 1], w + 8, 0, csk[i + 1], nref2, l2);
           } else {
-            block_p<false>(va, w, 64 * hf, lb[0], csk[4 * hf], nref2, l2);
-            block_p<false>(va + 16, w + 8, 64 * hf + 16, lb[1], csk[4 * hf + 1], nref2, l2);
-            tmem_st16_async(sp_col + (uint32_t)(32 * hf), w);
-            block_p<false>(vb, w, 64 * hf + 32, lb[2], csk[4 * hf + 2], nref2, l2);
-            block_p<false>(vb + 16, w + 8, 64 * hf + 48, lb[3], csk[4 * hf + 3], nref2, l2);
-            tmem_st16_async(sp_col + (uint32_t)(32 * hf + 16), w);
+            block_p<true>(v[i], w, ((good >> i) & 1u) ? lim - 16 * i : 0, csk[i], nref2, l2);
+            block_p<true>(v[i + 1], w + 8, ((good >> (i + 1)) & 1u) ? lim - 16 * i - 16 : 0, csk[i + 1], nref2, l2);
           }
+          tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
-        if (!ok) break;
         tmem_wait_st();
-        {
-          float a0, a1, b0, b1;
-          upk2(l2[0], a0, a1);
-          upk2(l2[1], b0, b1);
-          l_run += (a0 + a1) + (b0 + b1);
-        }
         tc_fence_before();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        float a0, a1, b0, b1;
+        upk2(l2[0], a0, a1);
+        upk2(l2[1], b0, b1);
+        l_run = l_run * al + ((a0 + a1) + (b0 + b1));
       }
       // the result once the last O_X += P_X V^ is done
       if (ok) ok = wwait8(pv_done, (uint32_t)(ntiles - 1) & 1u, abort);
@@ -517,6 +507,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // item (channel c, 16-position block): one 16-byte row of codes to two
     // 16-byte rows of f16; lanes take consecutive channels, so loads and
     // stores touch 128 contiguous bytes per eight lanes
+    reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
     const float vinv = vref > 0.0f ? 1.0f / vref : 0.0f;
     for (int j = 0; j < ntiles; ++j) {
@@ -557,7 +548,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       fence_async_smem();
       mbar_arrive(bars + 8 * (kVFull + slot));
     }
-  } else if (warp == kLdWarp) {
+  } else {
+   reg_dec<kRegsIssue>();
+   if (warp == kLdWarp) {
     // ------------------------------------------------------------ bulk copies
     // lane i < kGroups copies group i of each tile: K codes and scales, then V
     // codes and scales
@@ -617,7 +610,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       drain(kKFull, kKRing, kiss);
       drain(kV8Full, kVRing, viss);
     }
-  } else if (lane == 0) {
+   } else if (warp == kMWarp && lane == 0) {
     // ----------------------------------------------------------- tensor cores
     constexpr uint32_t kIdS = idesc_f16_f32(kRows, kT);  // E4M3 is type 0 of kind::f8f6f4, as f16 is of kind::f16
     constexpr uint32_t kIdO = idesc_f16_f32(kRows, D);
@@ -671,6 +664,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       while (!mbar_try_wait_hint(last_bar, last_par, kPoll8) && global_ns() - t0 < 20000000ull) {
       }
     }
+   }
   }
   tc_fence_before();
   __syncthreads();
