@@ -191,23 +191,25 @@ __device__ __forceinline__ void reg_inc() {
 }
 
 // P = 2^(S csk - m) for the 16 scores of a block as 8 f16 pairs, their sum
-// into l2; MASK: scores from `left` on give 0.
-template <bool MASK>
-__device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, int left, float csk, uint64_t nref2,
+// into l2.
+__device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, float csk, uint64_t nref2,
                                         uint64_t (&l2)[2]) {
   const uint64_t cs2 = pk2(csk, csk);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float y0, y1;
     upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cs2, nref2), y0, y1);
-    float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
-    if (MASK) {
-      if (2 * i >= left) e0 = 0.0f;
-      if (2 * i + 1 >= left) e1 = 0.0f;
-    }
+    const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
     l2[i & 1] = add2(l2[i & 1], pk2(e0, e1));
     w[i] = pack_f16x2(e0, e1);
   }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 template <int D, int GT>
@@ -412,21 +414,26 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         tmem_wait_ld_all();
 #pragma unroll
         for (int i = 0; i < 8; ++i) after_wait(v[i], vm[i]);
-        float mt = -INFINITY;
-        if (fast) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mt = fmaxf(mt, __uint_as_float(vm[i]) * csk[i]);
-        } else {
+        if (!fast) {
+          // masked scores (behind the row's last position, or in a page that is
+          // not valid) become -inf, their factor positive: 2^-inf is 0
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int left = ((good >> i) & 1u) ? lim - 16 * i : 0;
             float a = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c < left) a = fmaxf(a, __uint_as_float(v[i][c]));
-            if (left > 0) mt = fmaxf(mt, a * csk[i]);
+            for (int c = 0; c < 16; ++c) {
+              v[i][c] = c < left ? v[i][c] : 0xFF800000u;
+              a = fmaxf(a, __uint_as_float(v[i][c]));
+            }
+            vm[i] = __float_as_uint(a);
+            if (left < 16) csk[i] = left > 0 ? fmaxf(csk[i], 1e-37f) : 1.0f;
+            if (cs != cs) csk[i] = cs;
           }
         }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mt = fmaxf(mt, __uint_as_float(vm[i]) * csk[i]);
         // lazy reference: raised only past +8; O and l shrink then
         float al = 1.0f;
         if (mt > m_run + kSlack8) {
@@ -451,13 +458,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           uint32_t w[16];
-          if (fast) {
-            block_p<false>(v[i], w, 0, csk[i], nref2, l2);
-            block_p<false>(v[i + 1], w + 8, 0, csk[i + 1], nref2, l2);
-          } else {
-            block_p<true>(v[i], w, ((good >> i) & 1u) ? lim - 16 * i : 0, csk[i], nref2, l2);
-            block_p<true>(v[i + 1], w + 8, ((good >> (i + 1)) & 1u) ? lim - 16 * i - 16 : 0, csk[i + 1], nref2, l2);
-          }
+          block_p(v[i], w, csk[i], nref2, l2);
+          block_p(v[i + 1], w + 8, csk[i + 1], nref2, l2);
           tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
         tmem_wait_st();
@@ -610,53 +612,74 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       drain(kKFull, kKRing, kiss);
       drain(kV8Full, kVRing, viss);
     }
-   } else if (warp == kMWarp && lane == 0) {
+   } else if (warp == kMWarp) {
     // ----------------------------------------------------------- tensor cores
+    // The whole warp walks the tiles, so that descriptors and addresses stay in
+    // uniform registers; one elected lane issues.
     constexpr uint32_t kIdS = idesc_f16_f32(kRows, kT);  // E4M3 is type 0 of kind::f8f6f4, as f16 is of kind::f16
     constexpr uint32_t kIdO = idesc_f16_f32(kRows, D);
+    const uint64_t dq0 = smem_desc(sb + G::kQ, 128, 8 * D);
+    const uint64_t dk0 = smem_desc(sb + G::kK, 128, 8 * D);
+    const uint64_t dv0 = smem_desc(sb + G::kV, (D / 8) * 128, 128);
     uint32_t last_bar = 0, last_par = 0;
-    const auto issue_s = [&](int j, int x) {
-      const uint64_t dk = smem_desc(sb + G::kK + (j % kKRing) * kT * D, 128, 8 * D);
+    const auto issue_s = [&](int ring, int x) {
+      const uint64_t dq = dq0 + (uint64_t)(x * (2 * G::kQBytes / 16));
+      const uint64_t dk = dk0 + (uint64_t)(ring * (kT * D / 16));
+      const uint32_t d = tmem + (uint32_t)(x * kT);
+      if (elect_one()) {
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint64_t dq = smem_desc(sb + G::kQ + (2 * x + part) * G::kQBytes, 128, 8 * D);
+        for (int s = 0; s < D / 32; ++s) tc_mma_f8(d, dq + (uint64_t)(16 * s), dk + (uint64_t)(16 * s), kIdS, s > 0);
 #pragma unroll
         for (int s = 0; s < D / 32; ++s)
-          tc_mma_f8(tmem + (uint32_t)(x * kT), dq + (uint64_t)(16 * s), dk + (uint64_t)(16 * s), kIdS, part + s > 0);
+          tc_mma_f8(d, dq + (uint64_t)(G::kQBytes / 16 + 16 * s), dk + (uint64_t)(16 * s), kIdS, true);
+        tc_commit(bars + 8 * (kSFull + x));
+        if (x == nx - 1) tc_commit(bars + 8 * (kKEmpty + ring));
       }
-      tc_commit(bars + 8 * (kSFull + x));
-      last_bar = bars + 8 * (kSFull + x);
-      last_par = (uint32_t)j & 1u;
+      __syncwarp();
     };
-    bool ok = pwait8(bars + 8 * kKFull, 0u, abort);
+    bool ok = wwait8(bars + 8 * kKFull, 0u, abort);
     if (ok) {
       tc_fence_after();
       for (int x = 0; x < nx; ++x) issue_s(0, x);
-      tc_commit(bars + 8 * kKEmpty);
+      last_bar = bars + 8 * (kSFull + nx - 1);
     }
+    int kr = 0, vslot = 0;               // rings' positions
+    uint32_t kpar = 0, vpar = 0;         // and their phases
     for (int j = 0; j < ntiles && ok; ++j) {
-      if (!(ok = pwait8(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
-      const uint64_t dv = smem_desc(sb + G::kV + (j % kVSlots8) * kT * D * 2, (D / 8) * 128, 128);
+      if (!(ok = wwait8(bars + 8 * (kVFull + vslot), vpar, abort))) break;
+      const uint64_t dv = dv0 + (uint64_t)(vslot * (kT * D * 2 / 16));
+      const bool more = j + 1 < ntiles;
+      if (++kr == kKRing) {
+        kr = 0;
+        kpar ^= 1u;
+      }
       for (int x = 0; x < nx; ++x) {
-        if (!(ok = pwait8(bars + 8 * (kPFull + x), (uint32_t)j & 1u, abort))) break;
+        if (!(ok = wwait8(bars + 8 * (kPFull + x), (uint32_t)j & 1u, abort))) break;
         tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(kOCol8 + x * kT), a = tmem + (uint32_t)(x * kT);
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < kT / 16; ++s)
-          tc_mma_f16_ta(tmem + (uint32_t)(kOCol8 + x * kT), tmem + (uint32_t)(x * kT + s * 8),
-                        dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, j > 0 || s > 0);
-        tc_commit(bars + 8 * (kPvDone + x));
+          for (int s = 0; s < kT / 16; ++s)
+            tc_mma_f16_ta(d, a + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, j > 0 || s > 0);
+          tc_commit(bars + 8 * (kPvDone + x));
+          if (x == nx - 1) tc_commit(bars + 8 * (kVEmpty + vslot));
+        }
+        __syncwarp();
         last_bar = bars + 8 * (kPvDone + x);
         last_par = (uint32_t)j & 1u;
-        if (x == nx - 1) tc_commit(bars + 8 * (kVEmpty + j % kVSlots8));
-        if (j + 1 < ntiles) {
-          const int jn = j + 1;
-          if (x == 0 && !(ok = pwait8(bars + 8 * (kKFull + jn % kKRing), (uint32_t)(jn / kKRing) & 1u, abort))) break;
+        if (more) {
+          if (x == 0 && !(ok = wwait8(bars + 8 * (kKFull + kr), kpar, abort))) break;
           // P_X lives in S_X's columns: the next scores follow the product that reads it
-          if (!(ok = pwait8(bars + 8 * (kPvDone + x), (uint32_t)j & 1u, abort))) break;
+          if (!(ok = wwait8(bars + 8 * (kPvDone + x), (uint32_t)j & 1u, abort))) break;
           tc_fence_after();
-          issue_s(jn, x);
-          if (x == nx - 1) tc_commit(bars + 8 * (kKEmpty + jn % kKRing));
+          issue_s(kr, x);
+          last_bar = bars + 8 * (kSFull + x);
+          last_par = (uint32_t)(j + 1) & 1u;
         }
+      }
+      if (++vslot == kVSlots8) {
+        vslot = 0;
+        vpar ^= 1u;
       }
     }
     if (*abort && last_bar != 0) {  // MMAs still running when the CTA gave up
