@@ -68,7 +68,8 @@ enum : int {
   kSFull = kVEmpty + kVSlots8,     // [kXTiles] S_X in TMEM
   kPFull = kSFull + kXTiles,       // [kXTiles] P_X in TMEM, O_X rescaled
   kPvDone = kPFull + kXTiles,      // [kXTiles] O_X += P_X V^ done
-  kBars8 = kPvDone + kXTiles
+  kTurn = kPvDone + kXTiles,       // [kXTiles] query tile X's products may be issued
+  kBars8 = kTurn + kXTiles
 };
 
 struct Prefill8Params {
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   if (tid == 0) {
     for (int i = 0; i < kKRing; ++i) {
       mbar_init(bars + 8 * (kKFull + i), 1);
-      mbar_init(bars + 8 * (kKEmpty + i), 1 + 4 * nx);
+      mbar_init(bars + 8 * (kKEmpty + i), 5 * nx);
     }
     for (int i = 0; i < kVRing; ++i) {
       mbar_init(bars + 8 * (kV8Full + i), 1);
@@ -293,12 +294,13 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     }
     for (int i = 0; i < kVSlots8; ++i) {
       mbar_init(bars + 8 * (kVFull + i), 32 * kExpWarps);
-      mbar_init(bars + 8 * (kVEmpty + i), 1);
+      mbar_init(bars + 8 * (kVEmpty + i), nx);
     }
     for (int i = 0; i < kXTiles; ++i) {
       mbar_init(bars + 8 * (kSFull + i), 1);
       mbar_init(bars + 8 * (kPFull + i), 4);
       mbar_init(bars + 8 * (kPvDone + i), 1);
+      mbar_init(bars + 8 * (kTurn + i), 1);
     }
     *abort = 0;
     *vref_bits = 0u;
@@ -612,71 +614,78 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       drain(kKFull, kKRing, kiss);
       drain(kV8Full, kVRing, viss);
     }
-   } else if (warp == kMWarp) {
+   } else if (warp - kMWarp < nx) {
     // ----------------------------------------------------------- tensor cores
-    // The whole warp walks the tiles, so that descriptors and addresses stay in
-    // uniform registers; one elected lane issues.
+    // One warp per query tile, each with the chain S(0), O(0), S(1), O(1) ..
+    // of its own tile: a wait drains what its warp has issued, and the other
+    // warp's products fill the tensor pipe meanwhile.  The whole warp walks the
+    // tiles, so that descriptors and addresses stay in uniform registers; one
+    // elected lane issues.
     constexpr uint32_t kIdS = idesc_f16_f32(kRows, kT);  // E4M3 is type 0 of kind::f8f6f4, as f16 is of kind::f16
     constexpr uint32_t kIdO = idesc_f16_f32(kRows, D);
-    const uint64_t dq0 = smem_desc(sb + G::kQ, 128, 8 * D);
+    const int x = warp - kMWarp;
+    const uint64_t dq = smem_desc(sb + G::kQ + x * 2 * G::kQBytes, 128, 8 * D);
     const uint64_t dk0 = smem_desc(sb + G::kK, 128, 8 * D);
     const uint64_t dv0 = smem_desc(sb + G::kV, (D / 8) * 128, 128);
-    uint32_t last_bar = 0, last_par = 0;
-    const auto issue_s = [&](int ring, int x) {
-      const uint64_t dq = dq0 + (uint64_t)(x * (2 * G::kQBytes / 16));
+    const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * kT);
+    const uint32_t s_full = bars + 8 * (kSFull + x), p_full = bars + 8 * (kPFull + x);
+    const uint32_t pv_done = bars + 8 * (kPvDone + x);
+    const auto issue_s = [&](int ring) {
       const uint64_t dk = dk0 + (uint64_t)(ring * (kT * D / 16));
-      const uint32_t d = tmem + (uint32_t)(x * kT);
       if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < D / 32; ++s) tc_mma_f8(d, dq + (uint64_t)(16 * s), dk + (uint64_t)(16 * s), kIdS, s > 0);
+        for (int s = 0; s < D / 32; ++s) tc_mma_f8(s_col, dq + (uint64_t)(16 * s), dk + (uint64_t)(16 * s), kIdS, s > 0);
 #pragma unroll
         for (int s = 0; s < D / 32; ++s)
-          tc_mma_f8(d, dq + (uint64_t)(G::kQBytes / 16 + 16 * s), dk + (uint64_t)(16 * s), kIdS, true);
-        tc_commit(bars + 8 * (kSFull + x));
-        if (x == nx - 1) tc_commit(bars + 8 * (kKEmpty + ring));
+          tc_mma_f8(s_col, dq + (uint64_t)(G::kQBytes / 16 + 16 * s), dk + (uint64_t)(16 * s), kIdS, true);
+        tc_commit(s_full);
+        tc_commit(bars + 8 * (kKEmpty + ring));
       }
       __syncwarp();
     };
+    uint32_t last_bar = 0, last_par = 0;
     bool ok = wwait8(bars + 8 * kKFull, 0u, abort);
     if (ok) {
       tc_fence_after();
-      for (int x = 0; x < nx; ++x) issue_s(0, x);
-      last_bar = bars + 8 * (kSFull + nx - 1);
+      issue_s(0);
+      last_bar = s_full;
     }
-    int kr = 0, vslot = 0;               // rings' positions
+    int kr = 0, vslot = 0;               // the rings' positions
     uint32_t kpar = 0, vpar = 0;         // and their phases
     for (int j = 0; j < ntiles && ok; ++j) {
-      if (!(ok = wwait8(bars + 8 * (kVFull + vslot), vpar, abort))) break;
-      const uint64_t dv = dv0 + (uint64_t)(vslot * (kT * D * 2 / 16));
       const bool more = j + 1 < ntiles;
       if (++kr == kKRing) {
         kr = 0;
         kpar ^= 1u;
       }
-      for (int x = 0; x < nx; ++x) {
-        if (!(ok = wwait8(bars + 8 * (kPFull + x), (uint32_t)j & 1u, abort))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(kOCol8 + x * kT), a = tmem + (uint32_t)(x * kT);
-        if (elect_one()) {
+      if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), kpar, abort))) break;
+      if (!(ok = wwait8(bars + 8 * (kVFull + vslot), vpar, abort))) break;
+      if (!(ok = wwait8(p_full, (uint32_t)j & 1u, abort))) break;
+      // A(0), B(0), A(1), ..: the tiles take turns, so that one's softmax runs
+      // beside the other's products
+      if (nx > 1 && (x > 0 || j > 0) && !(ok = wwait8(bars + 8 * (kTurn + x), (uint32_t)(x > 0 ? j : j - 1) & 1u, abort)))
+        break;
+      tc_fence_after();
+      const uint64_t dv = dv0 + (uint64_t)(vslot * (kT * D * 2 / 16));
+      if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < kT / 16; ++s)
-            tc_mma_f16_ta(d, a + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, j > 0 || s > 0);
-          tc_commit(bars + 8 * (kPvDone + x));
-          if (x == nx - 1) tc_commit(bars + 8 * (kVEmpty + vslot));
-        }
-        __syncwarp();
-        last_bar = bars + 8 * (kPvDone + x);
-        last_par = (uint32_t)j & 1u;
-        if (more) {
-          if (x == 0 && !(ok = wwait8(bars + 8 * (kKFull + kr), kpar, abort))) break;
-          // P_X lives in S_X's columns: the next scores follow the product that reads it
-          if (!(ok = wwait8(bars + 8 * (kPvDone + x), (uint32_t)j & 1u, abort))) break;
-          tc_fence_after();
-          issue_s(kr, x);
-          last_bar = bars + 8 * (kSFull + x);
-          last_par = (uint32_t)(j + 1) & 1u;
-        }
+        for (int s = 0; s < kT / 16; ++s)
+          tc_mma_f16_ta(o_col, s_col + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, j > 0 || s > 0);
+        tc_commit(pv_done);
+        tc_commit(bars + 8 * (kVEmpty + vslot));
       }
+      __syncwarp();
+      last_bar = pv_done;
+      last_par = (uint32_t)j & 1u;
+      if (more) {
+        // P lives in S's columns: the next scores follow the product that reads it
+        if (!(ok = wwait8(pv_done, (uint32_t)j & 1u, abort))) break;
+        tc_fence_after();
+        issue_s(kr);
+        last_bar = s_full;
+        last_par = (uint32_t)(j + 1) & 1u;
+      }
+      if (nx > 1 && lane == 0) mbar_arrive(bars + 8 * (kTurn + (x ^ 1)));
       if (++vslot == kVSlots8) {
         vslot = 0;
         vpar ^= 1u;
