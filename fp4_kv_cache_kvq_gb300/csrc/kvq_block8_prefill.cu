@@ -107,7 +107,7 @@ __device__ __forceinline__ bool pwait8(uint32_t bar, uint32_t parity, volatile i
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
-    if (mbar_try_wait_hint(bar, parity, kPoll8)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       *abort = 1;
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (j >= kVSlots8 && !wwait8(bars + 8 * (kVEmpty + slot), (uint32_t)(j / kVSlots8 - 1) & 1u, abort)) break;
       const uint32_t good = vgood[s];
       const bool whole = valid == kT && good == 0xFFu;
-#pragma unroll 2
+#pragma unroll 1
       for (int it = dt; it < D * (kT / 16); it += 32 * kExpWarps) {
         const int c = it % D, blk = it / D;
         uint4 w = lds128(codes + (uint32_t)((blk * D + c) * 16));
