@@ -14,13 +14,13 @@
 // f16 (2^-11 relative) for the second product.
 //
 // What bounds it: HBM, 2 Hkv (d + 1/4) bytes a position against 4 Hq d flop.
-// Work split: all units' 64-token chunks laid end to end and cut into equal
+// Work split: all units' chunks (64 tokens, 128 at head_dim 64) laid end to end and cut into equal
 // ranges, one per CTA of a persistent grid, so ragged lengths balance to
 // within a chunk; a CTA leaves one partial (m, l, o) per unit it touches and
 // the merge (kvq_merge.cu) joins them.
-// CTA: 4 consumer warps, 16 tokens of a chunk each, and a producer lane that
+// CTA: 4 consumer warps, a quarter of a chunk each, and a producer warp that
 // keeps a ring of stages full with one bulk copy per group (mbarriers; every
-// wait bounded).  A chunk of a page of 64 tokens or more is one copy.
+// wait bounded).
 #include "kvq_block8.cuh"
 #include "kvq_common.cuh"
 #include "kvq_decode.cuh"
@@ -29,8 +29,11 @@
 namespace kvq {
 namespace {
 
-constexpr int kB8Chunk = 64;   // tokens per stage
-constexpr int kB8Warps = 4;    // consumer warps, one 16-token slice each
+constexpr int kB8Warps = 4;    // consumer warps
+// Tokens per stage: 16 KB of codes at either head size (at head_dim 64 a stage
+// of 64 tokens left too little to do between two hand-offs).
+template <int D>
+__host__ __device__ constexpr int chunk8() { return D == 64 ? 128 : 64; }
 constexpr int kB8Threads = 32 * (kB8Warps + 1);
 constexpr int kB8Stages = 3;
 constexpr int kB8CtasPerSm = 3;
@@ -54,12 +57,14 @@ struct Grp8 {
   static constexpr int kV = GT * D;
   static constexpr int kScales = 2 * GT * D;
   static constexpr int kBytes = 2 * GT * D + (GT >= 32 ? GT / 2 : 16);
-  static constexpr int kCopies = kB8Chunk / GT;  // groups per stage
+  static constexpr int kCopies = chunk8<D>() / GT;  // groups per stage
 };
 
 template <int D>
 struct Geo8 {
-  static constexpr int kStageBytes = (4 * Grp8<D, 16>::kBytes + 127) / 128 * 128;  // the largest of the group sizes
+  static constexpr int kSlices = chunk8<D>() / (16 * kB8Warps);  // 16-token slices per warp
+  static constexpr int kStageBytes =
+      (chunk8<D>() / 16 * Grp8<D, 16>::kBytes + 127) / 128 * 128;  // the largest of the group sizes
   static constexpr int kFlushBytes = kB8Warps * kNG * (D + 2) * 4;
   static constexpr int kSmemBytes = kB8Stages * kStageBytes + kFlushBytes + 2 * kB8Stages * 8 + 2 * kB8Stages * 4 + 16 + 128;
 };
@@ -73,7 +78,7 @@ struct Smem8 {
   uint64_t* full;
   uint64_t* empty;
   int* ntok;
-  uint32_t* good;   // bit w: slice w of the stage lies in a valid page
+  uint32_t* good;   // bit i: slice i of the stage lies in a valid page
   int* abort;
 };
 
@@ -116,58 +121,71 @@ __device__ __forceinline__ void f16x2x2_from_e4m3x4(uint32_t w, uint32_t& lo, ui
 }
 
 // ------------------------------------------------------------------ producer
-// Issue the bulk copies of one chunk into stage s.  Tokens of a group whose
-// page is not valid are left out: the slices of the group lose their bit.
-template <int D, int GT>
-__device__ __forceinline__ void issue_chunk8(const Decode8Params& p, Smem8<D>& sm, const Walker& wk, uint32_t s) {
-  using R = Grp8<D, GT>;
-  const int T = __ldg(p.lens + wk.b);
-  const int64_t tok0 = (int64_t)wk.c * kB8Chunk;
-  const int ntok = (int)min((int64_t)kB8Chunk, T - tok0);
-  const int P = p.c.page_size;
-  const uint32_t full = smem_addr(&sm.full[s]);
-  const uint32_t st = smem_addr(sm.stages) + s * Geo8<D>::kStageBytes;
-  const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
-  const int64_t page_bytes = (int64_t)(P / GT) * R::kBytes;
-  int64_t src[R::kCopies];
-  uint32_t good = 0, n = 0;
-#pragma unroll
-  for (int i = 0; i < R::kCopies; ++i) {
-    src[i] = -1;
-    if (i * GT >= ntok) continue;
-    const int64_t pos = tok0 + i * GT;
-    const int64_t phys = block8_page(p.c, wk.b, pos, p.flag);
-    if (phys < 0) continue;
-    src[i] = (phys * p.hkv + wk.h) * page_bytes + ((int)(pos & (P - 1)) / GT) * R::kBytes;
-    if (!KVQ_IN(src[i] >= 0 && src[i] + R::kBytes <= p.c.num_pages * (int64_t)p.hkv * page_bytes &&
-                    (i + 1) * R::kBytes <= Geo8<D>::kStageBytes,
-                p.flag)) {
-      src[i] = -1;
-      continue;
-    }
-    good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
-    ++n;
-  }
-  sm.ntok[s] = ntok;
-  sm.good[s] = good;
-  mbar_arrive_expect_tx(full, n * R::kBytes);
-#pragma unroll
-  for (int i = 0; i < R::kCopies; ++i)
-    if (src[i] >= 0) bulk_g2s(st + i * R::kBytes, pool + src[i], R::kBytes, full);
-}
-
+// The producer warp.  Lane i < kCopies issues the copy of the stage's group i.
+// The page table's entries come 32 at a time into the lanes' registers, the
+// next 32 ahead of their use, so that no copy waits for a lookup (a lookup per
+// copy bound the pages of 16 tokens to 0.78 of the rate).  Tokens of a group
+// whose page is not valid are left out: its slices lose their bit.
 template <int D, int GT>
 __device__ void producer8(const Decode8Params& p, Smem8<D>& sm, Walker wk, int64_t v1) {
+  using R = Grp8<D, GT>;
+  constexpr int C = chunk8<D>();
+  const int lane = threadIdx.x & 31;
+  const int P = p.c.page_size, lg_p = __ffs(P) - 1;
+  const int64_t page_bytes = (int64_t)(P / GT) * R::kBytes;
+  const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
+  const auto entry = [&](int b, int64_t pg) -> int64_t {
+    if (pg >= p.c.max_pages_per_seq) return -1;
+    const int64_t at = (int64_t)b * p.c.max_pages_per_seq + pg;
+    return p.c.page_table ? (int64_t)__ldg(p.c.page_table + at) : at;
+  };
+  int wb = -1;              // the window of 32 entries held: sequence and first page
+  int64_t w0 = 0, win = -1, nxt = -1;
   uint32_t it = 0;
-  for (; wk.v < v1; advance<kB8Chunk>(p, wk), ++it) {
+  for (; wk.v < v1; advance<C>(p, wk), ++it) {
     const uint32_t s = it % kB8Stages;
+    const int64_t tok0 = (int64_t)wk.c * C;
+    const int ntok = (int)min((int64_t)C, __ldg(p.lens + wk.b) - tok0);
+    const int64_t pg0 = tok0 >> lg_p, pg1 = (tok0 + ntok - 1) >> lg_p;
+    if (wk.b != wb || pg0 < w0 || pg1 >= w0 + 32) {
+      if (wk.b == wb && pg0 == w0 + 32) {
+        win = nxt;
+      } else {
+        win = entry(wk.b, pg0 + lane);
+      }
+      wb = wk.b;
+      w0 = pg0;
+      nxt = entry(wb, w0 + 32 + lane);
+    }
+    const int64_t pos = tok0 + lane * GT;
+    const bool need = lane < R::kCopies && lane * GT < ntok;
+    const int64_t phys = __shfl_sync(0xFFFFFFFFu, win, need ? (int)((pos >> lg_p) - w0) : 0);
+    const int64_t src = (phys * p.hkv + wk.h) * page_bytes + ((int)(pos & (P - 1)) / GT) * R::kBytes;
+    bool ok = need && phys >= 0 && phys < p.c.num_pages;
+    if (need && !ok) set_flag(p.flag, KVQ_FLAG_PAGE_OOB);
+    ok = ok && KVQ_IN(src >= 0 && src + R::kBytes <= p.c.num_pages * (int64_t)p.hkv * page_bytes &&
+                          (lane + 1) * R::kBytes <= Geo8<D>::kStageBytes,
+                      p.flag);
+    const uint32_t got = __ballot_sync(0xFFFFFFFFu, ok);
+    bool live = true;
     if (it >= (uint32_t)kB8Stages && !mbar_wait(smem_addr(&sm.empty[s]), ((it / kB8Stages) + 1) & 1)) {
       set_flag(p.flag, KVQ_FLAG_TIMEOUT);
       *reinterpret_cast<volatile int*>(sm.abort) = 1;
-      break;
+      live = false;
     }
-    if (*reinterpret_cast<volatile int*>(sm.abort)) break;
-    issue_chunk8<D, GT>(p, sm, wk, s);
+    if (!__all_sync(0xFFFFFFFFu, live && *reinterpret_cast<volatile int*>(sm.abort) == 0)) break;
+    const uint32_t full = smem_addr(&sm.full[s]);
+    if (lane == 0) {
+      uint32_t good = 0;
+#pragma unroll
+      for (int i = 0; i < R::kCopies; ++i)
+        if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
+      sm.ntok[s] = ntok;
+      sm.good[s] = good;
+      mbar_arrive_expect_tx(full, (uint32_t)__popc(got) * R::kBytes);
+    }
+    __syncwarp();
+    if (ok) bulk_g2s(smem_addr(sm.stages) + s * Geo8<D>::kStageBytes + lane * R::kBytes, pool + src, R::kBytes, full);
   }
   // every copy still in flight lands before the CTA can retire
   for (uint32_t j = it > (uint32_t)kB8Stages ? it - kB8Stages : 0; j < it; ++j) {
@@ -226,15 +244,16 @@ __device__ __forceinline__ void begin_unit8(const Decode8Params& p, State8<D>& s
     for (int i = 0; i < 4; ++i) st.o[mt][i] = 0.0f;
 }
 
-// This warp's slice of one stage.  PARTIAL: only tokens [0, ntok) of the slice
-// are attended (the last chunk of a unit).
-template <int D, int GT, bool PARTIAL>
-__device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int ntok, uint32_t empty_bar) {
+// Slice `sl` of a stage (16 tokens).  PARTIAL: only tokens [0, ntok) of it are
+// attended (the last chunk of a unit).  LAST: the warp is done with the stage
+// once the V codes are in registers.
+template <int D, int GT, bool PARTIAL, bool LAST>
+__device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int sl, int ntok, uint32_t empty_bar) {
   using R = Grp8<D, GT>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t grp = stage + (uint32_t)((16 * warp / GT) * R::kBytes);
-  const int blk = (16 * warp % GT) / 16;  // the slice's block in its group
+  const uint32_t grp = stage + (uint32_t)((16 * sl / GT) * R::kBytes);
+  const int blk = (16 * sl % GT) / 16;  // the slice's block in its group
   const uint2 sc = lds64(grp + R::kScales + 8 * blk);
   const float ks = __uint_as_float(sc.x), vs = __uint_as_float(sc.y);
 
@@ -291,7 +310,7 @@ __device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int ntok
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[4 * i + j] = r[j];
   }
-  mbar_arrive(empty_bar);
+  if (LAST) mbar_arrive(empty_bar);
   if (PARTIAL) {  // stale bytes of tokens behind the end must not inject NaN
     const uint32_t keep = (2 * t < ntok ? 0x000000FFu : 0u) | (2 * t + 1 < ntok ? 0x0000FF00u : 0u) |
                           (2 * t + 8 < ntok ? 0x00FF0000u : 0u) | (2 * t + 9 < ntok ? 0xFF000000u : 0u);
@@ -392,10 +411,10 @@ __global__ void __launch_bounds__(kB8Threads, kB8CtasPerSm) decode_block8_kernel
 
   int64_t total, v0, v1;
   Walker wk;
-  plan<kB8Chunk>(p, blockIdx.x, gridDim.x, total, v0, v1, wk);
+  plan<chunk8<D>()>(p, blockIdx.x, gridDim.x, total, v0, v1, wk);
   if (v0 >= v1) return;
   if (warp == kB8Warps) {
-    if (lane == 0) producer8<D, GT>(p, sm, wk, v1);
+    producer8<D, GT>(p, sm, wk, v1);
     return;
   }
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(kB8Threads, kB8CtasPerSm) decode_block8_kernel
   bool have = false, dead = false;
   int64_t slot = 0;
   uint32_t it = 0;
-  for (; wk.v < v1; advance<kB8Chunk>(p, wk), ++it) {
+  for (; wk.v < v1; advance<chunk8<D>()>(p, wk), ++it) {
     if (!have || wk.c == 0) {
       if (have) flush_unit8<D>(p, st, sm, slot);
       const int64_t u = (int64_t)wk.b * p.hkv + wk.h;
@@ -429,14 +448,19 @@ __global__ void __launch_bounds__(kB8Threads, kB8CtasPerSm) decode_block8_kernel
       }
       continue;
     }
-    const int n = sm.ntok[s] - 16 * warp;  // attended tokens of this warp's slice
-    const uint32_t bar = smem_addr(&sm.empty[s]);
-    if (n <= 0 || !((sm.good[s] >> warp) & 1u))
+    const int ntok = sm.ntok[s];
+    const uint32_t good = sm.good[s], bar = smem_addr(&sm.empty[s]), stage = stages + s * G::kStageBytes;
+    const int s0 = warp * G::kSlices;
+    constexpr uint32_t kAll = (1u << G::kSlices) - 1u;
+    if (ntok >= 16 * (s0 + G::kSlices) && ((good >> s0) & kAll) == kAll) {
+      if constexpr (G::kSlices > 1) consume8<D, GT, false, false>(st, stage, s0, 16, bar);
+      consume8<D, GT, false, true>(st, stage, s0 + G::kSlices - 1, 16, bar);
+    } else {
+#pragma unroll 1
+      for (int i = s0; i < s0 + G::kSlices; ++i)
+        if (ntok > 16 * i && ((good >> i) & 1u)) consume8<D, GT, true, false>(st, stage, i, ntok - 16 * i, bar);
       mbar_arrive(bar);
-    else if (n < 16)
-      consume8<D, GT, true>(st, stages + s * G::kStageBytes, n, bar);
-    else
-      consume8<D, GT, false>(st, stages + s * G::kStageBytes, 16, bar);
+    }
   }
   if (have) flush_unit8<D>(p, st, sm, slot);
 }
