@@ -337,6 +337,16 @@ def _table_rows(dev: int, cache, page_table: Optional[torch.Tensor], batch: int)
         raise ValueError("the page table has fewer rows than sequences")
 
 
+def _alloc(stream, shape, dtype: torch.dtype, dev: int, zero: bool = False) -> torch.Tensor:
+    """A buffer of a call on `stream` (None: the current one): from that stream's
+    memory, so that nothing still running on another stream uses it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+
+
 def _err_ptr(dev: int, err: Optional[torch.Tensor]) -> Optional[int]:
     if err is None:
         return None
@@ -435,7 +445,7 @@ def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: to
         if q.shape != (B, n, hq, d):
             raise ValueError("q must have shape [batch, n_new, num_q_heads, head_dim]")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _alloc(stream, q.shape, torch.bfloat16, dev)
         else:
             _on(dev, q_out, torch.bfloat16, "q_out")
             if q_out.shape != q.shape:
@@ -519,22 +529,22 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
 _OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _attn_out(dev: int, cache, q: torch.Tensor, out: Optional[torch.Tensor], padded: bool):
+def _attn_out(dev: int, cache, q: torch.Tensor, out: Optional[torch.Tensor], padded: bool, stream):
     """(out, its KVQ_DTYPE_*) of an attention over an Fp8BlockCache."""
     _on(dev, q, torch.bfloat16, "q")
     if q.shape[-1] != cache.head_dim:
         raise ValueError("q must have the cache's head_dim")
     if out is None:  # rows of a padded batch's padding are not written
-        out = (torch.zeros if padded else torch.empty)(q.shape, dtype=torch.float32, device=q.device)
+        out = _alloc(stream, q.shape, torch.float32, dev, zero=padded)
     code = _OUT_DTYPES.get(out.dtype)
     if code is None or out.get_device() != dev or not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be a contiguous float32 or bfloat16 tensor of q's shape on the cache's device")
     return out, code
 
 
-def _workspace(dev: int, workspace: Optional[torch.Tensor], need, *sizes) -> torch.Tensor:
+def _workspace(dev: int, workspace: Optional[torch.Tensor], stream, need, *sizes) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(max(16, need(*sizes)), dtype=torch.uint8, device=f"cuda:{dev}")
+        return _alloc(stream, max(16, need(*sizes)), torch.uint8, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return workspace  # its size is checked by the library
@@ -544,11 +554,11 @@ def _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, strea
     dev = _device(cache)
     if q.dim() != 3:
         raise ValueError("q must have shape [batch, num_q_heads, head_dim]")
-    out, code = _attn_out(dev, cache, q, out, False)
+    out, code = _attn_out(dev, cache, q, out, False, stream)
     B, hq, d = q.shape
     _per_seq(dev, seq_lens, B, "seq_lens")
     _table_rows(dev, cache, None, B)
-    ws = _workspace(dev, workspace, decode_workspace_bytes, B, hq, cache.num_kv_heads, d)
+    ws = _workspace(dev, workspace, stream, decode_workspace_bytes, B, hq, cache.num_kv_heads, d)
     s = cache.struct()
     st = load().kvq_fp8_block_decode_attn(ctypes.byref(s), B, hq, seq_lens.data_ptr(), q.data_ptr(),
                                           1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
@@ -594,13 +604,13 @@ def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_l
     dev = _device(cache)
     if q.dim() != 4:
         raise ValueError("q must have shape [batch, chunk, num_q_heads, head_dim]")
-    out, code = _attn_out(dev, cache, q, out, chunk_lens is not None)
+    out, code = _attn_out(dev, cache, q, out, chunk_lens is not None, stream)
     B, chunk, hq, d = q.shape
     _per_seq(dev, seq_lens, B, "seq_lens")
     if chunk_lens is not None:
         _per_seq(dev, chunk_lens, B, "chunk_lens")
     _table_rows(dev, cache, None, B)
-    ws = _workspace(dev, workspace, prefill_workspace_bytes, B, hq, cache.num_kv_heads, d, chunk)
+    ws = _workspace(dev, workspace, stream, prefill_workspace_bytes, B, hq, cache.num_kv_heads, d, chunk)
     s = cache.struct()
     st = load().kvq_fp8_block_prefill_attn(ctypes.byref(s), B, hq, chunk, seq_lens.data_ptr(), _ptr(chunk_lens),
                                            q.data_ptr(),
@@ -684,8 +694,11 @@ def dequant(cache, seq_lens: Optional[torch.Tensor], max_len: int, dtype: torch.
         device = cache.k_codes.device
     code = {torch.float32: 0, torch.bfloat16: 1}[dtype]
     shape = (batch, max_len, cache.num_kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=device)
-    v = torch.empty(shape, dtype=dtype, device=device)
+    if block8:
+        k, v = _alloc(stream, shape, dtype, dev), _alloc(stream, shape, dtype, dev)
+    else:
+        k = torch.empty(shape, dtype=dtype, device=device)
+        v = torch.empty(shape, dtype=dtype, device=device)
     fn = load().kvq_fp8_block_dequant if block8 else load().kvq_dequant
     st = fn(ctypes.byref(s), batch, _ptr(seq_lens), max_len, code, _ptr(k), _ptr(v), _ptr(err), _stream(stream))
     _check(st, "kvq_fp8_block_dequant" if block8 else "kvq_dequant")

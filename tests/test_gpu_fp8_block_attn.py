@@ -328,3 +328,63 @@ def test_python_and_workspace_refusals():
     with pytest.raises(kvq.KvqError) as e:
         kvq.decode_attn(cache, lens, torch.zeros((2, 18, 64), dtype=BF, device="cuda"))
     assert e.value.status == 2
+
+
+def test_pool_offsets_past_32_bits_and_far_positions():
+    """Pages at the far end of a pool of more than 2^32 bytes, and a sequence of
+    131,079 positions."""
+    d, H, G, page, mp, pages = 128, 2, 8, 256, 520, 33000  # 33000 x 2 x 4 x 16416 bytes = 4.33 GB
+    table = torch.randint(32900, pages, (1, mp), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    cache = kvq.Fp8BlockCache(H, d, page, pages, mp, page_table=table)
+    for pg in range(32900, pages):  # each page filled through a table of its own
+        k = torch.randn((1, page, H, d), generator=_gen(pg), device="cuda").to(BF)
+        one = torch.full((1, mp), pg, dtype=torch.int32, device="cuda")
+        kvq.append(cache, _ints([0]), k, (k.float() * 0.5 + 1.0).to(BF), page_table=one)
+    T = 131079
+    q = torch.randn((1, 3, H * G, d), generator=_gen(5), device="cuda").to(BF)
+    err = _ints([0])
+    dec = kvq.decode_attn(cache, _ints([T]), q[:, 2].contiguous(), err=err)
+    pre = kvq.prefill_attn(cache, _ints([T]), q, err=err)
+    assert err.item() == 0
+    check(dec[:, None], q[:, 2:], cache, [T], [1], 1 / math.sqrt(d), False)
+    check(pre, q, cache, [T], [3], 1 / math.sqrt(d), True)
+
+
+def test_a_large_batch_of_single_tokens():
+    """3000 sequences (24,000 units), lengths 0 to 3."""
+    B, H, G, d = 3000, 8, 1, 64
+    lens = torch.randint(0, 4, (B,), generator=torch.Generator().manual_seed(2)).tolist()
+    cache = build(lens, H, d, 16, seed=3)
+    q = torch.randn((B, 1, H * G, d), generator=_gen(4), device="cuda").to(BF)
+    dec = kvq.decode_attn(cache, _ints(lens), q[:, 0].contiguous())
+    K, V = kvq.dequant(cache, _ints(lens), 4)
+    s = torch.einsum("bhd,bthd->bht", q[:, 0].double(), K.double()) / math.sqrt(d)
+    s = s.masked_fill(torch.arange(4, device="cuda") >= _ints(lens)[:, None, None], -math.inf)
+    want = torch.einsum("bht,bthd->bhd", torch.softmax(s, -1).nan_to_num(0.0), V.double())
+    vmax = V.abs().amax((1, 3))[..., None].double()
+    a = (q[:, 0].double().abs()[:, None] * K.double().abs()).sum(-1).max().item() / math.sqrt(d) * math.log2(math.e)
+    tol = ref.tolerance(d, 4, 1.0, a) * vmax
+    assert ((dec.double() - want).abs() <= tol).all()
+    n = torch.tensor([min(1, x) for x in lens], dtype=torch.int32, device="cuda")
+    pre = kvq.prefill_attn(cache, _ints(lens), q, chunk_lens=n)
+    bq = (q[:, 0].double().abs().amax(-1)[:, None] * K.double().abs().sum(-1)).max().item() / math.sqrt(d) * math.log2(math.e)
+    assert ((pre[:, 0].double() - want).abs() <= ref.tolerance(d, 4, 1.0, a, bq) * vmax).all()
+
+
+def test_an_explicit_stream():
+    """Work on a stream given to the call, buffers made by it included, while the
+    current stream is busy with other memory."""
+    lens = [900, 77]
+    cache = build(lens, 2, 128, 64, seed=6)
+    q = torch.randn((2, 30, 8, 128), generator=_gen(7), device="cuda").to(BF)
+    want, dwant = kvq.prefill_attn(cache, _ints(lens), q), kvq.decode_attn(cache, _ints(lens), q[:, 3].contiguous())
+    n, q3 = _ints(lens), q[:, 3].contiguous()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        noise = torch.randn((1 << 22,), device="cuda")
+        del noise  # its memory is free for the current stream while the kernel that fills it runs
+        out = kvq.prefill_attn(cache, n, q, stream=side)
+        dec = kvq.decode_attn(cache, n, q3, stream=side)
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(dec, dwant)
