@@ -56,6 +56,8 @@ struct Decode8Params {
   int32_t batch, hkv, g, hq, window;  // window: 0 (the shared walk's parameter)
   float qk_log2;                      // softmax_scale * log2(e)
   int64_t n_slots;
+  void* out;                          // direct: the result, else nullptr
+  int32_t out_bf16;
 };
 
 // Compile-time view of one group of GT tokens (see Block8Layout).
@@ -342,8 +344,20 @@ __device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int sl, 
   }
 }
 
-// Combine the four warps' states for one unit and write the CTA's partial.
-template <int D>
+__device__ __forceinline__ void store_out8(const Decode8Params& p, int64_t row, int d, int c4, float4 o) {
+  if (p.out_bf16) {
+    uint2 v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(v.x) : "f"(o.y), "f"(o.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(v.y) : "f"(o.w), "f"(o.z));
+    *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * d) + c4) = v;
+  } else {
+    *(reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * d) + c4) = o;
+  }
+}
+
+// Combine the four warps' states for one unit and write the CTA's partial into
+// slot `slot` (DIRECT: the result, to the output rows from `slot` on).
+template <int D, bool DIRECT>
 __device__ void flush_unit8(const Decode8Params& p, State8<D>& st, Smem8<D>& sm, int64_t slot) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -369,7 +383,7 @@ __device__ void flush_unit8(const Decode8Params& p, State8<D>& st, Smem8<D>& sm,
     sm.flush_l[warp * kNG + 2 * t + 1] = st.l[1];
   }
   named_barrier_sync(1, 32 * kB8Warps);
-  if (!KVQ_IN(slot >= 0 && slot < p.n_slots, p.flag)) return;
+  if (!KVQ_IN(slot >= 0 && slot < (DIRECT ? (int64_t)p.batch * p.hq : p.n_slots), p.flag)) return;
   for (int idx = tid; idx < p.g * (D / 4); idx += 32 * kB8Warps) {
     const int r = idx / (D / 4), c4 = idx % (D / 4);
     float mx = -INFINITY;
@@ -390,12 +404,20 @@ __device__ void flush_unit8(const Decode8Params& p, State8<D>& st, Smem8<D>& sm,
         l = fmaf(f, sm.flush_l[w * kNG + r], l);
       }
     }
+    if constexpr (DIRECT) {
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      store_out8(p, slot + r, D, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      continue;
+    }
     *(reinterpret_cast<float4*>(p.part_o + (slot * p.g + r) * D) + c4) = o;
     if (c4 == 0) *(reinterpret_cast<float2*>(p.part_ml) + slot * p.g + r) = make_float2(mx, l);
   }
 }
 
-template <int D, int GT>
+// DIRECT: one CTA per unit, which walks all of its chunks and writes the result
+// itself (caches of few chunks); else the equal ranges and partials described
+// above.
+template <int D, int GT, bool DIRECT>
 __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(const Decode8Params p) {
   using G = Geo8<D>;
   extern __shared__ uint8_t smem8_raw[];
@@ -418,7 +440,23 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
 
   int64_t total, v0, v1;
   Walker wk;
-  plan<chunk8<D>()>(p, blockIdx.x, gridDim.x, total, v0, v1, wk);
+  if constexpr (DIRECT) {
+    wk.b = (int)(blockIdx.x / (unsigned)p.hkv);
+    wk.h = (int)(blockIdx.x % (unsigned)p.hkv);
+    const int32_t T = __ldg(p.lens + wk.b);
+    wk.c = 0;
+    wk.v = v0 = 0;
+    total = v1 = wk.nch = fp4_chunks<chunk8<D>()>(T, 0);
+    if (v1 == 0) {  // no position: zero rows
+      if (T < 0 && wk.h == 0 && threadIdx.x == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
+      for (int i = threadIdx.x; i < p.g * (D / 4); i += kB8Threads)
+        store_out8(p, (int64_t)wk.b * p.hq + (int64_t)wk.h * p.g + i / (D / 4), D, i % (D / 4),
+                   make_float4(0.f, 0.f, 0.f, 0.f));
+      return;
+    }
+  } else {
+    plan<chunk8<D>()>(p, blockIdx.x, gridDim.x, total, v0, v1, wk);
+  }
   if (v0 >= v1) return;
   if (warp == kB8Warps) {
     producer8<D, GT>(p, sm, wk, v1);
@@ -432,12 +470,12 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
   uint32_t it = 0;
   for (; wk.v < v1; advance<chunk8<D>()>(p, wk), ++it) {
     if (!have || wk.c == 0) {
-      if (have) flush_unit8<D>(p, st, sm, slot);
+      if (!DIRECT && have) flush_unit8<D, DIRECT>(p, st, sm, slot);
       const int64_t u = (int64_t)wk.b * p.hkv + wk.h;
-      slot = u + blockIdx.x;
+      slot = DIRECT ? u * p.g : u + blockIdx.x;  // (u * g: the unit's first output row)
       begin_unit8<D>(p, st, wk.b, wk.h);
       have = true;
-      if (wk.c == 0 && threadIdx.x == 0) {
+      if (!DIRECT && wk.c == 0 && threadIdx.x == 0) {
         const int64_t last_cta = (wk.v + wk.nch - 1) / per;
         if (KVQ_IN(u < (int64_t)p.batch * p.hkv && last_cta < gridDim.x, p.flag))
           p.unit_rec[u] = make_int2((int)slot, (int)(last_cta - blockIdx.x + 1));
@@ -469,17 +507,17 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
       mbar_arrive(bar);
     }
   }
-  if (have) flush_unit8<D>(p, st, sm, slot);
+  if (have) flush_unit8<D, DIRECT>(p, st, sm, slot);
 }
 
 // ------------------------------------------------------------------ host side
-template <int D, int GT>
+template <int D, int GT, bool DIRECT>
 kvq_status launch_decode8(const Decode8Params& dp, cudaStream_t s, int ctas) {
   static DeviceOnce attr_set;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
   if (attr_set.pending(dev)) {
-    if (cudaFuncSetAttribute(decode_block8_kernel<D, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_block8_kernel<D, GT, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Geo8<D>::kSmemBytes) != cudaSuccess)
       return KVQ_ERR_CUDA;
     attr_set.mark(dev);
@@ -494,17 +532,24 @@ kvq_status launch_decode8(const Decode8Params& dp, cudaStream_t s, int ctas) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_block8_kernel<D, GT>, dp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, decode_block8_kernel<D, GT, DIRECT>, dp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
-template <int D>
+template <int D, bool DIRECT>
 kvq_status launch_decode8_d(const Decode8Params& dp, cudaStream_t s, int ctas) {
   switch (dp.c.page_size) {
-    case 16: return launch_decode8<D, 16>(dp, s, ctas);
-    case 32: return launch_decode8<D, 32>(dp, s, ctas);
-    default: return launch_decode8<D, 64>(dp, s, ctas);
+    case 16: return launch_decode8<D, 16, DIRECT>(dp, s, ctas);
+    case 32: return launch_decode8<D, 32, DIRECT>(dp, s, ctas);
+    default: return launch_decode8<D, 64, DIRECT>(dp, s, ctas);
   }
 }
+
+// One CTA per unit, without partials and their merge, when the cache's capacity
+// (which the host knows; the lengths it does not) holds few chunks per unit, or
+// not many and units for every SM.  Both ways, us a call, 8 kv heads of 128:
+//   batch 8:   512 positions 6.8 direct, 7.4 split;  1024: 10.8, 8.7;  2048: 19.8, 12.3
+//   batch 32:  512           8.7,        12.9;       1024: 14.8, 19.2; 2048: 24.5, 29.0
+constexpr int kDirectChunks = 8, kDirectChunksFull = 32;
 
 }  // namespace
 }  // namespace kvq
@@ -540,7 +585,8 @@ extern "C" kvq_status kvq_fp8_block_decode_attn(const kvq_cache* cache, int32_t 
   // with fewer partials to merge)
   const int64_t cap = (int64_t)cache->max_pages_per_seq * cache->page_size;
   const int chunk = D == 128 ? chunk8<128>() : chunk8<64>();
-  const int64_t pairs = (units * ((cap + chunk - 1) / chunk) + 1) / 2;
+  const int64_t unit_chunks = (cap + chunk - 1) / chunk;
+  const int64_t pairs = (units * unit_chunks + 1) / 2;
   const int64_t full = (int64_t)sms * (D == 128 ? ctas8<128>() : ctas8<64>());
   const int ctas = (int)(pairs < full ? pairs : full);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -560,7 +606,13 @@ extern "C" kvq_status kvq_fp8_block_decode_attn(const kvq_cache* cache, int32_t 
   dp.hq = num_q_heads;
   dp.qk_log2 = softmax_scale * kLog2e;
   dp.n_slots = n_slots;
-  st = D == 128 ? launch_decode8_d<128>(dp, s, ctas) : launch_decode8_d<64>(dp, s, ctas);
+  if (units <= INT32_MAX &&
+      (unit_chunks <= kDirectChunks || (unit_chunks <= kDirectChunksFull && units >= (int64_t)sms))) {
+    dp.out = out;
+    dp.out_bf16 = out_dtype == KVQ_DTYPE_BF16;
+    return D == 128 ? launch_decode8_d<128, true>(dp, s, (int)units) : launch_decode8_d<64, true>(dp, s, (int)units);
+  }
+  st = D == 128 ? launch_decode8_d<128, false>(dp, s, ctas) : launch_decode8_d<64, false>(dp, s, ctas);
   if (st != KVQ_OK) return st;
 
   MergeParams mp = {};

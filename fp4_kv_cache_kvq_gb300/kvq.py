@@ -160,6 +160,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 # The current stream's handle without a torch.cuda.Stream object around it
 # (0.3 us a call instead of 3).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> Optional[int]:
@@ -284,13 +285,19 @@ class Fp8BlockCache:
         if page_table is not None:
             _need_table(page_table, max_pages_per_seq)
         self.pool, self.page_table = pool, page_table
+        self._struct = KvqCacheStruct(FORMAT_FP8_BLOCK, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
+                                      0, None, None, None, None, None)
 
     def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqCacheStruct:
         """The kvq_cache description of the cache as it is now; a page_table
         argument overrides the cache's own for one call."""
-        pt = self.page_table if page_table is None else page_table
-        return KvqCacheStruct(FORMAT_FP8_BLOCK, self.num_kv_heads, self.head_dim, self.page_size, self.num_pages,
-                              self.max_pages_per_seq, 0, _ptr(pt), self.pool.data_ptr(), None, None, None)
+        if page_table is not None:
+            return KvqCacheStruct(FORMAT_FP8_BLOCK, self.num_kv_heads, self.head_dim, self.page_size, self.num_pages,
+                                  self.max_pages_per_seq, 0, page_table.data_ptr(), self.pool.data_ptr(), None, None,
+                                  None)
+        s = self._struct
+        s.page_table, s.data = _ptr(self.page_table), self.pool.data_ptr()
+        return s
 
     @property
     def nbytes(self) -> int:
@@ -308,10 +315,14 @@ def _need_table(t: torch.Tensor, max_pages: int) -> None:
 def _device(cache) -> int:
     """The cache's device, which has to be the current one."""
     dev = cache.pool.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"the cache is on {cache.pool.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return dev
+
+
+def _stream_on(dev: int, stream) -> Optional[int]:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _on(dev: int, t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
@@ -468,7 +479,7 @@ def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: to
     s = cache.struct(page_table)
     st = load().kvq_rope_append(ctypes.byref(s), B, n, start_pos.data_ptr(), _ptr(new_lens), hq, q_ptr, qs,
                                 k.data_ptr(), ks, v.data_ptr(), vs, _ptr(table), rows, rd, 1 if interleaved else 0,
-                                out_ptr, _ptr(k_out), _err_ptr(dev, err), _stream(stream))
+                                out_ptr, _ptr(k_out), _err_ptr(dev, err), _stream_on(dev, stream))
     _check(st, "kvq_rope_append")
     return q_out
 
@@ -563,7 +574,7 @@ def _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, strea
     st = load().kvq_fp8_block_decode_attn(ctypes.byref(s), B, hq, seq_lens.data_ptr(), q.data_ptr(),
                                           1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
                                           out.data_ptr(), code, ws.data_ptr(), ws.nbytes, _err_ptr(dev, err),
-                                          _stream(stream))
+                                          _stream_on(dev, stream))
     _check(st, "kvq_fp8_block_decode_attn")
     return out
 
@@ -616,7 +627,7 @@ def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_l
                                            q.data_ptr(),
                                            1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
                                            out.data_ptr(), code, ws.data_ptr(), ws.nbytes, _err_ptr(dev, err),
-                                           _stream(stream))
+                                           _stream_on(dev, stream))
     _check(st, "kvq_fp8_block_prefill_attn")
     return out
 
