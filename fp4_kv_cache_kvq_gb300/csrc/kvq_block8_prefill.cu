@@ -51,7 +51,7 @@ constexpr int kMWarp = kLdWarp + 1;
 constexpr int kP8Threads = 512;
 constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192 + 72 + 56 = 4 x 128
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * 128, "registers of the launch");
-constexpr int kOCol8 = kXTiles * kT;  // TMEM: S_X (then P_X) at [128 X, +128), O_X at [256 + 128 X, +d)
+constexpr int kOCol8 = kXTiles * kT;  // TMEM: S_X at [128 X, +128), O_X at [256 + d X, +d), P_X: p_col8
 constexpr int kTmem8 = 512;
 constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
 // The running maximum is raised only when a score passes it by this much (log2):
@@ -73,7 +73,8 @@ enum : int {
   kPFull = kSFull + kXTiles,       // [kXTiles] P_X in TMEM, O_X rescaled
   kPvDone = kPFull + kXTiles,      // [kXTiles] O_X += P_X V^ done
   kTurn = kPvDone + kXTiles,       // [kXTiles] query tile X's products may be issued
-  kBars8 = kTurn + kXTiles
+  kSRead = kTurn + kXTiles,        // [kXTiles] S_X in the softmax's registers (head_dim 64)
+  kBars8 = kSRead + kXTiles
 };
 
 struct Prefill8Params {
@@ -90,6 +91,15 @@ struct Prefill8Params {
   int32_t parts;   // partials per row: splits, or twice that for a pair
   float qk_log2;
 };
+
+// P_X's first column.  At head_dim 128 S and O fill the 512 columns, and P_X
+// takes the first half of S_X's, so that the next scores follow the product that
+// reads P_X.  At head_dim 64 it has columns of its own behind O: the next scores
+// are computed as soon as a tile's are in registers, beside its softmax.
+template <int D>
+__host__ __device__ constexpr bool own_p8() { return D == 64; }
+template <int D>
+__host__ __device__ constexpr int p_col8(int x) { return own_p8<D>() ? kOCol8 + kXTiles * D + x * (kT / 2) : x * kT; }
 
 template <int D>
 struct P8Geo {
@@ -311,6 +321,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kPFull + i), 4);
       mbar_init(bars + 8 * (kPvDone + i), 1);
       mbar_init(bars + 8 * (kTurn + i), 1);
+      mbar_init(bars + 8 * (kSRead + i), 4);
     }
     *abort = 0;
     *vref_bits = 0u;
@@ -319,13 +330,65 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
   __syncthreads();
 
-  // sV_ref: the largest V scale of the positions this CTA reads
   const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
   const Block8Layout L(D, p.c.page_size);
-  {
+  // The loader warp's copies of tile j: lane i < kGroups takes group i, K codes
+  // and scales, then V codes and scales.
+  int kiss = 0, viss = 0;
+  const auto load_tile = [&](int j) -> bool {
+    const int ks = j % kKRing, vs = j % kVRing;
+    const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
+    const uint8_t* src = nullptr;
+    if (lane < kGroups && pos < limit) {
+      const int64_t phys = block8_page(p.c, b, pos, p.flag);
+      if (phys >= 0) {
+        const int64_t off = block8_group_offset(L, phys, p.hkv, h, (int)(pos & (p.c.page_size - 1)));
+        if (KVQ_IN(off >= 0 && off + kGroupBytes <= p.c.num_pages * (int64_t)p.hkv * L.page_bytes(), p.flag))
+          src = pool + off;
+      }
+    }
+    const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
+    uint32_t good = 0u;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+      if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
+    const uint32_t bytes = (uint32_t)__popc(got) * (uint32_t)(GT * D + kGroupScale);
+    if (j >= kKRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kKRing - 1) & 1u, abort)) return false;
+    if (lane == 0) {
+      kgood[ks] = good;
+      mbar_arrive_expect_tx(bars + 8 * (kKFull + ks), bytes);
+    }
+    __syncwarp();
+    if (src != nullptr) {
+      bulk_g2s(sb + G::kK + ks * kT * D + lane * GT * D, src, GT * D, bars + 8 * (kKFull + ks));
+      bulk_g2s(sb + G::kKS + ks * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
+               bars + 8 * (kKFull + ks));
+    }
+    kiss = j + 1;
+    if (j >= kVRing && !wwait8(bars + 8 * (kV8Empty + vs), (uint32_t)(j / kVRing - 1) & 1u, abort)) return false;
+    if (lane == 0) {
+      vgood[vs] = good;
+      mbar_arrive_expect_tx(bars + 8 * (kV8Full + vs), bytes);
+    }
+    __syncwarp();
+    if (src != nullptr) {
+      bulk_g2s(sb + G::kV8 + vs * kT * D + lane * GT * D, src + GT * D, GT * D, bars + 8 * (kV8Full + vs));
+      bulk_g2s(sb + G::kVS + vs * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
+               bars + 8 * (kV8Full + vs));
+    }
+    viss = j + 1;
+    return true;
+  };
+  constexpr int kAhead = kKRing < kVRing ? kKRing : kVRing;  // tiles that need no empty slot
+  if (warp == kLdWarp)
+    for (int j = 0; j < min(kAhead, ntiles); ++j) load_tile(j);
+
+  // sV_ref: the largest V scale of the positions this CTA reads (the other
+  // warps prepare the queries meanwhile)
+  if (warp >= kSmWarps) {
     uint32_t best = 0u;
     const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
-    for (int64_t gi = g0 + tid; gi < g1; gi += kP8Threads) {
+    for (int64_t gi = g0 + tid - 32 * kSmWarps; gi < g1; gi += kP8Threads - 32 * kSmWarps) {
       const int64_t phys = block8_page(p.c, b, gi * GT, p.flag);
       if (phys < 0) continue;
       const uint8_t* grp = pool + block8_group_offset(L, phys, p.hkv, h, (int)((gi * GT) & (p.c.page_size - 1)));
@@ -341,7 +404,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 
   // query rows: power-of-two prescale, hi and lo E4M3 parts in operand layout
   float cs = 0.0f;
-  if (warp < kSmWarps) {
+  if (warp < kSmWarps) {  // (one converged block: the prescan above is the other warps')
     const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
     uint32_t amax = 0u;
     if (row_ok) {
@@ -402,7 +465,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     } else {
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t sp_col = t_lane + (uint32_t)(X * kT);
-      const uint32_t op = t_lane + (uint32_t)(kOCol8 + X * kT);
+      const uint32_t p_col = t_lane + (uint32_t)p_col8<D>(X);
+      const uint32_t op = t_lane + (uint32_t)(kOCol8 + X * D);
       const uint32_t s_full = bars + 8 * (kSFull + X), p_full = bars + 8 * (kPFull + X);
       const uint32_t pv_done = bars + 8 * (kPvDone + X);
       const int64_t pos_r = first + ti;  // last position this row attends
@@ -432,6 +496,11 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         tmem_wait_ld_all();
 #pragma unroll
         for (int i = 0; i < 8; ++i) after_wait(v[i], vm[i]);
+        if (own_p8<D>()) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + 8 * (kSRead + X));
+        }
         if (!fast) {
           // masked scores (behind the row's last position, or in a page that is
           // not valid) become -inf, their factor positive: 2^-inf is 0
@@ -458,6 +527,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
           m_run = mt;
         }
+        if (own_p8<D>() && i_own > 0) {  // the product that reads the previous P is done
+          if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
+          tc_fence_after();
+        }
         const float nref = m_run == -INFINITY ? 0.0f : -m_run;
         const uint64_t nref2 = pk2(nref, nref);
         uint64_t l2[2] = {0ull, 0ull};
@@ -466,7 +539,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           uint32_t w[16];
           block_p(v[i], w, csk[i], nref2, l2);
           block_p(v[i + 1], w + 8, csk[i + 1], nref2, l2);
-          tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
+          tmem_st16_async(p_col + (uint32_t)(8 * i), w);
         }
         if (i_own > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
           if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
@@ -580,52 +653,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
    reg_dec<kRegsIssue>();
    if (warp == kLdWarp) {
     // ------------------------------------------------------------ bulk copies
-    // lane i < kGroups copies group i of each tile: K codes and scales, then V
-    // codes and scales
-    int kiss = 0, viss = 0;
-    for (int j = 0; j < ntiles; ++j) {
-      const int ks = j % kKRing, vs = j % kVRing;
-      const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
-      const uint8_t* src = nullptr;
-      if (lane < kGroups && pos < limit) {
-        const int64_t phys = block8_page(p.c, b, pos, p.flag);
-        if (phys >= 0) {
-          const int64_t off = block8_group_offset(L, phys, p.hkv, h, (int)(pos & (p.c.page_size - 1)));
-          if (KVQ_IN(off >= 0 && off + kGroupBytes <= p.c.num_pages * (int64_t)p.hkv * L.page_bytes(), p.flag))
-            src = pool + off;
-        }
-      }
-      const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
-      uint32_t good = 0u;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i)
-        if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
-      const uint32_t bytes = (uint32_t)__popc(got) * (uint32_t)(GT * D + kGroupScale);
-      if (j >= kKRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kKRing - 1) & 1u, abort)) break;
-      if (lane == 0) {
-        kgood[ks] = good;
-        mbar_arrive_expect_tx(bars + 8 * (kKFull + ks), bytes);
-      }
-      __syncwarp();
-      if (src != nullptr) {
-        bulk_g2s(sb + G::kK + ks * kT * D + lane * GT * D, src, GT * D, bars + 8 * (kKFull + ks));
-        bulk_g2s(sb + G::kKS + ks * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
-                 bars + 8 * (kKFull + ks));
-      }
-      kiss = j + 1;
-      if (j >= kVRing && !wwait8(bars + 8 * (kV8Empty + vs), (uint32_t)(j / kVRing - 1) & 1u, abort)) break;
-      if (lane == 0) {
-        vgood[vs] = good;
-        mbar_arrive_expect_tx(bars + 8 * (kV8Full + vs), bytes);
-      }
-      __syncwarp();
-      if (src != nullptr) {
-        bulk_g2s(sb + G::kV8 + vs * kT * D + lane * GT * D, src + GT * D, GT * D, bars + 8 * (kV8Full + vs));
-        bulk_g2s(sb + G::kVS + vs * kScaleBytes + lane * kGroupScale, src + 2 * GT * D, kGroupScale,
-                 bars + 8 * (kV8Full + vs));
-      }
-      viss = j + 1;
-    }
+    for (int j = kAhead; j < ntiles; ++j)
+      if (!load_tile(j)) break;
     if (*abort) {  // copies still in flight land before the shared memory goes away
       const auto drain = [&](int bar, int ring, int issued) {
         for (int j = max(0, issued - ring); j < issued; ++j) {
@@ -651,7 +680,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     const uint64_t dq = smem_desc(sb + G::kQ + (p.pair ? 0 : x) * 2 * G::kQBytes, 128, 8 * D);
     const uint64_t dk0 = smem_desc(sb + G::kK, 128, 8 * D);
     const uint64_t dv0 = smem_desc(sb + G::kV, (D / 8) * 128, 128);
-    const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * kT);
+    const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * D);
+    const uint32_t p_col = tmem + (uint32_t)p_col8<D>(x);
     const uint32_t s_full = bars + 8 * (kSFull + x), p_full = bars + 8 * (kPFull + x);
     const uint32_t pv_done = bars + 8 * (kPvDone + x);
     const auto issue_s = [&](int ring) {
@@ -675,11 +705,18 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       issue_s(j);
       last_bar = s_full;
     }
-    const bool turns = !p.pair && nx > 1;
+    const bool turns = !own_p8<D>() && !p.pair && nx > 1;
     for (uint32_t i = 0; j < ntiles && ok; j += step, ++i) {
       const int jn = j + step, kr = jn % kKRing, vslot = j % kVSlots8;
       const bool more = jn < ntiles;
       if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), (uint32_t)(jn / kKRing) & 1u, abort))) break;
+      if (own_p8<D>() && more) {
+        if (!(ok = wwait8(bars + 8 * (kSRead + x), i & 1u, abort))) break;
+        tc_fence_after();
+        issue_s(kr);
+        last_bar = s_full;
+        last_par = (i + 1) & 1u;
+      }
       if (!(ok = wwait8(bars + 8 * (kVFull + vslot), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
       if (!(ok = wwait8(p_full, i & 1u, abort))) break;
       // A(0), B(0), A(1), ..: the tiles take turns, so that one's softmax runs
@@ -690,14 +727,14 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < kT / 16; ++s)
-          tc_mma_f16_ta(o_col, s_col + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, i > 0 || s > 0);
+          tc_mma_f16_ta(o_col, p_col + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, i > 0 || s > 0);
         tc_commit(pv_done);
         tc_commit(bars + 8 * (kVEmpty + vslot));
       }
       __syncwarp();
       last_bar = pv_done;
       last_par = i & 1u;
-      if (more) {
+      if (!own_p8<D>() && more) {
         // P lives in S's columns: the next scores follow the product that reads it
         if (!(ok = wwait8(pv_done, i & 1u, abort))) break;
         tc_fence_after();
@@ -733,8 +770,8 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const Prefill8Params
   const int b = (int)(tok / p.chunk), ti = (int)(tok % p.chunk);
   const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
   if (n < 0 || n > p.chunk || ti >= n) return;
-  // eight partials at a time, their loads in flight together
-  constexpr int kBatch = 8;
+  // twelve partials at a time, their loads in flight together
+  constexpr int kBatch = 12;
   float mx = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < p.parts; s0 += kBatch) {
