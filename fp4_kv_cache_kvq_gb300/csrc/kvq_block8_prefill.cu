@@ -22,13 +22,21 @@
 // 128-row tiles that share each 128-position cache tile; when few rows would
 // leave SMs idle, the positions are split over several CTAs too and a second
 // launch joins their partials.
-// Fourteen warps: softmax (2 x 4, thread = row), V expansion (4), loader (1),
-// MMA issue (1 thread), joined by mbarriers (every wait bounded):
+// Sixteen warps: softmax (2 x 4, thread = row), V expansion (4), loader (1), MMA
+// issue (one per query tile), joined by mbarriers (every wait bounded):
 //   loader    bulk copies of K codes, V codes and scales into rings of 3 tiles;
 //             the pool's K layout is the tensor core's operand layout
 //   MMA       S_X(j) = Qhi_X K(j)^T + Qlo_X K(j)^T   kind::f8f6f4
 //             O_X += P_X(j) V^(j)                    kind::f16, P_X from TMEM
-//             in the order O_A(j), S_A(j+1), O_B(j), S_B(j+1)
+//             the two tiles in turn: O_A(j), S_A(j+1), O_B(j), S_B(j+1)
+// Measured (1024 tokens over 16384 positions, 4 sequences, 64 query and 8 kv heads
+// of 128, page 64): 1.51 ms, 1.41 PFLOP/s, 0.74 of the bf16 GEMM rate.  From 2.09:
+// a row's scores in registers with the maxima that the TMEM load takes 1.99; the
+// issuing warp uniform 1.75; one issuing warp per query tile, in turns 1.67; the
+// running maximum raised only past 2^15 1.50.  The products alone (softmax and
+// expansion left out) take 1.38.  Slower: two threads per row 1.72; S of the next
+// tile started before O of this one's turn ends 1.58; P stored in halves with O
+// started on the first 1.57; P in a loop over TMEM instead of registers 1.58.
 #include "kvq_block8.cuh"
 #include "kvq_common.cuh"
 #include "kvq_host.cuh"
@@ -51,7 +59,11 @@ constexpr int kMWarp = kLdWarp + 1;
 constexpr int kP8Threads = 512;
 constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192 + 72 + 56 = 4 x 128
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * 128, "registers of the launch");
-constexpr int kOCol8 = kXTiles * kT;  // TMEM: S_X at [128 X, +128), O_X at [256 + d X, +d), P_X: p_col8
+// TMEM: S_X, then P_X, at [128 X, +128), O_X at [256 + 128 X, +d).  (At head_dim
+// 64 P_X fits beside S_X, and the next scores need not wait for the product that
+// reads it; but there the softmax is the bound: 1270 us so, 1254 like this, for a
+// chunk of 1024 over 16384 positions, 4 x 64 heads.)
+constexpr int kOCol8 = kXTiles * kT;
 constexpr int kTmem8 = 512;
 constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
 // The running maximum is raised only when a score passes it by this much (log2):
@@ -73,8 +85,7 @@ enum : int {
   kPFull = kSFull + kXTiles,       // [kXTiles] P_X in TMEM, O_X rescaled
   kPvDone = kPFull + kXTiles,      // [kXTiles] O_X += P_X V^ done
   kTurn = kPvDone + kXTiles,       // [kXTiles] query tile X's products may be issued
-  kSRead = kTurn + kXTiles,        // [kXTiles] S_X in the softmax's registers (head_dim 64)
-  kBars8 = kSRead + kXTiles
+  kBars8 = kTurn + kXTiles
 };
 
 struct Prefill8Params {
@@ -91,15 +102,6 @@ struct Prefill8Params {
   int32_t parts;   // partials per row: splits, or twice that for a pair
   float qk_log2;
 };
-
-// P_X's first column.  At head_dim 128 S and O fill the 512 columns, and P_X
-// takes the first half of S_X's, so that the next scores follow the product that
-// reads P_X.  At head_dim 64 it has columns of its own behind O: the next scores
-// are computed as soon as a tile's are in registers, beside its softmax.
-template <int D>
-__host__ __device__ constexpr bool own_p8() { return D == 64; }
-template <int D>
-__host__ __device__ constexpr int p_col8(int x) { return own_p8<D>() ? kOCol8 + kXTiles * D + x * (kT / 2) : x * kT; }
 
 template <int D>
 struct P8Geo {
@@ -321,7 +323,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kPFull + i), 4);
       mbar_init(bars + 8 * (kPvDone + i), 1);
       mbar_init(bars + 8 * (kTurn + i), 1);
-      mbar_init(bars + 8 * (kSRead + i), 4);
     }
     *abort = 0;
     *vref_bits = 0u;
@@ -465,8 +466,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     } else {
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t sp_col = t_lane + (uint32_t)(X * kT);
-      const uint32_t p_col = t_lane + (uint32_t)p_col8<D>(X);
-      const uint32_t op = t_lane + (uint32_t)(kOCol8 + X * D);
+      const uint32_t op = t_lane + (uint32_t)(kOCol8 + X * kT);
       const uint32_t s_full = bars + 8 * (kSFull + X), p_full = bars + 8 * (kPFull + X);
       const uint32_t pv_done = bars + 8 * (kPvDone + X);
       const int64_t pos_r = first + ti;  // last position this row attends
@@ -496,11 +496,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         tmem_wait_ld_all();
 #pragma unroll
         for (int i = 0; i < 8; ++i) after_wait(v[i], vm[i]);
-        if (own_p8<D>()) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + 8 * (kSRead + X));
-        }
         if (!fast) {
           // masked scores (behind the row's last position, or in a page that is
           // not valid) become -inf, their factor positive: 2^-inf is 0
@@ -527,10 +522,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
           m_run = mt;
         }
-        if (own_p8<D>() && i_own > 0) {  // the product that reads the previous P is done
-          if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
-          tc_fence_after();
-        }
         const float nref = m_run == -INFINITY ? 0.0f : -m_run;
         const uint64_t nref2 = pk2(nref, nref);
         uint64_t l2[2] = {0ull, 0ull};
@@ -539,7 +530,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           uint32_t w[16];
           block_p(v[i], w, csk[i], nref2, l2);
           block_p(v[i + 1], w + 8, csk[i + 1], nref2, l2);
-          tmem_st16_async(p_col + (uint32_t)(8 * i), w);
+          tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
         if (i_own > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
           if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
@@ -680,8 +671,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     const uint64_t dq = smem_desc(sb + G::kQ + (p.pair ? 0 : x) * 2 * G::kQBytes, 128, 8 * D);
     const uint64_t dk0 = smem_desc(sb + G::kK, 128, 8 * D);
     const uint64_t dv0 = smem_desc(sb + G::kV, (D / 8) * 128, 128);
-    const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * D);
-    const uint32_t p_col = tmem + (uint32_t)p_col8<D>(x);
+    const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * kT);
     const uint32_t s_full = bars + 8 * (kSFull + x), p_full = bars + 8 * (kPFull + x);
     const uint32_t pv_done = bars + 8 * (kPvDone + x);
     const auto issue_s = [&](int ring) {
@@ -705,18 +695,11 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       issue_s(j);
       last_bar = s_full;
     }
-    const bool turns = !own_p8<D>() && !p.pair && nx > 1;
+    const bool turns = !p.pair && nx > 1;
     for (uint32_t i = 0; j < ntiles && ok; j += step, ++i) {
       const int jn = j + step, kr = jn % kKRing, vslot = j % kVSlots8;
       const bool more = jn < ntiles;
       if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), (uint32_t)(jn / kKRing) & 1u, abort))) break;
-      if (own_p8<D>() && more) {
-        if (!(ok = wwait8(bars + 8 * (kSRead + x), i & 1u, abort))) break;
-        tc_fence_after();
-        issue_s(kr);
-        last_bar = s_full;
-        last_par = (i + 1) & 1u;
-      }
       if (!(ok = wwait8(bars + 8 * (kVFull + vslot), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
       if (!(ok = wwait8(p_full, i & 1u, abort))) break;
       // A(0), B(0), A(1), ..: the tiles take turns, so that one's softmax runs
@@ -727,14 +710,14 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < kT / 16; ++s)
-          tc_mma_f16_ta(o_col, p_col + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, i > 0 || s > 0);
+          tc_mma_f16_ta(o_col, s_col + (uint32_t)(s * 8), dv + (uint64_t)(s * 2 * (D / 8) * 8), kIdO, i > 0 || s > 0);
         tc_commit(pv_done);
         tc_commit(bars + 8 * (kVEmpty + vslot));
       }
       __syncwarp();
       last_bar = pv_done;
       last_par = i & 1u;
-      if (!own_p8<D>() && more) {
+      if (more) {
         // P lives in S's columns: the next scores follow the product that reads it
         if (!(ok = wwait8(pv_done, i & 1u, abort))) break;
         tc_fence_after();
