@@ -60,6 +60,12 @@ struct Decode8Params {
   int32_t out_bf16;
 };
 
+// Positions of sequence b: no more than its pages can hold (a longer length is
+// flagged where its last chunk is read).
+__device__ __forceinline__ int32_t walk_len(const Decode8Params& p, int b) {
+  return (int32_t)min((int64_t)__ldg(p.lens + b), (int64_t)p.c.max_pages_per_seq * p.c.page_size);
+}
+
 // Compile-time view of one group of GT tokens (see Block8Layout).
 template <int D, int GT>
 struct Grp8 {
@@ -154,7 +160,8 @@ __device__ void producer8(const Decode8Params& p, Smem8<D>& sm, Walker wk, int64
   for (; wk.v < v1; advance<C>(p, wk), ++it) {
     const uint32_t s = it % stages8<D>();
     const int64_t tok0 = (int64_t)wk.c * C;
-    const int ntok = (int)min((int64_t)C, __ldg(p.lens + wk.b) - tok0);
+    const int ntok = (int)min((int64_t)C, walk_len(p, wk.b) - tok0);
+    if (wk.c == wk.nch - 1 && lane == 0 && __ldg(p.lens + wk.b) > walk_len(p, wk.b)) set_flag(p.flag, KVQ_FLAG_PAGE_OOB);
     const int64_t pg0 = tok0 >> lg_p, pg1 = (tok0 + ntok - 1) >> lg_p;
     if (wk.b != wb || pg0 < w0 || pg1 >= w0 + 32) {
       if (wk.b == wb && pg0 == w0 + 32) {
@@ -443,7 +450,7 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
   if constexpr (DIRECT) {
     wk.b = (int)(blockIdx.x / (unsigned)p.hkv);
     wk.h = (int)(blockIdx.x % (unsigned)p.hkv);
-    const int32_t T = __ldg(p.lens + wk.b);
+    const int32_t T = walk_len(p, wk.b);
     wk.c = 0;
     wk.v = v0 = 0;
     total = v1 = wk.nch = fp4_chunks<chunk8<D>()>(T, 0);

@@ -109,6 +109,10 @@ struct Walker {
   int64_t v;  // index on the line
 };
 
+// Positions of sequence b that the walk covers (another decode's parameters
+// bring an overload of their own).
+__device__ __forceinline__ int32_t walk_len(const DecodeParams& p, int b) { return __ldg(p.lens + b); }
+
 // Every warp computes the same thing: the line's length and where range
 // `idx` of `count` equal ranges starts.  Lanes scan 32 sequences at a time.
 // CHUNK: tokens per chunk (the 8-bit cache's decode takes shorter ones).
@@ -121,7 +125,7 @@ __device__ __forceinline__ void plan(const Params& p, int idx, int count, int64_
   // pass 1: total
   for (int base = 0; base < p.batch; base += 32) {
     const int bb = base + lane;
-    int64_t x = bb < p.batch ? (int64_t)fp4_chunks<CHUNK>(__ldg(p.lens + bb), p.window) * p.hkv : 0;
+    int64_t x = bb < p.batch ? (int64_t)fp4_chunks<CHUNK>(walk_len(p, bb), p.window) * p.hkv : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
     acc += x;
@@ -140,7 +144,7 @@ __device__ __forceinline__ void plan(const Params& p, int idx, int count, int64_
   acc = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int bb = base + lane;
-    const int n = bb < p.batch ? fp4_chunks<CHUNK>(__ldg(p.lens + bb), p.window) : 0;
+    const int n = bb < p.batch ? fp4_chunks<CHUNK>(walk_len(p, bb), p.window) : 0;
     const int64_t x = (int64_t)n * p.hkv;
     int64_t incl = x;
 #pragma unroll
@@ -174,7 +178,7 @@ __device__ __forceinline__ void advance(const Params& p, Walker& wk) {
   wk.h = 0;
   do {
     ++wk.b;
-    wk.nch = wk.b < p.batch ? fp4_chunks<CHUNK>(__ldg(p.lens + wk.b), p.window) : 1;
+    wk.nch = wk.b < p.batch ? fp4_chunks<CHUNK>(walk_len(p, wk.b), p.window) : 1;
   } while (wk.nch == 0);
 }
 

@@ -95,7 +95,8 @@ kvq_status kvq_rope_table(int64_t num_positions, int32_t rotary_dim, double base
  *                num_q_heads * head_dim; otherwise disjoint from the inputs.
  *   k_out        device bf16 [batch][n_new][num_kv_heads][head_dim] or NULL:
  *                the rotated keys; as q_out.
- * Two sequences of one call must not write the same page.  Device flags:
+ * No page may be written through two entries of the page table in one call.
+ * Device flags:
  * NONFINITE, PAGE_OOB (the page's tokens are skipped), BAD_LENGTH (a negative
  * start, n_b outside 0..n_new: the sequence is skipped), POSITION (a position
  * past the table: the sequence's tokens from there on are left out).  Host

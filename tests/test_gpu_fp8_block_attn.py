@@ -388,3 +388,20 @@ def test_an_explicit_stream():
         dec = kvq.decode_attn(cache, n, q3, stream=side)
         side.synchronize()
         assert torch.equal(out, want) and torch.equal(dec, dwant)
+
+
+def test_lengths_far_past_the_pages_end_soon():
+    """A length of 2^31 - 1 reads what the pages hold, flags the rest and returns
+    at once, in every form of the kernels."""
+    for mp, page, B in ((2, 16, 1), (40, 64, 2), (600, 16, 1), (300, 16, 40)):
+        cap = mp * page
+        cache = build([cap] * B, 2, 128, page, seed=mp)
+        q = torch.randn((B, 8, 128), generator=_gen(3), device="cuda").to(BF)
+        want = kvq.decode_attn(cache, _ints([cap] * B), q)
+        far, err = _ints([2 ** 31 - 1] * B), _ints([0])
+        out = kvq.decode_attn(cache, far, q, err=err)
+        assert err.item() == kvq.FLAG_PAGE_OOB and torch.equal(out, want)
+        err = _ints([0])
+        pre = kvq.prefill_attn(cache, far, q[:, None].contiguous(), err=err)
+        assert err.item() == kvq.FLAG_PAGE_OOB
+        check(pre, q[:, None], cache, [cap] * B, [1] * B, 1 / math.sqrt(128), True)
