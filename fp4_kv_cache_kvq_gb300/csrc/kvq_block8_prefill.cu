@@ -513,12 +513,15 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
             if (cs != cs) csk[i] = cs;
           }
         }
-        float mt = -INFINITY;
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mt = fmaxf(mt, __uint_as_float(vm[i]) * csk[i]);
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(vm[i]) * csk[i];
+        const float mt = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
         // lazy reference: when it is raised, O and l shrink
         float al = 1.0f;
-        if (mt > m_run + kSlack8) {
+        const bool up = mt > m_run + kSlack8;
+        const bool any_up = __any_sync(0xFFFFFFFFu, up);  // (TMEM accesses are warp-collective)
+        if (any_up && up) {
           if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
           m_run = mt;
         }
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           block_p(v[i + 1], w + 8, csk[i + 1], nref2, l2);
           tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
-        if (i_own > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {  // TMEM accesses are warp-collective
+        if (any_up && i_own > 0) {
           if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
           tc_fence_after();
 #pragma unroll 1
