@@ -42,6 +42,8 @@
 #include "kvq_host.cuh"
 #include "kvq_tc.cuh"
 
+#include <type_traits>
+
 namespace kvq {
 namespace {
 
@@ -473,21 +475,14 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       float m_run = -INFINITY, l_run = 0.0f;
       bool ok = true;
       uint32_t i_own = 0;  // this half's tiles so far
-      for (int j = p.pair ? X : 0; j < ntiles; j += step, ++i_own) {
-        // the tile's K scales, ahead of its scores
-        const int ks = j % kKRing;
-        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kKRing) & 1u, abort))) break;
+      // One cache tile; MASKED: some of its scores are not attended.  Two bodies, so
+      // that the whole tiles' is one straight run of instructions.
+      const auto tile = [&](auto masked_c, int j, uint32_t good, const float (&csk_in)[8]) -> bool {
+        constexpr bool MASKED = decltype(masked_c)::value;
         float csk[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          csk[i] = cs * __uint_as_float(lds32(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, i)));
-        const uint32_t good = kgood[ks];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
-        const int64_t p0 = (int64_t)(j0 + j) * kT;
-        const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
-        const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
-        if (!(ok = wwait8(s_full, i_own & 1u, abort))) break;
+        for (int i = 0; i < 8; ++i) csk[i] = csk_in[i];
+        if (!wwait8(s_full, i_own & 1u, abort)) return false;
         tc_fence_after();
         // the row's 128 scores in registers, each block's maximum with them
         uint32_t v[8][16], vm[8];
@@ -496,7 +491,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         tmem_wait_ld_all();
 #pragma unroll
         for (int i = 0; i < 8; ++i) after_wait(v[i], vm[i]);
-        if (!fast) {
+        if constexpr (MASKED) {
+          const int64_t p0 = (int64_t)(j0 + j) * kT;
+          const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
           // masked scores (behind the row's last position, or in a page that is
           // not valid) become -inf, their factor positive: 2^-inf is 0
 #pragma unroll
@@ -536,22 +533,15 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
         if (any_up && i_own > 0) {
-          if (!(ok = wwait8(pv_done, (i_own - 1) & 1u, abort))) break;
+          if (!wwait8(pv_done, (i_own - 1) & 1u, abort)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 64) {
-            uint32_t oa[32], ob[32];
-            tmem_ld32_async(op + (uint32_t)c0, oa);
-            tmem_ld32_async(op + (uint32_t)c0 + 32u, ob);
-            tmem_wait_ld(oa);
-            tmem_wait_ld(ob);
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(op + (uint32_t)c0, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              oa[i] = __float_as_uint(__uint_as_float(oa[i]) * al);
-              ob[i] = __float_as_uint(__uint_as_float(ob[i]) * al);
-            }
-            tmem_st32_async(op + (uint32_t)c0, oa);
-            tmem_st32_async(op + (uint32_t)c0 + 32u, ob);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st32_async(op + (uint32_t)c0, o);
           }
         }
         tmem_wait_st();
@@ -562,6 +552,26 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         upk2(l2[0], a0, a1);
         upk2(l2[1], b0, b1);
         l_run = l_run * al + ((a0 + a1) + (b0 + b1));
+        return true;
+      };
+      for (int j = p.pair ? X : 0; j < ntiles; j += step, ++i_own) {
+        // the tile's K scales, ahead of its scores
+        const int ks = j % kKRing;
+        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kKRing) & 1u, abort))) break;
+        float csk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          csk[i] = cs * __uint_as_float(lds32(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, i)));
+        const uint32_t good = kgood[ks];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
+        const int64_t p0 = (int64_t)(j0 + j) * kT;
+        const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
+        if (fast)
+          ok = tile(std::false_type{}, j, good, csk);
+        else
+          ok = tile(std::true_type{}, j, good, csk);
+        if (!ok) break;
       }
       // the result once the last O_X += P_X V^ is done
       if (ok) ok = wwait8(pv_done, (i_own - 1) & 1u, abort);
