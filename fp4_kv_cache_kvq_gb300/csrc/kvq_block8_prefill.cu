@@ -102,6 +102,7 @@ struct Prefill8Params {
   int32_t batch, hkv, g, hq, chunk, splits, qpb, nqb, out_bf16;
   int32_t pair;    // few rows: both halves of the CTA serve one query tile, every second cache tile each
   int32_t parts;   // partials per row: splits, or twice that for a pair
+  uint32_t g_inv;  // 2^16 / g rounded up: row / g is row * g_inv >> 16 for rows < 512
   float qk_log2;
 };
 
@@ -116,7 +117,14 @@ struct P8Geo {
   static constexpr int kVS = kKS + kKRing * kScaleBytes;
   static constexpr int kBar = kVS + kVRing * kScaleBytes;
   static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, sV_ref bits, masks
-  static constexpr int kUsed = kMisc + 4 * (3 + kKRing + kVRing) + 128;
+  static constexpr int kMiscEnd = kMisc + 4 * (3 + kKRing + kVRing);
+  // where a half's rows are turned for coalesced stores: 128 bytes a row.  At
+  // head_dim 128 that is query memory that no product reads any more: the half's
+  // own tile's, for a pair the second tile's, which holds no queries
+  static constexpr int kStage = (kMiscEnd + 127) / 128 * 128;
+  static constexpr int kStageBytes = 128 * kRows;
+  static constexpr bool kStageInQ = kQBytes >= kStageBytes;
+  static constexpr int kUsed = (kStageInQ ? kMiscEnd : kStage + kXTiles * kStageBytes) + 128;
   // at least half an SM's shared memory, so that one CTA (holding all 512
   // TMEM columns) runs per SM
   static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
@@ -226,6 +234,17 @@ __device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, fl
   }
 }
 
+// A load that is issued where it stands.
+__device__ __forceinline__ uint4 ldg128_now(const void* ptr) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(ptr));
+  return r;
+}
+
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -257,6 +276,21 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   const int bh = rest / p.nqb;
   const int h = bh % p.hkv, b = bh / p.hkv;
   const int32_t T = __ldg(p.lens + b);
+  // the query rows' loads, in flight while the lengths are looked at
+  uint4 qv[4][D / 32];
+#pragma unroll
+  for (int rg = 0; rg < 4; ++rg) {
+    const int qr = (p.pair ? warp & 3 : warp) * 32 + 8 * rg + (lane >> 2);
+    const int qt = (int)((unsigned)qr * p.g_inv >> 16);  // qr / g
+    const int qti = qb * p.qpb + qt;
+    const bool in = warp < kSmWarps && qr < p.qpb * p.g && qti < p.chunk;
+    const uint16_t* src = p.q + (((int64_t)b * p.chunk + qti) * p.hq + h * p.g + qr - qt * p.g) * D + (lane & 3) * 8;
+#pragma unroll
+    for (int cg = 0; cg < D / 32; ++cg) {
+      qv[rg][cg] = make_uint4(0u, 0u, 0u, 0u);
+      if (in) qv[rg][cg] = ldg128_now(src + 32 * cg);
+    }
+  }
   const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
   if (n < 0 || n > p.chunk || T < 0) {
     if (tid == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
@@ -265,8 +299,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   if (qb * p.qpb >= n) return;  // padding only
   const int X = tid / kRows;                   // softmax threads: the half of the CTA,
   const int r = p.pair ? tid % kRows : tid;    // the row,
-  const int ti = qb * p.qpb + r / p.g;         // its query token and head
-  const int hh = h * p.g + r % p.g;
+  const int rt = (int)((unsigned)r * p.g_inv >> 16);  // r / g
+  const int ti = qb * p.qpb + rt;              // its query token and head
+  const int hh = h * p.g + r - rt * p.g;
   const bool row_ok = tid < kCtaRows8 && r < p.qpb * p.g && ti < n;
   const int part = p.pair ? 2 * sp + X : sp;   // which of the row's partials
   const int64_t row = ((int64_t)b * p.chunk + ti) * p.hq + hh;
@@ -331,26 +366,37 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
 
   const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
   const Block8Layout L(D, p.c.page_size);
   // The loader warp's copies of tile j: lane i < kGroups takes group i, K codes
-  // and scales, then V codes and scales.
+  // and scales, then V codes and scales.  The lanes look up the groups of 32 /
+  // kGroups tiles at once.
   int kiss = 0, viss = 0;
+  const uint8_t* src_l = nullptr;
   const auto load_tile = [&](int j) -> bool {
     const int ks = j % kKRing, vs = j % kVRing;
-    const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
-    const uint8_t* src = nullptr;
-    if (lane < kGroups && pos < limit) {
-      const int64_t phys = block8_page(p.c, b, pos, p.flag);
-      if (phys >= 0) {
-        const int64_t off = block8_group_offset(L, phys, p.hkv, h, (int)(pos & (p.c.page_size - 1)));
-        if (KVQ_IN(off >= 0 && off + kGroupBytes <= p.c.num_pages * (int64_t)p.hkv * L.page_bytes(), p.flag))
-          src = pool + off;
+    const int g_first = j % (32 / kGroups) * kGroups;
+    if (g_first == 0) {
+      const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
+      src_l = nullptr;
+      if (pos < limit && pos < (int64_t)(j0 + ntiles) * kT) {
+        const int64_t phys = block8_page(p.c, b, pos, p.flag);
+        if (phys >= 0) {
+          const int64_t off = block8_group_offset(L, phys, p.hkv, h, (int)(pos & (p.c.page_size - 1)));
+          if (KVQ_IN(off >= 0 && off + kGroupBytes <= p.c.num_pages * (int64_t)p.hkv * L.page_bytes(), p.flag))
+            src_l = pool + off;
+        }
       }
     }
-    const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr);
+    const uint32_t got = (__ballot_sync(0xFFFFFFFFu, src_l != nullptr) >> g_first) & ((1u << kGroups) - 1u);
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(
+        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src_l), (g_first + lane) & 31));
+    if (lane >= kGroups) src = nullptr;
     uint32_t good = 0u;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
@@ -382,84 +428,62 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     viss = j + 1;
     return true;
   };
-  constexpr int kAhead = kKRing < kVRing ? kKRing : kVRing;  // tiles that need no empty slot
-  if (warp == kLdWarp)
-    for (int j = 0; j < min(kAhead, ntiles); ++j) load_tile(j);
-
-  // sV_ref: the largest V scale of the positions this CTA reads (the other
-  // warps prepare the queries meanwhile)
-  if (warp >= kSmWarps) {
-    uint32_t best = 0u;
-    const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
-    for (int64_t gi = g0 + tid - 32 * kSmWarps; gi < g1; gi += kP8Threads - 32 * kSmWarps) {
-      const int64_t phys = block8_page(p.c, b, gi * GT, p.flag);
-      if (phys < 0) continue;
-      const uint8_t* grp = pool + block8_group_offset(L, phys, p.hkv, h, (int)((gi * GT) & (p.c.page_size - 1)));
+  if (warp < kSmWarps) {
+    // query rows: power-of-two prescale, hi and lo E4M3 parts in operand layout.
+    // Four lanes share a row's 16-byte parts (a thread per row would touch 32 lines
+    // a load), and a warp's stores are whole core matrices.
+    float cs;
+    const uint32_t dst = sb + G::kQ + X * 2 * G::kQBytes + (uint32_t)((warp & 3) * 32 * D + (lane >> 2) * 16);
+    uint32_t amax = 0u;  // of the thread's own row
+    int k_own = 0;
+    // (a loop, with the rows ahead moved down: the instructions of this part are
+    // fetched for one pass only)
+#pragma unroll 1
+    for (int rg = 0; rg < 4; ++rg) {
+      uint32_t am = 0u;
 #pragma unroll
-      for (int k = 0; k < GT / 16; ++k) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(grp + L.scale(k, 1)));
-        if (gi * GT + 16 * k < limit && v < 0x7F800000u) best = max(best, v);
+      for (int cg = 0; cg < D / 32; ++cg) {
+        const uint32_t ws[4] = {qv[0][cg].x, qv[0][cg].y, qv[0][cg].z, qv[0][cg].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = max(am, max((ws[i] << 16) & 0x7FFF0000u, ws[i] & 0x7FFF0000u));
       }
-    }
-    best = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (lane == 0 && best != 0u) atomicMax(vref_bits, best);
-  }
-
-  // query rows: power-of-two prescale, hi and lo E4M3 parts in operand layout
-  float cs = 0.0f;
-  if (warp < kSmWarps) {  // (one converged block: the prescan above is the other warps')
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
-    uint32_t amax = 0u;
-    if (row_ok) {
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = __ldg(src + i);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max((ws[k] << 16) & 0x7FFF0000u, ws[k] & 0x7FFF0000u));
-      }
-    }
-    int k = 0;
-    if (amax > 0u && amax < 0x7F800000u) k = min(100, max(-120, 7 - ((int)(amax >> 23) - 127)));
-    const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-    const uint32_t dst = sb + G::kQ + X * 2 * G::kQBytes + (uint32_t)(((tid % kRows) >> 3) * 8 * D + (tid & 7) * 16);
-#pragma unroll 2
-    for (int c16 = 0; c16 < D / 16; ++c16) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (row_ok) w = __ldg(src + 2 * c16 + half);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        uint32_t hp[4], lp[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = bf16_lo(ws[i]) * up, x1 = bf16_hi(ws[i]) * up;
-          hp[i] = e4m3x2_from_f32(x0, x1);
-          const float2 f = f16x2_to_float2(f16x2_from_e4m3x2(hp[i]));
-          lp[i] = e4m3x2_from_f32(x0 - f.x, x1 - f.y);
-        }
-        hi[2 * half] = hp[0] | (hp[1] << 16);
-        hi[2 * half + 1] = hp[2] | (hp[3] << 16);
-        lo[2 * half] = lp[0] | (lp[1] << 16);
-        lo[2 * half + 1] = lp[2] | (lp[3] << 16);
-      }
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      int k = 0;
+      if (am > 0u && am < 0x7F800000u) k = min(100, max(-120, 7 - ((int)(am >> 23) - 127)));
+      const float up = __uint_as_float((uint32_t)(k + 127) << 23);
       if (!p.pair || X == 0) {
-        sts128(dst + 128 * c16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(dst + G::kQBytes + 128 * c16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+        for (int cg = 0; cg < D / 32; ++cg) {
+          const uint32_t ws[4] = {qv[0][cg].x, qv[0][cg].y, qv[0][cg].z, qv[0][cg].w};
+          uint32_t hp[4], lp[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = bf16_lo(ws[i]) * up, x1 = bf16_hi(ws[i]) * up;
+            hp[i] = e4m3x2_from_f32(x0, x1);
+            const float2 f = f16x2_to_float2(f16x2_from_e4m3x2(hp[i]));
+            lp[i] = e4m3x2_from_f32(x0 - f.x, x1 - f.y);
+          }
+          const uint32_t at = dst + (uint32_t)(rg * 8 * D + (2 * cg + ((lane & 3) >> 1)) * 128 + (lane & 1) * 8);
+          sts64(at, hp[0] | (hp[1] << 16), hp[2] | (hp[3] << 16));
+          sts64(at + G::kQBytes, lp[0] | (lp[1] << 16), lp[2] | (lp[3] << 16));
+        }
       }
+      const uint32_t am_r = __shfl_sync(0xFFFFFFFFu, am, (lane & 7) * 4);
+      const int k_r = __shfl_sync(0xFFFFFFFFu, k, (lane & 7) * 4);
+      if (lane >> 3 == rg) {
+        amax = am_r;
+        k_own = k_r;
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int cg = 0; cg < D / 32; ++cg) qv[i][cg] = qv[i + 1][cg];
     }
-    cs = p.qk_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+    cs = p.qk_log2 * __uint_as_float((uint32_t)(127 - k_own) << 23);
     if (amax >= 0x7F800000u) cs = __uint_as_float(0x7FC00000u);  // Inf or NaN query: the row is NaN
     fence_async_smem();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
-  const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
-
-  if (warp < kSmWarps) {
+    asm volatile("bar.arrive 2, %0;\n" ::"r"(32 * (kSmWarps + nx)) : "memory");  // the MMA warps wait for the queries
     // ---------------------------------------------------------------- softmax
     reg_inc<kRegsSoftmax>();
     if (X >= nx) {  // a half without tiles
@@ -578,32 +602,61 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (ok) {
         tc_fence_after();
         const bool partial = p.parts > 1;
+        // (written before the expansion that this half's last product waited for)
+        const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
         const float f = partial ? vref : (l_run > 0.0f || l_run != l_run ? vref / l_run : 0.0f);
-        float* of = partial ? p.part_o + (part * rows_all + row) * D : static_cast<float*>(p.out) + row * D;
-        uint16_t* ob = static_cast<uint16_t*>(p.out) + row * D;
         if (partial && row_ok)
           *(reinterpret_cast<float2*>(p.part_ml) + part * rows_all + row) = make_float2(m_run, l_run);
+        // 128 bytes of every row at a time, turned in shared memory so that eight
+        // lanes store one row's (a thread per row would touch 32 lines a store)
+        const bool bf = p.out_bf16 && !partial;
+        const int64_t row0 = ((int64_t)b * p.chunk + qb * p.qpb) * p.hq + h * p.g;
+        const int rel_own = row_ok ? (int)(row - row0) : -1;
+        int rel[8];
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(op + (uint32_t)c0, o);
-          if (!row_ok) continue;
-          if (p.out_bf16 && !partial) {
+        for (int i = 0; i < 8; ++i) rel[i] = __shfl_sync(0xFFFFFFFFu, rel_own, 4 * i + (lane >> 3));
+        const uint32_t stage =
+            sb + (G::kStageInQ ? G::kQ + (p.pair ? 1 : X) * 2 * G::kQBytes : G::kStage) + X * G::kStageBytes +
+            (uint32_t)((warp & 3) * 32 * 128);
+        const uint32_t st_w = stage + (uint32_t)(lane * 128);
+        uint8_t* ob = partial ? reinterpret_cast<uint8_t*>(p.part_o + (part * rows_all + row0) * D)
+                              : static_cast<uint8_t*>(p.out) + row0 * D * (bf ? 2 : 4);
+        const int row_b = D * (bf ? 2 : 4);
+#pragma unroll 1
+        for (int c0 = 0; c0 < row_b; c0 += 128) {
+          if (bf) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t o[32];
+              tmem_ld32(op + (uint32_t)(c0 / 2 + 32 * half), o);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = bf16x2_of(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
-              *reinterpret_cast<uint4*>(ob + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = bf16x2_of(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
+                sts128(st_w + (uint32_t)(((4 * half + i) ^ (lane & 7)) * 16), make_uint4(w[0], w[1], w[2], w[3]));
+              }
             }
           } else {
+            uint32_t o[32];
+            tmem_ld32(op + (uint32_t)(c0 / 4), o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(of + c0 + i) =
-                  make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f,
-                              __uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * f);
+              sts128(st_w + (uint32_t)((i ^ (lane & 7)) * 16), make_uint4(w[0], w[1], w[2], w[3]));
+            }
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3);
+            const uint4 w = lds128(stage + (uint32_t)(rr * 128 + (((lane & 7) ^ (rr & 7)) * 16)));
+            if (rel[i] >= 0) *reinterpret_cast<uint4*>(ob + (int64_t)rel[i] * row_b + c0 + (lane & 7) * 16) = w;
+          }
+          __syncwarp();
         }
       }
     }
@@ -614,6 +667,25 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // stores touch 128 contiguous bytes per eight lanes
     reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
+    // sV_ref: the largest V scale of the positions this CTA reads; the first
+    // scores are on their way meanwhile
+    uint32_t best = 0u;
+    const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
+#pragma unroll 2
+    for (int64_t gi = g0 + dt; gi < g1; gi += 32 * kExpWarps) {
+      const int64_t phys = block8_page(p.c, b, gi * GT, p.flag);
+      if (phys < 0) continue;
+      const uint8_t* grp = pool + block8_group_offset(L, phys, p.hkv, h, (int)((gi * GT) & (p.c.page_size - 1)));
+#pragma unroll
+      for (int k = 0; k < GT / 16; ++k) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(grp + L.scale(k, 1)));
+        if (gi * GT + 16 * k < limit && v < 0x7F800000u) best = max(best, v);
+      }
+    }
+    best = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (lane == 0 && best != 0u) atomicMax(vref_bits, best);
+    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kExpWarps) : "memory");
+    const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
     const float vinv = vref > 0.0f ? 1.0f / vref : 0.0f;
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kVRing, slot = j % kVSlots8;
@@ -623,10 +695,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (j >= kVSlots8 && !wwait8(bars + 8 * (kVEmpty + slot), (uint32_t)(j / kVSlots8 - 1) & 1u, abort)) break;
       const uint32_t good = vgood[s];
       const bool whole = valid == kT && good == 0xFFu;
+      const uint32_t c = dt % D;
 #pragma unroll 1
-      for (int it = dt; it < D * (kT / 16); it += 32 * kExpWarps) {
-        const int c = it % D, blk = it / D;
-        uint4 w = lds128(codes + (uint32_t)((blk * D + c) * 16));
+      for (int blk = dt / D; blk < kT / 16; blk += 32 * kExpWarps / D) {
+        uint4 w = lds128(codes + ((uint32_t)(blk * D) + c) * 16);
         const float r = __uint_as_float(lds32(scale_at<GT>(sb + G::kVS + s * kScaleBytes, blk) + 4)) * vinv;
         uint32_t r2 = pack_f16x2(r, r);
         uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -644,7 +716,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           lo[t] = hmul2_u32(f16x2_from_e4m3x2(ws[t] & 0xFFFFu), r2);
           hi[t] = hmul2_u32(f16x2_from_e4m3x2(ws[t] >> 16), r2);
         }
-        const uint32_t at = dst + core_offset((uint32_t)c, (uint32_t)(16 * blk), D);
+        const uint32_t at = dst + core_offset(c, (uint32_t)(16 * blk), D);
         sts128(at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         sts128(at + (D / 8) * 128, make_uint4(hi[0], hi[1], hi[2], hi[3]));
       }
@@ -657,7 +729,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
    reg_dec<kRegsIssue>();
    if (warp == kLdWarp) {
     // ------------------------------------------------------------ bulk copies
-    for (int j = kAhead; j < ntiles; ++j)
+    for (int j = 0; j < ntiles; ++j)
       if (!load_tile(j)) break;
     if (*abort) {  // copies still in flight land before the shared memory goes away
       const auto drain = [&](int bar, int ring, int issued) {
@@ -702,6 +774,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     };
     uint32_t last_bar = 0, last_par = 0;
     int j = p.pair ? x : 0;              // this half's first tile (x < nx <= ntiles for a pair)
+    asm volatile("bar.sync 2, %0;\n" ::"r"(32 * (kSmWarps + nx)) : "memory");  // the queries are written
     bool ok = wwait8(bars + 8 * (kKFull + j), 0u, abort);
     if (ok) {
       tc_fence_after();
@@ -923,6 +996,7 @@ extern "C" kvq_status kvq_fp8_block_prefill_attn(const kvq_cache* cache, int32_t
   pp.batch = batch;
   pp.hkv = hkv;
   pp.g = g;
+  pp.g_inv = (65536u + (unsigned)g - 1) / (unsigned)g;
   pp.hq = num_q_heads;
   pp.chunk = chunk;
   pp.splits = splits;
