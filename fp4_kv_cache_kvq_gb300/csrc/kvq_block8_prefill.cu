@@ -245,6 +245,22 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_from_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(v));
+  return r;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // Four lanes share a row's 16-byte parts (a thread per row would touch 32 lines
     // a load), and a warp's stores are whole core matrices.
     float cs;
-    const uint32_t dst = sb + G::kQ + X * 2 * G::kQBytes + (uint32_t)((warp & 3) * 32 * D + (lane >> 2) * 16);
+    const uint32_t dst = sb + G::kQ + (p.pair ? 0 : X) * 2 * G::kQBytes + (uint32_t)((warp & 3) * 32 * D + (lane >> 2) * 16);
     uint32_t amax = 0u;  // of the thread's own row
     int k_own = 0;
     // (a loop, with the rows ahead moved down: the instructions of this part are
@@ -445,24 +461,26 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       for (int cg = 0; cg < D / 32; ++cg) {
         const uint32_t ws[4] = {qv[0][cg].x, qv[0][cg].y, qv[0][cg].z, qv[0][cg].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) am = max(am, max((ws[i] << 16) & 0x7FFF0000u, ws[i] & 0x7FFF0000u));
+        for (int i = 0; i < 4; ++i) am = max_u16x2(am, ws[i] & 0x7FFF7FFFu);
       }
+      am = max(am << 16, am & 0xFFFF0000u);
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
       int k = 0;
       if (am > 0u && am < 0x7F800000u) k = min(100, max(-120, 7 - ((int)(am >> 23) - 127)));
       const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-      if (!p.pair || X == 0) {
+      if (!p.pair || X == rg >> 1) {  // (the halves of a pair prepare half of the rows each)
 #pragma unroll
         for (int cg = 0; cg < D / 32; ++cg) {
           const uint32_t ws[4] = {qv[0][cg].x, qv[0][cg].y, qv[0][cg].z, qv[0][cg].w};
           uint32_t hp[4], lp[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x0 = bf16_lo(ws[i]) * up, x1 = bf16_hi(ws[i]) * up;
-            hp[i] = e4m3x2_from_f32(x0, x1);
-            const float2 f = f16x2_to_float2(f16x2_from_e4m3x2(hp[i]));
-            lp[i] = e4m3x2_from_f32(x0 - f.x, x1 - f.y);
+            // f16 holds the scaled values exactly down to 2^-17, where both parts are
+            // zero, and their difference from hi
+            const uint32_t x = pack_f16x2(bf16_lo(ws[i]) * up, bf16_hi(ws[i]) * up);
+            hp[i] = e4m3x2_from_f16x2(x);
+            lp[i] = e4m3x2_from_f16x2(hsub2_u32(x, f16x2_from_e4m3x2(hp[i])));
           }
           const uint32_t at = dst + (uint32_t)(rg * 8 * D + (2 * cg + ((lane & 3) >> 1)) * 128 + (lane & 1) * 8);
           sts64(at, hp[0] | (hp[1] << 16), hp[2] | (hp[3] << 16));
