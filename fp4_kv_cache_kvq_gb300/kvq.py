@@ -404,9 +404,10 @@ def append(cache, start_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:
     """kvq_rope_table: float32 [num_positions][rotary_dim], of each position
     the rotary_dim/2 cosines, then the sines."""
-    table = torch.empty((num_positions, rotary_dim), dtype=torch.float32, device=device)
-    if table.device.index != torch.cuda.current_device():
-        raise ValueError(f"device {table.device} is not the current one")
+    where, dev = torch.device(device), torch.cuda.current_device()
+    if where.type != "cuda" or where.index not in (None, dev):
+        raise ValueError(f"device {where} is not the current one, cuda:{dev}")
+    table = _alloc(stream, (num_positions, rotary_dim), torch.float32, dev)
     _check(load().kvq_rope_table(num_positions, rotary_dim, float(base), _ptr(table), _stream(stream)),
            "kvq_rope_table")
     return table

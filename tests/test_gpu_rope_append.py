@@ -154,6 +154,24 @@ def test_rope_table(base, rd):
     assert (t[:, rd // 2:] - ang.sin()).abs().max() <= 2.0 ** -24
 
 
+def test_a_table_on_an_explicit_stream():
+    """Memory that was freed for the current stream while a kernel on it still
+    writes there does not become the table of a call on another stream."""
+    want = kvq.rope_table(40000, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy = torch.empty((40000, 128), device="cuda")
+        for _ in range(50):
+            busy.fill_(7.0)
+        del busy
+        got = kvq.rope_table(40000, 128, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        side.synchronize()
+        del got
+
+
 CASES = [  # d, rotary, interleaved, heads, group, n, starts
     (128, 128, False, 2, 8, 5, [0, 77, 1000]),
     (128, 128, True, 1, 3, 17, [3, 0, 30]),
