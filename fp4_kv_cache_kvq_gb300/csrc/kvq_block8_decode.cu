@@ -274,8 +274,9 @@ __device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int sl, 
   const float ks = __uint_as_float(sc.x), vs = __uint_as_float(sc.y);
 
   // S^T = K Q^T: 16 tokens x 16 channels per step; matrices (tokens 0-7,
-  // 8-15) x (channel block, the next one)
-  float S[4] = {0.f, 0.f, 0.f, 0.f};
+  // 8-15) x (channel block, the next one).  Two chains of products, as one of
+  // eight in a row is the longest wait of a slice (16 x 8192: 48.4 -> 48.1 us)
+  float S[4] = {0.f, 0.f, 0.f, 0.f}, S2[4] = {0.f, 0.f, 0.f, 0.f};
   const uint32_t ka = grp + (uint32_t)((2 * blk + ((lane >> 3) & 1)) * 8 * D + (lane >> 4) * 128 + (lane & 7) * 16);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -284,8 +285,10 @@ __device__ __forceinline__ void consume8(State8<D>& st, uint32_t stage, int sl, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) f16x2x2_from_e4m3x4(r[j], a[2 * j], a[2 * j + 1]);
     mma_f16_16816(S, a[0], a[2], a[1], a[3], st.qf[4 * i], st.qf[4 * i + 1]);
-    mma_f16_16816(S, a[4], a[6], a[5], a[7], st.qf[4 * i + 2], st.qf[4 * i + 3]);
+    mma_f16_16816(S2, a[4], a[6], a[5], a[7], st.qf[4 * i + 2], st.qf[4 * i + 3]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) S[i] += S2[i];
   const float c0 = st.cs[0] * ks, c1 = st.cs[1] * ks;
   float y0 = S[0] * c0, y1 = S[1] * c1, y2 = S[2] * c0, y3 = S[3] * c1;
   if (PARTIAL) {
