@@ -30,13 +30,21 @@
 //             O_X += P_X(j) V^(j)                    kind::f16, P_X from TMEM
 //             the two tiles in turn: O_A(j), S_A(j+1), O_B(j), S_B(j+1)
 // Measured (1024 tokens over 16384 positions, 4 sequences, 64 query and 8 kv heads
-// of 128, page 64): 1.51 ms, 1.41 PFLOP/s, 0.74 of the bf16 GEMM rate.  From 2.09:
+// of 128, page 64): 1.46 ms, 1.46 PFLOP/s, 0.76 of the bf16 GEMM rate.  From 2.09:
 // a row's scores in registers with the maxima that the TMEM load takes 1.99; the
 // issuing warp uniform 1.75; one issuing warp per query tile, in turns 1.67; the
-// running maximum raised only past 2^15 1.50.  The products alone (softmax and
-// expansion left out) take 1.38.  Slower: two threads per row 1.72; S of the next
-// tile started before O of this one's turn ends 1.58; P stored in halves with O
-// started on the first 1.57; P in a loop over TMEM instead of registers 1.58.
+// running maximum raised only past 2^15 1.52; queries read by four lanes a row and
+// results stored through shared memory (a thread per row touches 32 lines an
+// access), and no CTA-wide wait before the first product 1.46 (4096 tokens over
+// nothing, 2 sequences: 548 -> 480 us).
+// Per tile of both query tiles 2980 cycles, 2048 of them products: each query
+// tile's chain is P V^ 890, S 890 (512 and a wait each), softmax 1090, and the other
+// tile's fills the gaps.
+// Slower: two threads per row 1.72; S of the next tile started before O of this
+// one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
+// loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
+// 64 columns, the second beside P V^ 1.56 (against 1.46: an MMA of 64 columns reads
+// as much of the queries as one of 128).
 #include "kvq_block8.cuh"
 #include "kvq_common.cuh"
 #include "kvq_host.cuh"
@@ -63,15 +71,15 @@ constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * 128, "registers of the launch");
 // TMEM: S_X, then P_X, at [128 X, +128), O_X at [256 + 128 X, +d).  (At head_dim
 // 64 P_X fits beside S_X, and the next scores need not wait for the product that
-// reads it; but there the softmax is the bound: 1270 us so, 1254 like this, for a
-// chunk of 1024 over 16384 positions, 4 x 64 heads.)
+// reads it; but there the softmax is the bound: 1 % slower for a chunk of 1024 over
+// 16384 positions, 4 x 64 heads.)
 constexpr int kOCol8 = kXTiles * kT;
 constexpr int kTmem8 = 512;
 constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
 // The running maximum is raised only when a score passes it by this much (log2):
 // f16 holds 2^15, and among 32 rows with heavy-tailed scores a smaller slack has
 // some row raise it on every few tiles (prefill of 1024 over 16384 positions,
-// 4 x 64 heads: 8 1552 us, 12 1523, 15 1503).
+// 4 x 64 heads: 8 1529 us, 12 1488, 15 1459).
 constexpr float kSlack8 = 15.0f;
 constexpr uint32_t kPoll8 = 20000;
 constexpr int kScaleBytes = 128;  // scales of one tile: up to 8 groups of 16 bytes
@@ -910,7 +918,7 @@ int prefill_splits(int64_t ctas, int sms) {
 
 // The chunk's rows of one kv head fit one query tile: a CTA's two halves then
 // share it and take every second cache tile each (a draft of 5 tokens x 8 heads
-// over 9000 to 12345 positions, 2 sequences: 28.2 us against 31.4).
+// over 9000 to 12345 positions, 2 sequences: 25.2 us against 28.6).
 bool one_tile(int32_t chunk, int g) { return (int64_t)chunk * g <= kRows; }
 
 size_t part_bytes(int64_t parts, int64_t rows, int d) {
