@@ -413,21 +413,22 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, devic
     return table
 
 
-def _token_stride(dev: int, t: torch.Tensor, name: str) -> int:
+def _token_stride(dev: int, t: torch.Tensor, name: str):
     """Elements from one token to the next of a bf16 [batch][n][heads][d] tensor
     whose tokens' values are contiguous and evenly spaced (a contiguous tensor,
-    or a part of a packed projection)."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.dim() != 4:
+    or a part of a packed projection), and its shape."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or len(shape) != 4:
         raise ValueError(f"{name} must be a bfloat16 tensor [batch, n_new, heads, head_dim] on cuda:{dev}")
-    B, n, H, d = t.shape
+    B, n, H, d = shape
     if t.is_contiguous():
-        return H * d
+        return H * d, shape
     sb, sn, sh, sd = t.stride()
     step = sn if n > 1 else sb
     if t.numel() and not ((sd == 1 or d == 1) and (H == 1 or sh == d) and step >= H * d and
                           (n == 1 or B == 1 or sb == n * sn)):
         raise ValueError(f"{name}: the values of a token must be contiguous and the tokens evenly spaced")
-    return step
+    return step, shape
 
 
 def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -445,22 +446,22 @@ def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: to
     if not isinstance(cache, (Fp4Cache, Fp8BlockCache)):
         raise ValueError("rope_append needs an Fp4Cache or Fp8BlockCache (append k_out to a window ring)")
     dev = _device(cache)
-    ks, vs = _token_stride(dev, k, "k"), _token_stride(dev, v, "v")
-    shape = k.shape
+    (ks, shape), (vs, v_shape) = _token_stride(dev, k, "k"), _token_stride(dev, v, "v")
     B, n, hkv, d = shape
-    if shape != v.shape or hkv != cache.num_kv_heads or d != cache.head_dim:
+    if shape != v_shape or hkv != cache.num_kv_heads or d != cache.head_dim:
         raise ValueError("k and v must have shape [batch, n_new, num_kv_heads, head_dim]")
     hq = qs = 0
     q_ptr = out_ptr = None
     if q is not None:
-        qs, hq = _token_stride(dev, q, "q"), q.shape[2]
-        if q.shape != (B, n, hq, d):
+        qs, q_shape = _token_stride(dev, q, "q")
+        hq = q_shape[2]
+        if q_shape[0] != B or q_shape[1] != n or q_shape[3] != d:
             raise ValueError("q must have shape [batch, n_new, num_q_heads, head_dim]")
         if q_out is None:
-            q_out = _alloc(stream, q.shape, torch.bfloat16, dev)
+            q_out = _alloc(stream, q_shape, torch.bfloat16, dev)
         else:
             _on(dev, q_out, torch.bfloat16, "q_out")
-            if q_out.shape != q.shape:
+            if q_out.shape != q_shape:
                 raise ValueError("q_out must have q's shape")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -541,15 +542,15 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
 _OUT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _attn_out(dev: int, cache, q: torch.Tensor, out: Optional[torch.Tensor], padded: bool, stream):
-    """(out, its KVQ_DTYPE_*) of an attention over an Fp8BlockCache."""
+def _attn_out(dev: int, cache, q: torch.Tensor, shape, out: Optional[torch.Tensor], padded: bool, stream):
+    """(out, its KVQ_DTYPE_*) of an attention over an Fp8BlockCache; shape: q's."""
     _on(dev, q, torch.bfloat16, "q")
-    if q.shape[-1] != cache.head_dim:
+    if shape[-1] != cache.head_dim:
         raise ValueError("q must have the cache's head_dim")
     if out is None:  # rows of a padded batch's padding are not written
-        out = _alloc(stream, q.shape, torch.float32, dev, zero=padded)
+        out = _alloc(stream, shape, torch.float32, dev, zero=padded)
     code = _OUT_DTYPES.get(out.dtype)
-    if code is None or out.get_device() != dev or not out.is_contiguous() or out.shape != q.shape:
+    if code is None or out.get_device() != dev or not out.is_contiguous() or out.shape != shape:
         raise ValueError("out must be a contiguous float32 or bfloat16 tensor of q's shape on the cache's device")
     return out, code
 
@@ -564,10 +565,11 @@ def _workspace(dev: int, workspace: Optional[torch.Tensor], stream, need, *sizes
 
 def _decode_block8(cache, seq_lens, q, softmax_scale, out, workspace, err, stream) -> torch.Tensor:
     dev = _device(cache)
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must have shape [batch, num_q_heads, head_dim]")
-    out, code = _attn_out(dev, cache, q, out, False, stream)
-    B, hq, d = q.shape
+    out, code = _attn_out(dev, cache, q, shape, out, False, stream)
+    B, hq, d = shape
     _per_seq(dev, seq_lens, B, "seq_lens")
     _table_rows(dev, cache, None, B)
     ws = _workspace(dev, workspace, stream, decode_workspace_bytes, B, hq, cache.num_kv_heads, d)
@@ -614,10 +616,11 @@ def prefill_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, hea
 
 def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace) -> torch.Tensor:
     dev = _device(cache)
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must have shape [batch, chunk, num_q_heads, head_dim]")
-    out, code = _attn_out(dev, cache, q, out, chunk_lens is not None, stream)
-    B, chunk, hq, d = q.shape
+    out, code = _attn_out(dev, cache, q, shape, out, chunk_lens is not None, stream)
+    B, chunk, hq, d = shape
     _per_seq(dev, seq_lens, B, "seq_lens")
     if chunk_lens is not None:
         _per_seq(dev, chunk_lens, B, "chunk_lens")
