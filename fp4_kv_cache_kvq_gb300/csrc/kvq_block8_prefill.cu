@@ -108,7 +108,6 @@ struct Prefill8Params {
   float* part_ml;  // [parts][batch * chunk * hq][2]
   int32_t* flag;
   int32_t batch, hkv, g, hq, chunk, splits, qpb, nqb, out_bf16;
-  int32_t pair;    // few rows: both halves of the CTA serve one query tile, every second cache tile each
   int32_t parts;   // partials per row: splits, or twice that for a pair
   uint32_t g_inv;  // 2^16 / g rounded up: row / g is row * g_inv >> 16 for rows < 512
   float qk_log2;
@@ -276,9 +275,15 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-template <int D, int GT>
+// PAIR: few rows: both halves of the CTA serve one query tile, every second cache
+// tile each.
+template <int D, int GT, bool PAIR>
 __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Prefill8Params p) {
   using G = P8Geo<D>;
+  // K slots in use.  A pair's half sees every second tile only: with two slots it
+  // waits on the same barrier phase after phase.  (With three it would skip phases,
+  // and could take a tile that is still on its way for the one before.)
+  constexpr int kRing = PAIR ? 2 : kKRing;
   constexpr int kGroups = kT / GT;
   constexpr int kGroupBytes = 2 * GT * D + (GT >= 32 ? GT / 2 : 16);
   constexpr int kGroupScale = GT >= 32 ? GT / 2 : 16;
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   uint4 qv[4][D / 32];
 #pragma unroll
   for (int rg = 0; rg < 4; ++rg) {
-    const int qr = (p.pair ? warp & 3 : warp) * 32 + 8 * rg + (lane >> 2);
+    const int qr = (PAIR ? warp & 3 : warp) * 32 + 8 * rg + (lane >> 2);
     const int qt = (int)((unsigned)qr * p.g_inv >> 16);  // qr / g
     const int qti = qb * p.qpb + qt;
     const bool in = warp < kSmWarps && qr < p.qpb * p.g && qti < p.chunk;
@@ -322,12 +327,12 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   }
   if (qb * p.qpb >= n) return;  // padding only
   const int X = tid / kRows;                   // softmax threads: the half of the CTA,
-  const int r = p.pair ? tid % kRows : tid;    // the row,
+  const int r = PAIR ? tid % kRows : tid;    // the row,
   const int rt = (int)((unsigned)r * p.g_inv >> 16);  // r / g
   const int ti = qb * p.qpb + rt;              // its query token and head
   const int hh = h * p.g + r - rt * p.g;
   const bool row_ok = tid < kCtaRows8 && r < p.qpb * p.g && ti < n;
-  const int part = p.pair ? 2 * sp + X : sp;   // which of the row's partials
+  const int part = PAIR ? 2 * sp + X : sp;   // which of the row's partials
   const int64_t row = ((int64_t)b * p.chunk + ti) * p.hq + hh;
   const int64_t rows_all = (int64_t)p.batch * p.chunk * p.hq;
   if (T < n) {  // the chunk's own tokens must be in the cache
@@ -358,9 +363,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   const int per = (tiles + p.splits - 1) / p.splits;
   const int j0 = min(tiles, sp * per), ntiles = min(tiles, j0 + per) - j0;
   const int rows_used = (last_ti - qb * p.qpb + 1) * p.g;
-  const int nx = p.pair ? min(2, ntiles) : rows_used > kRows ? 2 : 1;  // halves with work
-  const int users = p.pair ? 1 : nx;                // halves that read one cache tile
-  const int step = p.pair ? 2 : 1;
+  const int nx = PAIR ? min(2, ntiles) : rows_used > kRows ? 2 : 1;  // halves with work
+  const int users = PAIR ? 1 : nx;                // halves that read one cache tile
+  const int step = PAIR ? 2 : 1;
   if (ntiles <= 0) {                                // a split without positions
     if (row_ok) *(reinterpret_cast<float2*>(p.part_ml) + part * rows_all + row) = make_float2(-INFINITY, 0.0f);
     return;
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   int kiss = 0, viss = 0;
   const uint8_t* src_l = nullptr;
   const auto load_tile = [&](int j) -> bool {
-    const int ks = j % kKRing, vs = j % kVRing;
+    const int ks = j % kRing, vs = j % kVRing;
     const int g_first = j % (32 / kGroups) * kGroups;
     if (g_first == 0) {
       const int64_t pos = (int64_t)(j0 + j) * kT + lane * GT;
@@ -426,7 +431,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     for (int i = 0; i < kGroups; ++i)
       if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
     const uint32_t bytes = (uint32_t)__popc(got) * (uint32_t)(GT * D + kGroupScale);
-    if (j >= kKRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kKRing - 1) & 1u, abort)) return false;
+    if (j >= kRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kRing - 1) & 1u, abort)) return false;
     if (lane == 0) {
       kgood[ks] = good;
       mbar_arrive_expect_tx(bars + 8 * (kKFull + ks), bytes);
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // Four lanes share a row's 16-byte parts (a thread per row would touch 32 lines
     // a load), and a warp's stores are whole core matrices.
     float cs;
-    const uint32_t dst = sb + G::kQ + (p.pair ? 0 : X) * 2 * G::kQBytes + (uint32_t)((warp & 3) * 32 * D + (lane >> 2) * 16);
+    const uint32_t dst = sb + G::kQ + (PAIR ? 0 : X) * 2 * G::kQBytes + (uint32_t)((warp & 3) * 32 * D + (lane >> 2) * 16);
     uint32_t amax = 0u;  // of the thread's own row
     int k_own = 0;
     // (a loop, with the rows ahead moved down: the instructions of this part are
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       int k = 0;
       if (am > 0u && am < 0x7F800000u) k = min(100, max(-120, 7 - ((int)(am >> 23) - 127)));
       const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-      if (!p.pair || X == rg >> 1) {  // (the halves of a pair prepare half of the rows each)
+      if (!PAIR || X == rg >> 1) {  // (the halves of a pair prepare half of the rows each)
 #pragma unroll
         for (int cg = 0; cg < D / 32; ++cg) {
           const uint32_t ws[4] = {qv[0][cg].x, qv[0][cg].y, qv[0][cg].z, qv[0][cg].w};
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // ---------------------------------------------------------------- softmax
     reg_inc<kRegsSoftmax>();
     if (X >= nx) {  // a half without tiles
-      if (p.pair && row_ok)
+      if (PAIR && row_ok)
         *(reinterpret_cast<float2*>(p.part_ml) + part * rows_all + row) = make_float2(-INFINITY, 0.0f);
     } else {
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -604,10 +609,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         l_run = l_run * al + ((a0 + a1) + (b0 + b1));
         return true;
       };
-      for (int j = p.pair ? X : 0; j < ntiles; j += step, ++i_own) {
+      for (int j = PAIR ? X : 0; j < ntiles; j += step, ++i_own) {
         // the tile's K scales, ahead of its scores
-        const int ks = j % kKRing;
-        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kKRing) & 1u, abort))) break;
+        const int ks = j % kRing;
+        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u, abort))) break;
         float csk[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 #pragma unroll
         for (int i = 0; i < 8; ++i) rel[i] = __shfl_sync(0xFFFFFFFFu, rel_own, 4 * i + (lane >> 3));
         const uint32_t stage =
-            sb + (G::kStageInQ ? G::kQ + (p.pair ? 1 : X) * 2 * G::kQBytes : G::kStage) + X * G::kStageBytes +
+            sb + (G::kStageInQ ? G::kQ + (PAIR ? 1 : X) * 2 * G::kQBytes : G::kStage) + X * G::kStageBytes +
             (uint32_t)((warp & 3) * 32 * 128);
         const uint32_t st_w = stage + (uint32_t)(lane * 128);
         uint8_t* ob = partial ? reinterpret_cast<uint8_t*>(p.part_o + (part * rows_all + row0) * D)
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           }
         }
       };
-      drain(kKFull, kKRing, kiss);
+      drain(kKFull, kRing, kiss);
       drain(kV8Full, kVRing, viss);
     }
    } else if (warp - kMWarp < nx) {
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     constexpr uint32_t kIdS = idesc_f16_f32(kRows, kT);  // E4M3 is type 0 of kind::f8f6f4, as f16 is of kind::f16
     constexpr uint32_t kIdO = idesc_f16_f32(kRows, D);
     const int x = warp - kMWarp;
-    const uint64_t dq = smem_desc(sb + G::kQ + (p.pair ? 0 : x) * 2 * G::kQBytes, 128, 8 * D);
+    const uint64_t dq = smem_desc(sb + G::kQ + (PAIR ? 0 : x) * 2 * G::kQBytes, 128, 8 * D);
     const uint64_t dk0 = smem_desc(sb + G::kK, 128, 8 * D);
     const uint64_t dv0 = smem_desc(sb + G::kV, (D / 8) * 128, 128);
     const uint32_t s_col = tmem + (uint32_t)(x * kT), o_col = tmem + (uint32_t)(kOCol8 + x * kT);
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       __syncwarp();
     };
     uint32_t last_bar = 0, last_par = 0;
-    int j = p.pair ? x : 0;              // this half's first tile (x < nx <= ntiles for a pair)
+    int j = PAIR ? x : 0;              // this half's first tile (x < nx <= ntiles for a pair)
     asm volatile("bar.sync 2, %0;\n" ::"r"(32 * (kSmWarps + nx)) : "memory");  // the queries are written
     bool ok = wwait8(bars + 8 * (kKFull + j), 0u, abort);
     if (ok) {
@@ -807,11 +812,11 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       issue_s(j);
       last_bar = s_full;
     }
-    const bool turns = !p.pair && nx > 1;
+    const bool turns = !PAIR && nx > 1;
     for (uint32_t i = 0; j < ntiles && ok; j += step, ++i) {
-      const int jn = j + step, kr = jn % kKRing, vslot = j % kVSlots8;
+      const int jn = j + step, kr = jn % kRing, vslot = j % kVSlots8;
       const bool more = jn < ntiles;
-      if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), (uint32_t)(jn / kKRing) & 1u, abort))) break;
+      if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), (uint32_t)(jn / kRing) & 1u, abort))) break;
       if (!(ok = wwait8(bars + 8 * (kVFull + vslot), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
       if (!(ok = wwait8(p_full, i & 1u, abort))) break;
       // A(0), B(0), A(1), ..: the tiles take turns, so that one's softmax runs
@@ -925,18 +930,18 @@ size_t part_bytes(int64_t parts, int64_t rows, int d) {
   return parts > 1 ? (size_t)parts * (size_t)rows * (size_t)(d + 2) * sizeof(float) : 16;
 }
 
-template <int D, int GT>
+template <int D, int GT, bool PAIR>
 kvq_status launch_prefill8(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
   static DeviceOnce attr_set;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
   if (attr_set.pending(dev)) {
-    if (cudaFuncSetAttribute(prefill_block8_kernel<D, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(prefill_block8_kernel<D, GT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              P8Geo<D>::kBytes) != cudaSuccess)
       return KVQ_ERR_CUDA;
     attr_set.mark(dev);
   }
-  prefill_block8_kernel<D, GT><<<grid, kP8Threads, P8Geo<D>::kBytes, s>>>(pp);
+  prefill_block8_kernel<D, GT, PAIR><<<grid, kP8Threads, P8Geo<D>::kBytes, s>>>(pp);
   const kvq_status st = launch_status();
   if (st != KVQ_OK || pp.parts == 1) return st;
   const int64_t rows = (int64_t)pp.batch * pp.chunk * pp.hq;
@@ -952,12 +957,12 @@ kvq_status launch_prefill8(const Prefill8Params& pp, cudaStream_t s, unsigned gr
   return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, pp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
-template <int D>
+template <int D, bool PAIR>
 kvq_status launch_prefill8_d(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
   switch (pp.c.page_size) {
-    case 16: return launch_prefill8<D, 16>(pp, s, grid);
-    case 32: return launch_prefill8<D, 32>(pp, s, grid);
-    default: return launch_prefill8<D, 64>(pp, s, grid);
+    case 16: return launch_prefill8<D, 16, PAIR>(pp, s, grid);
+    case 32: return launch_prefill8<D, 32, PAIR>(pp, s, grid);
+    default: return launch_prefill8<D, 64, PAIR>(pp, s, grid);
   }
 }
 
@@ -1015,7 +1020,6 @@ extern "C" kvq_status kvq_fp8_block_prefill_attn(const kvq_cache* cache, int32_t
   pp.q = static_cast<const uint16_t*>(q);
   pp.out = out;
   pp.part_o = static_cast<float*>(workspace);
-  pp.pair = pair ? 1 : 0;
   pp.parts = splits * (pair ? 2 : 1);
   pp.part_ml = pp.part_o + (size_t)pp.parts * rows * D;
   pp.flag = d_err_flag;
@@ -1032,5 +1036,6 @@ extern "C" kvq_status kvq_fp8_block_prefill_attn(const kvq_cache* cache, int32_t
   pp.qk_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)(ctas * splits);
-  return D == 128 ? launch_prefill8_d<128>(pp, s, grid) : launch_prefill8_d<64>(pp, s, grid);
+  if (pair) return D == 128 ? launch_prefill8_d<128, true>(pp, s, grid) : launch_prefill8_d<64, true>(pp, s, grid);
+  return D == 128 ? launch_prefill8_d<128, false>(pp, s, grid) : launch_prefill8_d<64, false>(pp, s, grid);
 }
