@@ -30,13 +30,13 @@
 //             O_X += P_X(j) V^(j)                    kind::f16, P_X from TMEM
 //             the two tiles in turn: O_A(j), S_A(j+1), O_B(j), S_B(j+1)
 // Measured (1024 tokens over 16384 positions, 4 sequences, 64 query and 8 kv heads
-// of 128, page 64): 1.46 ms, 1.46 PFLOP/s, 0.76 of the bf16 GEMM rate.  From 2.09:
+// of 128, page 64): 1.43 ms, 1.49 PFLOP/s, 0.78 of the bf16 GEMM rate.  From 2.09:
 // a row's scores in registers with the maxima that the TMEM load takes 1.99; the
 // issuing warp uniform 1.75; one issuing warp per query tile, in turns 1.67; the
 // running maximum raised only past 2^15 1.52; queries read by four lanes a row and
 // results stored through shared memory (a thread per row touches 32 lines an
-// access), and no CTA-wide wait before the first product 1.46 (4096 tokens over
-// nothing, 2 sequences: 548 -> 480 us).
+// access), and no CTA-wide wait before the first product 1.46; a kernel of its own
+// for pairs 1.43 (4096 tokens over nothing, 2 sequences: 548 -> 469 us).
 // Per tile of both query tiles 2980 cycles, 2048 of them products: each query
 // tile's chain is P V^ 890, S 890 (512 and a wait each), softmax 1090, and the other
 // tile's fills the gaps.
@@ -44,7 +44,9 @@
 // one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
 // loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
 // 64 columns, the second beside P V^ 1.56 (against 1.46: an MMA of 64 columns reads
-// as much of the queries as one of 128).
+// as much of the queries as one of 128); one CTA per SM that works off an equal
+// share of all tiles, with partials where a share ends inside a block, 1.57; the
+// queries as bulk copies to V^'s place 1.45 (both against 1.43).
 #include "kvq_block8.cuh"
 #include "kvq_common.cuh"
 #include "kvq_host.cuh"
@@ -71,7 +73,7 @@ constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * 128, "registers of the launch");
 // TMEM: S_X, then P_X, at [128 X, +128), O_X at [256 + 128 X, +d).  (At head_dim
 // 64 P_X fits beside S_X, and the next scores need not wait for the product that
-// reads it; but there the softmax is the bound: 1 % slower for a chunk of 1024 over
+// reads it; but there the softmax is the bound: 1% slower for a chunk of 1024 over
 // 16384 positions, 4 x 64 heads.)
 constexpr int kOCol8 = kXTiles * kT;
 constexpr int kTmem8 = 512;
