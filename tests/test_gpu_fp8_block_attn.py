@@ -159,6 +159,13 @@ def test_prefill_chunk_lengths(n, lens):
     prefill(lens, n, 1, 1, 64, 16, seed=n + 1, dtype=BF)
 
 
+@pytest.mark.parametrize("d,G,page,n", [(128, 8, 64, 5), (64, 3, 16, 40), (128, 1, 32, 128), (64, 8, 256, 1)])
+def test_prefill_few_rows_over_many_tiles(d, G, page, n):
+    """More (sequence, head) units than SMs: one CTA walks all of a unit's tiles, from
+    one to 21, with its two halves at every second one."""
+    lens = [max(n, x) for x in (1, 127, 128, 129, 256, 257, 385, 512, 640, 641, 900, 1024, 1300, 2001, 2600)] * 3
+    prefill(lens, n, 4, G, d, page, seed=n, ragged=[n - i % min(n, 3) for i in range(len(lens))])
+
 def test_prefill_without_a_split():
     """A grid larger than the GPU: one CTA walks all positions of its rows."""
     prefill([900, 650], 640, 8, 8, 128, 64, seed=21)
