@@ -220,16 +220,23 @@ struct State8 {
   float cs[2], m[2], l[2];
 };
 
+// A unit's query rows, loaded ahead of the last unit's flush (which hides them).
 template <int D>
-__device__ __forceinline__ void begin_unit8(const Decode8Params& p, State8<D>& st, int b, int h) {
+__device__ __forceinline__ void load_rows8(const Decode8Params& p, uint2 (&w)[D / 16], int b, int h) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t qrow = (int64_t)b * p.hq + (int64_t)h * p.g + g;
   const bool row = g < p.g && KVQ_IN(qrow < (int64_t)p.batch * p.hq, p.flag);
-  uint2 w[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    w[i] = row ? __ldcg(reinterpret_cast<const uint2*>(p.q + qrow * D + 16 * i + 4 * t)) : make_uint2(0u, 0u);
+}
+
+template <int D>
+__device__ __forceinline__ void begin_unit8(const Decode8Params& p, State8<D>& st, const uint2 (&w)[D / 16]) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
   uint32_t amax = 0u;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    w[i] = row ? __ldcg(reinterpret_cast<const uint2*>(p.q + qrow * D + 16 * i + 4 * t)) : make_uint2(0u, 0u);
     amax = max(amax, max(max((w[i].x << 16) & 0x7FFF0000u, w[i].x & 0x7FFF0000u),
                          max((w[i].y << 16) & 0x7FFF0000u, w[i].y & 0x7FFF0000u)));
   }
@@ -516,10 +523,12 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
   uint32_t it = 0;
   for (; wk.v < v1; advance<chunk8<D>()>(p, wk), ++it) {
     if (!have || wk.c == 0) {
+      uint2 rows[D / 16];
+      load_rows8<D>(p, rows, wk.b, wk.h);
       if (!DIRECT && have) flush_unit8<D, DIRECT>(p, st, sm, slot);
       const int64_t u = (int64_t)wk.b * p.hkv + wk.h;
       slot = DIRECT ? u * p.g : u + blockIdx.x;  // (u * g: the unit's first output row)
-      begin_unit8<D>(p, st, wk.b, wk.h);
+      begin_unit8<D>(p, st, rows);
       have = true;
       if (!DIRECT && wk.c == 0 && threadIdx.x == 0) {
         const int64_t last_cta = (wk.v + wk.nch - 1) / per;
