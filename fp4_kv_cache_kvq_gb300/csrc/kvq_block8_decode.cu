@@ -383,6 +383,11 @@ __device__ void flush_unit8(const Decode8Params& p, State8<D>& st, Smem8<D>& sm,
     st.l[0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[0], o);
     st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
   }
+  // scores that were all NaN raised no maximum: a finite one keeps their NaN sums
+  // from counting as empty
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (st.l[i] != st.l[i] && st.m[i] == -INFINITY) st.m[i] = 0.0f;
   named_barrier_sync(1, 32 * kB8Warps);  // the previous flush has been read
   float* ow = sm.flush_o + warp * kNG * D;
 #pragma unroll

@@ -296,6 +296,24 @@ def test_nonfinite_queries_stay_in_their_rows():
         assert torch.equal(dec[0, keep], dgood[0, keep])
 
 
+@pytest.mark.parametrize("lens", [[16, 40], [3, 9000]])
+def test_nan_keys_reach_their_rows(lens):
+    """A sequence whose keys are all NaN gives NaN, also where a warp or a range has
+    seen no other score; the other sequence stays as it is."""
+    H, G, d = 2, 4, 128
+    cache = build(lens, H, d, 64, seed=21)
+    q = torch.randn((2, H * G, d), generator=_gen(22), device="cuda").to(BF)
+    want = kvq.decode_attn(cache, _ints(lens), q)
+    pre = kvq.prefill_attn(cache, _ints(lens), q[:, None].contiguous())
+    err = _ints([0])
+    nan = torch.full((2, lens[0], H, d), float("nan"), dtype=BF, device="cuda")
+    kvq.append(cache, _ints([0, 0]), nan, torch.ones_like(nan), new_lens=_ints([lens[0], 0]), err=err)
+    assert err.item() == kvq.FLAG_NONFINITE
+    out = kvq.decode_attn(cache, _ints(lens), q)
+    assert out[0].isnan().all() and torch.equal(out[1], want[1])
+    out = kvq.prefill_attn(cache, _ints(lens), q[:, None].contiguous())
+    assert out[0].isnan().all() and torch.equal(out[1], pre[1])
+
 def test_decode_and_prefill_agree_and_repeat():
     lens = [1000, 77, 129]
     cache = build(lens, 2, 128, 64, seed=5)
