@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kTurn + i), 1);
     }
     *abort = 0;
-    *vref_bits = 0u;
+    *vref_bits = 0x00800000u;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
@@ -700,8 +700,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // stores touch 128 contiguous bytes per eight lanes
     reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
-    // sV_ref: the largest V scale of the positions this CTA reads; the first
-    // scores are on their way meanwhile
+    // sV_ref: the largest V scale of the positions this CTA reads, or 2^-126 (the
+    // append's smallest), whose reciprocal is finite, when all are smaller; the
+    // first scores are on their way meanwhile
     uint32_t best = 0u;
     const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
 #pragma unroll 2
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     if (lane == 0 && best != 0u) atomicMax(vref_bits, best);
     asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kExpWarps) : "memory");
     const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
-    const float vinv = vref > 0.0f ? 1.0f / vref : 0.0f;
+    const float vinv = 1.0f / vref;
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kVRing, slot = j % kVSlots8;
       const uint32_t codes = sb + G::kV8 + s * kT * D, dst = sb + G::kV + slot * kT * D * 2;

@@ -1,0 +1,80 @@
+"""Values of extreme scales in the 8-bit block cache's attention, against float64
+with each row's own bound (tests/attn_bounds.py)."""
+import math
+
+import pytest
+import torch
+
+from fp4_kv_cache_kvq_gb300 import kvq
+from tests import attn_bounds
+from tests.helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_built()
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def scales(cache):
+    """The scales' view [pages][heads][groups][G / 16][2] of the pool."""
+    g, d = cache.group, cache.head_dim
+    s = cache.pool[..., 2 * g * d:2 * g * d + max(16, g // 2)].view(torch.float32)
+    return s.view(*s.shape[:-1], -1, 2)[..., :g // 16, :]
+
+
+def filled(T, H, d, page, seed=0):
+    """A contiguous cache of one sequence of T random tokens."""
+    mp = -(-T // page)
+    cache = kvq.Fp8BlockCache(H, d, page, mp, mp)
+    k, v = (torch.randn((1, T, H, d), generator=_gen(seed + i), device="cuda").to(BF) for i in range(2))
+    kvq.append(cache, _ints([0]), k, v)
+    return cache
+
+
+def value_scales(cache, T):
+    """[T][H] of a contiguous cache of one sequence."""
+    s = scales(cache)[..., 1]                              # [pages][H][groups][G/16]
+    return s.permute(0, 2, 3, 1).reshape(-1, s.shape[1]).repeat_interleave(16, 0)[:T]
+
+
+def check(cache, T, q, out, last, v_rel=0.0, floor=0.0, prefill=True):
+    """out, q [n][Hq][d]: within the bound of the row, or `floor`."""
+    n, hq, d = q.shape
+    g, scale = hq // cache.num_kv_heads, 1.0 / math.sqrt(d)
+    K, V = kvq.dequant(cache, _ints([T]), T)
+    vs = value_scales(cache, T)
+    for h in range(cache.num_kv_heads):
+        rows = slice(h * g, (h + 1) * g)
+        want, p = attn_bounds.attend(q[:, rows], K[0, :, h], V[0, :, h], scale, last)
+        tol = attn_bounds.bound(q[:, rows], K[0, :, h], V[0, :, h], p, scale, vs[:, h] if prefill else None,
+                                out.dtype, want, v_rel) + floor
+        off = (out[:, rows].double() - want).abs()
+        assert (off <= tol).all(), (h, (off / tol).nan_to_num(math.inf).max().item())
+
+
+@pytest.mark.parametrize("d,n", [(64, 5), (128, 5), (128, 150)])
+@pytest.mark.parametrize("exponent", [-126, -128, -130, -140])
+def test_tiny_value_scales(d, n, exponent):
+    """The readers take any finite scale: all values of a cache next to and among
+    fp32's subnormals."""
+    T, H = 300, 2
+    cache = filled(T, H, d, 64, seed=1)
+    scales(cache)[..., 1] = 2.0 ** exponent
+    q = torch.randn((1, n, 4 * H, d), generator=_gen(3), device="cuda").to(BF)
+    out = kvq.prefill_attn(cache, _ints([T]), q)
+    # half steps of fp32's subnormals: of a value, of each of the T / 16 sums, of a join and the result
+    floor = (T / 16 + 3) * 2.0 ** -150
+    check(cache, T, q[0], out[0], torch.arange(T - n, T), floor=floor)
+    dec = kvq.decode_attn(cache, _ints([T]), q[:, -1].contiguous())
+    check(cache, T, q[0, -1:], dec, torch.tensor([T - 1]), floor=floor, prefill=False)
