@@ -4,18 +4,24 @@
 //
 // Mathematics.  Query token i of n sits at position T - n + i and attends
 // 0 .. T - n + i.  With one K and one V scale per 16 positions,
-//   S = q . code_K,  y = S (softmax_scale log2 e sK),  P = 2^(y - m),
-//   O = sum P (sV / sV_ref) code_V,  out = sV_ref O / sum P.
+//   S = q . code_K,  y = S (softmax_scale log2 e sK),  P = 2^(y + log2 sV - m'),
+//   O = sum P code_V,  l = sum P / sV,  out = O / l.
 // S takes the cached K codes as they are: q, scaled per row by a power of two
 // to [2^7, 2^8), is the sum of two E4M3 values hi = RNE(q) and lo = q - hi
 // (a bf16 value has 8 significant bits and an E4M3 value 4; lo is exact down
 // to 2^-10 of the row's largest element and off by at most 2^-18 of it under
 // that), so S = hi . K + lo . K are two fp8 products, which together cost one
-// f16 product and need no expansion of K.  V is expanded to f16 with sV/sV_ref
-// (sV_ref the largest V scale of the CTA's positions: the ratio is a power of
-// two <= 1, so the product is exact down to 2^-24), and P is rounded to f16
-// (2^-11 relative): f16 keeps the weights finer than an fp8 P could.
-// Accumulation, maxima and sums are fp32.
+// f16 product and need no expansion of K.  The V scale of a block goes into P's
+// exponent, beside the softmax's own, so V^ is the codes themselves (exact in
+// f16; a scale that is no power of two leaves its significand, [1, 2), to V^,
+// rounded to f16 there).  P is rounded to f16: 2^-11 relative, or 2^-25 of 2^m',
+// where m' runs over the largest y + log2 sV that the row has attended.  So what
+// a row loses is measured by what it attends itself, and no value behind its last
+// position, however large, reaches it.  l takes P's fp32 value back to 2^(y - m),
+// m a second reference, with one factor per block: weights on blocks of tiny values
+// count in l although their P rounds to 0 (the exponent that V adds is held at -60
+// and up for that, far under what f16 sees).  Both references are whole numbers, so
+// every sum of exponents is exact.  Accumulation, maxima and sums are fp32.
 //
 // What bounds it: the tensor pipe, 4 Hq d flop per attended pair.  Work split:
 // a CTA takes 256 query rows (G heads x 256/G tokens) of one kv head as two
@@ -23,7 +29,7 @@
 // leave SMs idle, the positions are split over several CTAs too and a second
 // launch joins their partials.
 // Sixteen warps: softmax (2 x 4, thread = row), V expansion (4), loader (1), MMA
-// issue (one per query tile), joined by mbarriers (every wait bounded):
+// issue (one per query tile), scales (1), joined by mbarriers (every wait bounded):
 //   loader    bulk copies of K codes, V codes and scales into rings of 3 tiles;
 //             the pool's K layout is the tensor core's operand layout
 //   MMA       S_X(j) = Qhi_X K(j)^T + Qlo_X K(j)^T   kind::f8f6f4
@@ -39,7 +45,11 @@
 // for pairs 1.43 (4096 tokens over nothing, 2 sequences: 548 -> 469 us).
 // Per tile of both query tiles 2980 cycles, 2048 of them products: each query
 // tile's chain is P V^ 890, S 890 (512 and a wait each), softmax 1090, and the other
-// tile's fills the gaps.
+// tile's fills the gaps.  V's scales in P's exponent instead of a factor relative to
+// the largest of the CTA's positions: 1407 -> 1450 us (head_dim 64: 1200 -> 1224);
+// what follows from the scales alone is computed ahead of the scores, by one warp for
+// all rows where it does not depend on the row (1493 behind the scores, 1466 by every
+// row).
 // Slower: two threads per row 1.72; S of the next tile started before O of this
 // one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
 // loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
@@ -65,8 +75,9 @@ constexpr int kSmWarps = 4 * kXTiles;
 constexpr int kExpWarps = 4;
 constexpr int kLdWarp = kSmWarps + kExpWarps;
 constexpr int kMWarp = kLdWarp + 1;
+constexpr int kScWarp = kMWarp + kXTiles;
 // four warpgroups, so that registers can move between them: the loader's and
-// the MMA issuer's group (two of its warps idle) and the expansion leave theirs
+// the MMA issuers' group and the expansion leave theirs
 // to the softmax, which holds a row's 128 scores at once
 constexpr int kP8Threads = 512;
 constexpr int kRegsSoftmax = 192, kRegsExpand = 72, kRegsIssue = 56;  // 2 x 192 + 72 + 56 = 4 x 128
@@ -83,13 +94,21 @@ constexpr int kKRing = 3, kVRing = 3, kVSlots8 = 2;
 // some row raise it on every few tiles (prefill of 1024 over 16384 positions,
 // 4 x 64 heads: 8 1529 us, 12 1488, 15 1459).
 constexpr float kSlack8 = 15.0f;
+// log2 of P over 2^(y - m): from kMinFactor up in P, to kMaxFactor in l (where more
+// makes the weight one under 2^-105).
+constexpr float kMinFactor = -60.0f, kMaxFactor = 120.0f;
+// m is raised when it is this far under a score beside a held exponent, and once l
+// has grown to kMaxSum; between, l counts what m lags.
+constexpr float kIntBias = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the integer
+constexpr float kSlackSum = 4.0f, kMaxSum = 1073741824.0f;  // 2^30
 constexpr uint32_t kPoll8 = 20000;
 constexpr int kScaleBytes = 128;  // scales of one tile: up to 8 groups of 16 bytes
 
 enum : int {
   kKFull = 0,                      // [kKRing] K codes and scales landed
   kKEmpty = kKFull + kKRing,       // [kKRing] S products done (commit), softmax warps have the scales
-  kV8Full = kKEmpty + kKRing,      // [kVRing] V codes and scales landed
+  kScFull = kKEmpty + kKRing,      // [kKRing] the tile's scales as the softmax takes them
+  kV8Full = kScFull + kKRing,      // [kVRing] V codes and scales landed
   kV8Empty = kV8Full + kVRing,     // [kVRing] expanded (one arrival per warp)
   kVFull = kV8Empty + kVRing,      // [kVSlots8] V^ slot written
   kVEmpty = kVFull + kVSlots8,     // [kVSlots8] O products done with it (commit)
@@ -106,8 +125,8 @@ struct Prefill8Params {
   kvq_cache c;
   const uint16_t* q;
   void* out;
-  float* part_o;   // [parts][batch * chunk * hq][D] when parts > 1
-  float* part_ml;  // [parts][batch * chunk * hq][2]
+  float* part_o;   // [parts][batch * chunk * hq][D] when parts > 1: a part's own result O / l
+  float* part_ml;  // [parts][batch * chunk * hq][2]: its m and l
   int32_t* flag;
   int32_t batch, hkv, g, hq, chunk, splits, qpb, nqb, out_bf16;
   int32_t parts;   // partials per row: splits, or twice that for a pair
@@ -124,9 +143,12 @@ struct P8Geo {
   static constexpr int kV = kV8 + kVRing * kT * D;       // [kVSlots8][D][128] f16
   static constexpr int kKS = kV + kVSlots8 * kT * D * 2;
   static constexpr int kVS = kKS + kKRing * kScaleBytes;
-  static constexpr int kBar = kVS + kVRing * kScaleBytes;
-  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, sV_ref bits, masks
-  static constexpr int kMiscEnd = kMisc + 4 * (3 + kKRing + kVRing);
+  // [2 kKRing][8] (sK, log2 sV): a tile's are read until the tile one K ring later
+  // has been taken
+  static constexpr int kSc = kVS + kVRing * kScaleBytes;
+  static constexpr int kBar = kSc + 2 * kKRing * 64;
+  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, (unused), masks, exponents
+  static constexpr int kMiscEnd = kMisc + 4 * (3 + 2 * kKRing + kVRing);
   // where a half's rows are turned for coalesced stores: 128 bytes a row.  At
   // head_dim 128 that is query memory that no product reads any more: the half's
   // own tile's, for a pair the second tile's, which holds no queries
@@ -228,19 +250,32 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-// P = 2^(S csk - m) for the 16 scores of a block as 8 f16 pairs, their sum
-// into l2.
-__device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, float csk, uint64_t nref2,
-                                        uint64_t (&l2)[2]) {
-  const uint64_t cs2 = pk2(csk, csk);
+// P = 2^(S csk + c) for the 16 scores of a block as 8 f16 pairs; their sum times
+// f into l2.
+__device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, float csk, float c, float f,
+                                        uint64_t& l2) {
+  const uint64_t cs2 = pk2(csk, csk), c2 = pk2(c, c);
+  uint64_t sum = 0ull;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float y0, y1;
-    upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cs2, nref2), y0, y1);
+    upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cs2, c2), y0, y1);
     const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
-    l2[i & 1] = add2(l2[i & 1], pk2(e0, e1));
+    sum = i == 0 ? pk2(e0, e1) : add2(sum, pk2(e0, e1));
     w[i] = pack_f16x2(e0, e1);
   }
+  l2 = fma2(sum, pk2(f, f), l2);
+}
+
+// The part of a V scale that goes into P's exponent: 2^e = its power of two, with
+// e from -126 (fp32's subnormals keep the rest in the significand) to 120 (where
+// the rest times a code stays an f16 value for every finite product).
+__device__ __forceinline__ uint32_t v_exponent(uint32_t bits) { return min(max(bits >> 23, 1u), 247u); }
+// e as a float, from v_exponent's biased form
+__device__ __forceinline__ float v_log2(uint32_t e) { return __uint_as_float(0x4B000000u | e) - (8388608.0f + 127.0f); }
+// the rest, sV / 2^e
+__device__ __forceinline__ float v_rest(uint32_t bits) {
+  return __uint_as_float(bits) * __uint_as_float((254u - v_exponent(bits)) << 23);
 }
 
 // A load that is issued where it stands.
@@ -296,9 +331,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
   uint32_t* tslot = misc;
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
-  uint32_t* vref_bits = misc + 2;
   volatile uint32_t* kgood = misc + 3;             // [kKRing] bit i: block i of the tile lies in a valid page
   volatile uint32_t* vgood = misc + 3 + kKRing;    // [kVRing]
+  volatile uint32_t* emin = misc + 3 + kKRing + kVRing;  // [kKRing] the smallest log2 sV of the tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int sp = (int)(blockIdx.x % (unsigned)p.splits);
@@ -377,6 +412,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     for (int i = 0; i < kKRing; ++i) {
       mbar_init(bars + 8 * (kKFull + i), 1);
       mbar_init(bars + 8 * (kKEmpty + i), 5 * users);
+      mbar_init(bars + 8 * (kScFull + i), 1);
     }
     for (int i = 0; i < kVRing; ++i) {
       mbar_init(bars + 8 * (kV8Full + i), 1);
@@ -393,7 +429,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kTurn + i), 1);
     }
     *abort = 0;
-    *vref_bits = 0x00800000u;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
@@ -529,12 +564,26 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       const uint32_t s_full = bars + 8 * (kSFull + X), p_full = bars + 8 * (kPFull + X);
       const uint32_t pv_done = bars + 8 * (kPvDone + X);
       const int64_t pos_r = first + ti;  // last position this row attends
-      float m_run = -INFINITY, l_run = 0.0f;
+      float m_run = -INFINITY, mv_run = -INFINITY, l_run = 0.0f;  // m, m', l
       bool ok = true;
       uint32_t i_own = 0;  // this half's tiles so far
+      // A block's exponent in P, beside y, and its factor in l, both from log2 sV and
+      // the references.
+      const auto factors = [&](const float (&lv)[8], float (&pc)[8], float (&pf)[8]) {
+        const float mo = m_run == -INFINITY ? 0.0f : m_run;
+        const float dm = mo - (mv_run == -INFINITY ? 0.0f : mv_run);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = fmaxf(lv[i] + dm, kMinFactor);
+          pc[i] = a - mo;
+          // 2^-a of a whole number, no less than 2^-kMaxFactor
+          pf[i] = __uint_as_float(__float_as_uint(fmaxf(kIntBias + 127.0f - a, kIntBias + 127.0f - kMaxFactor)) << 23);
+        }
+      };
       // One cache tile; MASKED: some of its scores are not attended.  Two bodies, so
       // that the whole tiles' is one straight run of instructions.
-      const auto tile = [&](auto masked_c, int j, uint32_t good, const float (&csk_in)[8]) -> bool {
+      const auto tile = [&](auto masked_c, int j, uint32_t good, const float (&csk_in)[8], uint32_t sc,
+                            float (&pc)[8], float (&pf)[8], bool held) -> bool {
         constexpr bool MASKED = decltype(masked_c)::value;
         float csk[8];
 #pragma unroll
@@ -567,26 +616,42 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
             if (cs != cs) csk[i] = cs;
           }
         }
-        float y[8];
+        float y[8];  // y + log2 sV - m'
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(vm[i]) * csk[i];
-        const float mt = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-        // lazy reference: when it is raised, O and l shrink
-        float al = 1.0f;
-        const bool up = mt > m_run + kSlack8;
-        const bool any_up = __any_sync(0xFFFFFFFFu, up);  // (TMEM accesses are warp-collective)
-        if (any_up && up) {
-          if (m_run != -INFINITY) al = fast_exp2(m_run - mt);
-          m_run = mt;
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(__uint_as_float(vm[i]), csk[i], pc[i]);
+        const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+        // lazy references: when m' is raised O shrinks, when m is l does
+        float al = 1.0f, al_l = 1.0f;
+        bool any_up = false;  // (TMEM accesses are warp-collective)
+        if (__any_sync(0xFFFFFFFFu, top > (mv_run == -INFINITY ? -INFINITY : kSlack8)) || held) {
+          float mt = -INFINITY, mv = -INFINITY, lv[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = __uint_as_float(vm[i]) * csk[i];
+            lv[i] = __uint_as_float(lds32(sc + 8 * i + 4));
+            mt = fmaxf(mt, x);
+            mv = fmaxf(mv, x + lv[i]);
+          }
+          const bool up = mv > mv_run + kSlack8;
+          any_up = __any_sync(0xFFFFFFFFu, up);
+          if (up) {
+            const float to = ceilf(mv);
+            if (mv_run != -INFINITY) al = fast_exp2(mv_run - to);
+            mv_run = to;
+          }
+          if (mt > m_run + kSlackSum) {
+            const float to = ceilf(mt);
+            if (m_run != -INFINITY) al_l = fast_exp2(m_run - to);
+            m_run = to;
+          }
+          factors(lv, pc, pf);
         }
-        const float nref = m_run == -INFINITY ? 0.0f : -m_run;
-        const uint64_t nref2 = pk2(nref, nref);
         uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           uint32_t w[16];
-          block_p(v[i], w, csk[i], nref2, l2);
-          block_p(v[i + 1], w + 8, csk[i + 1], nref2, l2);
+          block_p(v[i], w, csk[i], pc[i], pf[i], l2[0]);
+          block_p(v[i + 1], w + 8, csk[i + 1], pc[i + 1], pf[i + 1], l2[1]);
           tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
         if (any_up && i_own > 0) {
@@ -608,26 +673,39 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         float a0, a1, b0, b1;
         upk2(l2[0], a0, a1);
         upk2(l2[1], b0, b1);
-        l_run = l_run * al + ((a0 + a1) + (b0 + b1));
+        l_run = l_run * al_l + ((a0 + a1) + (b0 + b1));
+        if (l_run > kMaxSum) {
+          const uint32_t k = min((__float_as_uint(l_run) >> 23) - 127u, 127u);
+          l_run *= __uint_as_float((127u - k) << 23);
+          m_run += (float)k;
+        }
         return true;
       };
       for (int j = PAIR ? X : 0; j < ntiles; j += step, ++i_own) {
-        // the tile's K scales, ahead of its scores
+        // the tile's scales, ahead of its scores
         const int ks = j % kRing;
-        if (!(ok = wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u, abort))) break;
-        float csk[8];
+        if (!(ok = wwait8(bars + 8 * (kScFull + ks), (uint32_t)(j / kRing) & 1u, abort))) break;
+        const uint32_t sc = sb + G::kSc + j % (2 * kRing) * 64;
+        float csk[8], lv[8], pc[8], pf[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          csk[i] = cs * __uint_as_float(lds32(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, i)));
+        for (int i = 0; i < 8; i += 2) {
+          const uint4 x = lds128(sc + 8 * i);
+          csk[i] = cs * __uint_as_float(x.x);
+          lv[i] = __uint_as_float(x.y);
+          csk[i + 1] = cs * __uint_as_float(x.z);
+          lv[i + 1] = __uint_as_float(x.w);
+        }
+        factors(lv, pc, pf);
         const uint32_t good = kgood[ks];
-        __syncwarp();
+        // some block's exponent is held at kMinFactor in some row
+        const bool held = __any_sync(0xFFFFFFFFu, __uint_as_float(emin[ks]) + m_run < mv_run + kMinFactor);
         if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
         if (fast)
-          ok = tile(std::false_type{}, j, good, csk);
+          ok = tile(std::false_type{}, j, good, csk, sc, pc, pf, held);
         else
-          ok = tile(std::true_type{}, j, good, csk);
+          ok = tile(std::true_type{}, j, good, csk, sc, pc, pf, held);
         if (!ok) break;
       }
       // the result once the last O_X += P_X V^ is done
@@ -635,9 +713,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       if (ok) {
         tc_fence_after();
         const bool partial = p.parts > 1;
-        // (written before the expansion that this half's last product waited for)
-        const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
-        const float f = partial ? vref : (l_run > 0.0f || l_run != l_run ? vref / l_run : 0.0f);
+        // O's scale over l, in two factors: 2^(m' - m) alone can pass fp32's exponents
+        const float f0 = m_run == -INFINITY ? 1.0f : fast_exp2(0.5f * (mv_run - m_run));
+        const float f = f0 * (l_run > 0.0f || l_run != l_run ? 1.0f / l_run : 0.0f);
         if (partial && row_ok)
           *(reinterpret_cast<float2*>(p.part_ml) + part * rows_all + row) = make_float2(m_run, l_run);
         // 128 bytes of every row at a time, turned in shared memory so that eight
@@ -667,7 +745,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  w[k] = bf16x2_of(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
+                  w[k] = bf16x2_of(__uint_as_float(o[8 * i + 2 * k]) * f0 * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f0 * f);
                 sts128(st_w + (uint32_t)(((4 * half + i) ^ (lane & 7)) * 16), make_uint4(w[0], w[1], w[2], w[3]));
               }
             }
@@ -678,7 +756,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
             for (int i = 0; i < 8; ++i) {
               uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * f);
+              for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * f0 * f);
               sts128(st_w + (uint32_t)((i ^ (lane & 7)) * 16), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
@@ -700,27 +778,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // stores touch 128 contiguous bytes per eight lanes
     reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
-    // sV_ref: the largest V scale of the positions this CTA reads, or 2^-126 (the
-    // append's smallest), whose reciprocal is finite, when all are smaller; the
-    // first scores are on their way meanwhile
-    uint32_t best = 0u;
-    const int64_t g0 = (int64_t)j0 * kGroups, g1 = min((limit + GT - 1) / GT, (int64_t)(j0 + ntiles) * kGroups);
-#pragma unroll 2
-    for (int64_t gi = g0 + dt; gi < g1; gi += 32 * kExpWarps) {
-      const int64_t phys = block8_page(p.c, b, gi * GT, p.flag);
-      if (phys < 0) continue;
-      const uint8_t* grp = pool + block8_group_offset(L, phys, p.hkv, h, (int)((gi * GT) & (p.c.page_size - 1)));
-#pragma unroll
-      for (int k = 0; k < GT / 16; ++k) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(grp + L.scale(k, 1)));
-        if (gi * GT + 16 * k < limit && v < 0x7F800000u) best = max(best, v);
-      }
-    }
-    best = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (lane == 0 && best != 0u) atomicMax(vref_bits, best);
-    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kExpWarps) : "memory");
-    const float vref = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(vref_bits));
-    const float vinv = 1.0f / vref;
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kVRing, slot = j % kVSlots8;
       const uint32_t codes = sb + G::kV8 + s * kT * D, dst = sb + G::kV + slot * kT * D * 2;
@@ -733,7 +790,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 #pragma unroll 1
       for (int blk = dt / D; blk < kT / 16; blk += 32 * kExpWarps / D) {
         uint4 w = lds128(codes + ((uint32_t)(blk * D) + c) * 16);
-        const float r = __uint_as_float(lds32(scale_at<GT>(sb + G::kVS + s * kScaleBytes, blk) + 4)) * vinv;
+        const float r = v_rest(lds32(scale_at<GT>(sb + G::kVS + s * kScaleBytes, blk) + 4));
         uint32_t r2 = pack_f16x2(r, r);
         uint32_t ws[4] = {w.x, w.y, w.z, w.w};
         if (!whole) {  // positions that are not attended: zero codes and a finite factor
@@ -776,6 +833,21 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       };
       drain(kKFull, kRing, kiss);
       drain(kV8Full, kVRing, viss);
+    }
+   } else if (warp == kScWarp) {
+    // ------------------------------------------------------------ scales
+    // what every row's softmax needs of the tile's 8 blocks: sK and log2 of sV's power
+    // of two (once here instead of in 256 rows)
+    for (int j = 0; j < ntiles; ++j) {
+      const int ks = j % kRing;
+      if (!wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u, abort)) break;
+      const uint2 sc = lds64(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, lane & 7));
+      const uint32_t e = v_exponent(sc.y);
+      if (lane < 8) sts64(sb + G::kSc + j % (2 * kRing) * 64 + 8 * lane, sc.x, __float_as_uint(v_log2(e)));
+      const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, e);
+      if (lane == 0) emin[ks] = __float_as_uint(v_log2(least));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kScFull + ks));
     }
    } else if (warp - kMWarp < nx) {
     // ----------------------------------------------------------- tensor cores
@@ -899,9 +971,9 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const Prefill8Params
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (ml[k].x == -INFINITY && ml[k].y == 0.0f) continue;  // no position of this row (its sums were not written)
-      const float f = ml[k].x == -INFINITY ? 1.0f : fast_exp2(ml[k].x - ref);
+      const float f = (ml[k].x == -INFINITY ? 1.0f : fast_exp2(ml[k].x - ref)) * ml[k].y;
       o = make_float4(fmaf(f, x[k].x, o.x), fmaf(f, x[k].y, o.y), fmaf(f, x[k].z, o.z), fmaf(f, x[k].w, o.w));
-      l = fmaf(f, ml[k].y, l);
+      l += f;
     }
     mx = mn;
   }

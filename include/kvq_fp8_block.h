@@ -170,11 +170,13 @@ kvq_status kvq_fp8_block_decode_attn(const kvq_cache *cache, int32_t batch, int3
  *   q, out       device [batch][chunk][num_q_heads][head_dim], q bf16, out of
  *                out_dtype; 16-byte aligned.
  * q enters the products exactly or off by at most 2^-18 of its row's largest
- * element, the weights as f16, and the values as f16 relative to the largest
- * value scale of the positions that a block of query rows reads (exact for
- * scales down to 2^-15 of it, off by at most 2^-25 of it below that).  A value
- * that the append flagged NONFINITE can therefore reach every row of its chunk,
- * those before its position included.
+ * element.  A weight enters the second product times its block's value scale, as
+ * f16: off by at most 2^-11 of that, or 2^-25 of the largest such product that
+ * the row attends.  Value codes enter exactly; a value scale that is no power of
+ * two (the append makes none) is off by at most 2^-11, and so is its product
+ * with a code.  Values behind a row's last position do not change the row, but
+ * for NaN codes (the append flags them NONFINITE), which can reach every row of
+ * their chunk.
  *   workspace    kvq_fp8_block_prefill_workspace_bytes(...) bytes, 16-byte
  *                aligned, not shared by calls that may overlap.
  * Device flags: BAD_LENGTH (n_b outside 0..chunk: the sequence is skipped;

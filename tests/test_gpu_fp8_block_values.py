@@ -78,3 +78,52 @@ def test_tiny_value_scales(d, n, exponent):
     check(cache, T, q[0], out[0], torch.arange(T - n, T), floor=floor)
     dec = kvq.decode_attn(cache, _ints([T]), q[:, -1].contiguous())
     check(cache, T, q[0, -1:], dec, torch.tensor([T - 1]), floor=floor, prefill=False)
+
+
+@pytest.mark.parametrize("d,page,T,n", [(128, 64, 300, 5), (64, 16, 129, 40), (128, 32, 1000, 150), (64, 64, 700, 300)])
+@pytest.mark.parametrize("larger", [2.0 ** 30, 2.0 ** 100])
+def test_larger_values_later_in_a_chunk(d, page, T, n, larger):
+    """The values of the chunk's last token, far above all others, leave the rows
+    before it as they are; the last row is theirs.  (The 15 tokens that share its
+    block of 16 are held at its scale: what the cache holds of them is what counts.)"""
+    H, G = 2, 4
+    cache = filled(T, H, d, page, seed=5)
+    k, v = (torch.randn((1, 1, H, d), generator=_gen(8 + i), device="cuda") for i in range(2))
+    kvq.append(cache, _ints([T - 1]), k.to(BF), (v * larger).to(BF))
+    q = torch.randn((1, n, H * G, d), generator=_gen(7), device="cuda").to(BF)
+    last = torch.arange(T - n, T)
+    out = kvq.prefill_attn(cache, _ints([T]), q)
+    check(cache, T, q[0], out[0], last)
+    for i in (0, n - 2, n - 1):  # one row at its own length
+        dec = kvq.decode_attn(cache, _ints([T - n + i + 1]), q[:, i].contiguous())
+        check(cache, T, q[0, i:i + 1], dec, last[i:i + 1], prefill=False)
+
+
+@pytest.mark.parametrize("d,n", [(64, 3), (128, 70), (128, 200)])
+def test_values_of_every_scale(d, n):
+    """Blocks from 2^-120 to 2^110, each row's weight on a block of its own, the
+    blocks in falling and in rising order of their values."""
+    T, H = 640, 1
+    blocks = T // 16
+    for order in (1, -1):
+        cache = filled(T, H, d, 64, seed=11)
+        at = torch.linspace(-120, 110, blocks, device="cuda").round()[::1]
+        e = at if order == 1 else at.flip(0)
+        s = scales(cache)[..., 1]                              # [pages][1][1][4]
+        s.copy_(torch.ldexp(torch.ones(blocks, device="cuda"), e.int()).view(s.shape))
+        # keys: block i answers channel i alone
+        k = torch.zeros((1, T, H, d), device="cuda")
+        k[0, torch.arange(T), 0, (torch.arange(T) // 16) % d] = 1.0
+        codes = cache.pool.clone()
+        kvq.append(cache, _ints([0]), k.to(BF), torch.zeros_like(k).to(BF))
+        g = cache.group
+        cache.pool[..., g * d:2 * g * d] = codes[..., g * d:2 * g * d]
+        scales(cache)[..., 1].copy_(torch.ldexp(torch.ones(blocks, device="cuda"), e.int()).view(s.shape))
+        q = torch.zeros((1, n, blocks, d), device="cuda")      # head i looks at block i
+        q[..., torch.arange(blocks), torch.arange(blocks) % d] = 60.0 * math.sqrt(d)
+        H8 = blocks // 8                                       # (eight query heads a call)
+        for h in range(H8):
+            x = q[:, :, 8 * h:8 * h + 8].to(BF).contiguous()
+            out = kvq.prefill_attn(cache, _ints([T]), x)
+            assert torch.isfinite(out).all()
+            check(cache, T, x[0], out[0], torch.arange(T - n, T))
