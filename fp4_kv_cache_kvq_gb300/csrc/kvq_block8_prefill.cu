@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         const uint32_t good = kgood[ks];
         // some block's exponent is held at kMinFactor in some row
         const bool held = __any_sync(0xFFFFFFFFu, __uint_as_float(emin[ks]) + m_run < mv_run + kMinFactor);
+        __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
