@@ -22,6 +22,10 @@
 // count in l although their P rounds to 0 (the exponent that V adds is held at -60
 // and up for that, far under what f16 sees).  Both references are whole numbers, so
 // every sum of exponents is exact.  Accumulation, maxima and sums are fp32.
+// A block that a row sees in part can owe its scale to a token behind the row.  In a
+// tile that some row sees in part, with a scale 2^kScaleSpread over the smallest so far,
+// each token's own largest code therefore goes into P's exponent instead of its block's
+// scale, and out of V^ (exactly, too).
 //
 // What bounds it: the tensor pipe, 4 Hq d flop per attended pair.  Work split:
 // a CTA takes 256 query rows (G heads x 256/G tokens) of one kv head as two
@@ -49,7 +53,8 @@
 // the largest of the CTA's positions: 1407 -> 1450 us (head_dim 64: 1200 -> 1224);
 // what follows from the scales alone is computed ahead of the scores, by one warp for
 // all rows where it does not depend on the row (1493 behind the scores, 1466 by every
-// row).
+// row).  The form with exponents for single tokens beside it: 1468 (1247), in code that
+// these cases do not enter (1505 with every partly attended tile looked at).
 // Slower: two threads per row 1.72; S of the next tile started before O of this
 // one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
 // loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
@@ -99,6 +104,11 @@ constexpr float kSlack8 = 15.0f;
 constexpr float kMinFactor = -60.0f, kMaxFactor = 120.0f;
 // m is raised when it is this far under a score beside a held exponent, and once l
 // has grown to kMaxSum; between, l counts what m lags.
+// Value scales that differ by this much (log2; f16 has 14 before its subnormals) give the
+// tokens of a partly attended tile exponents of their own; V^ of such a token is under
+// 2^(kTokenTop + 1).
+constexpr uint32_t kScaleSpread = 10;
+constexpr int kTokenTop = 5;
 constexpr float kIntBias = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the integer
 constexpr float kSlackSum = 4.0f, kMaxSum = 1073741824.0f;  // 2^30
 constexpr uint32_t kPoll8 = 20000;
@@ -107,8 +117,8 @@ constexpr int kScaleBytes = 128;  // scales of one tile: up to 8 groups of 16 by
 enum : int {
   kKFull = 0,                      // [kKRing] K codes and scales landed
   kKEmpty = kKFull + kKRing,       // [kKRing] S products done (commit), softmax warps have the scales
-  kScFull = kKEmpty + kKRing,      // [kKRing] the tile's scales as the softmax takes them
-  kV8Full = kScFull + kKRing,      // [kVRing] V codes and scales landed
+  kScFull = kKEmpty + kKRing,      // [2 kKRing] the tile's scales as the softmax takes them
+  kV8Full = kScFull + 2 * kKRing,      // [kVRing] V codes and scales landed
   kV8Empty = kV8Full + kVRing,     // [kVRing] expanded (one arrival per warp)
   kVFull = kV8Empty + kVRing,      // [kVSlots8] V^ slot written
   kVEmpty = kVFull + kVSlots8,     // [kVSlots8] O products done with it (commit)
@@ -116,7 +126,8 @@ enum : int {
   kPFull = kSFull + kXTiles,       // [kXTiles] P_X in TMEM, O_X rescaled
   kPvDone = kPFull + kXTiles,      // [kXTiles] O_X += P_X V^ done
   kTurn = kPvDone + kXTiles,       // [kXTiles] query tile X's products may be issued
-  kBars8 = kTurn + kXTiles
+  kTok = kTurn + kXTiles,          // the expansion's threads have looked at a tile's tokens
+  kBars8 = kTok + 1
 };
 
 struct Prefill8Params {
@@ -143,12 +154,15 @@ struct P8Geo {
   static constexpr int kV = kV8 + kVRing * kT * D;       // [kVSlots8][D][128] f16
   static constexpr int kKS = kV + kVSlots8 * kT * D * 2;
   static constexpr int kVS = kKS + kKRing * kScaleBytes;
-  // [2 kKRing][8] (sK, log2 sV): a tile's are read until the tile one K ring later
-  // has been taken
+  // [2 kKRing][8] (sK, log2 sV), with kScFull and emin: a tile's are read by the softmax
+  // until the tile one K ring later has been taken, and by the expansion until then too
+  // (the tile before that one has its scores only once this tile's product is issued)
   static constexpr int kSc = kVS + kVRing * kScaleBytes;
-  static constexpr int kBar = kSc + 2 * kKRing * 64;
+  static constexpr int kTokExp = kSc + 2 * kKRing * 64;    // [kVSlots8][128] a token's exponent, biased
+  static constexpr int kTokMul = kTokExp + kVSlots8 * kT;  // [128] a token's factor in V^, f16
+  static constexpr int kBar = kTokMul + kT * 2;
   static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, (unused), masks, exponents
-  static constexpr int kMiscEnd = kMisc + 4 * (3 + 2 * kKRing + kVRing);
+  static constexpr int kMiscEnd = kMisc + 4 * (3 + 3 * kKRing + kVRing);
   // where a half's rows are turned for coalesced stores: 128 bytes a row.  At
   // head_dim 128 that is query memory that no product reads any more: the half's
   // own tile's, for a pair the second tile's, which holds no queries
@@ -273,6 +287,12 @@ __device__ __forceinline__ void block_p(const uint32_t (&v)[16], uint32_t* w, fl
 __device__ __forceinline__ uint32_t v_exponent(uint32_t bits) { return min(max(bits >> 23, 1u), 247u); }
 // e as a float, from v_exponent's biased form
 __device__ __forceinline__ float v_log2(uint32_t e) { return __uint_as_float(0x4B000000u | e) - (8388608.0f + 127.0f); }
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
 // the rest, sV / 2^e
 __device__ __forceinline__ float v_rest(uint32_t bits) {
   return __uint_as_float(bits) * __uint_as_float((254u - v_exponent(bits)) << 23);
@@ -305,6 +325,13 @@ __device__ __forceinline__ uint32_t e4m3x2_from_f16x2(uint32_t v) {
   return r;
 }
 
+// 8 columns of this warp's TMEM lanes, without the wait.
+__device__ __forceinline__ void tmem_st8_async(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
   volatile uint32_t* kgood = misc + 3;             // [kKRing] bit i: block i of the tile lies in a valid page
   volatile uint32_t* vgood = misc + 3 + kKRing;    // [kVRing]
-  volatile uint32_t* emin = misc + 3 + kKRing + kVRing;  // [kKRing] the smallest log2 sV of the tile
+  volatile uint32_t* emin = misc + 3 + kKRing + kVRing;  // [2 kKRing] the smallest log2 sV of the tile; NaN: its tokens have exponents of their own
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int sp = (int)(blockIdx.x % (unsigned)p.splits);
@@ -413,6 +440,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kKFull + i), 1);
       mbar_init(bars + 8 * (kKEmpty + i), 5 * users);
       mbar_init(bars + 8 * (kScFull + i), 1);
+      mbar_init(bars + 8 * (kScFull + kKRing + i), 1);
     }
     for (int i = 0; i < kVRing; ++i) {
       mbar_init(bars + 8 * (kV8Full + i), 1);
@@ -428,6 +456,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       mbar_init(bars + 8 * (kPvDone + i), 1);
       mbar_init(bars + 8 * (kTurn + i), 1);
     }
+    mbar_init(bars + 8 * kTok, 32 * kExpWarps);
     *abort = 0;
     fence_barrier_init();
   }
@@ -580,6 +609,48 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           pf[i] = __uint_as_float(__float_as_uint(fmaxf(kIntBias + 127.0f - a, kIntBias + 127.0f - kMaxFactor)) << 23);
         }
       };
+      // Lazy references: when m' is raised O shrinks (by al), when m is l does (al_l).
+      // Returns whether a row of the warp raised m' (TMEM accesses are warp-collective).
+      const auto raise = [&](float mt, float mv, float& al, float& al_l) -> bool {
+        const bool up = mv > mv_run + kSlack8, any_up = __any_sync(0xFFFFFFFFu, up);
+        if (up) {
+          const float to = ceilf(mv);
+          if (mv_run != -INFINITY) al = fast_exp2(mv_run - to);
+          mv_run = to;
+        }
+        if (mt > m_run + kSlackSum) {
+          const float to = ceilf(mt);
+          if (m_run != -INFINITY) al_l = fast_exp2(m_run - to);
+          m_run = to;
+        }
+        return any_up;
+      };
+      // P is on its way to TMEM: O_X rescaled, P handed over, l.
+      const auto finish = [&](bool any_up, float al, float al_l, float sum) -> bool {
+        if (any_up && i_own > 0) {
+          if (!wwait8(pv_done, (i_own - 1) & 1u, abort)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(op + (uint32_t)c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st32_async(op + (uint32_t)c0, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        l_run = l_run * al_l + sum;
+        if (l_run > kMaxSum) {
+          const uint32_t k = min((__float_as_uint(l_run) >> 23) - 127u, 127u);
+          l_run *= __uint_as_float((127u - k) << 23);
+          m_run += (float)k;
+        }
+        return true;
+      };
       // One cache tile; MASKED: some of its scores are not attended.  Two bodies, so
       // that the whole tiles' is one straight run of instructions.
       const auto tile = [&](auto masked_c, int j, uint32_t good, const float (&csk_in)[8], uint32_t sc,
@@ -620,9 +691,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = fmaf(__uint_as_float(vm[i]), csk[i], pc[i]);
         const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-        // lazy references: when m' is raised O shrinks, when m is l does
         float al = 1.0f, al_l = 1.0f;
-        bool any_up = false;  // (TMEM accesses are warp-collective)
+        bool any_up = false;
         if (__any_sync(0xFFFFFFFFu, top > (mv_run == -INFINITY ? -INFINITY : kSlack8)) || held) {
           float mt = -INFINITY, mv = -INFINITY, lv[8];
 #pragma unroll
@@ -632,18 +702,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
             mt = fmaxf(mt, x);
             mv = fmaxf(mv, x + lv[i]);
           }
-          const bool up = mv > mv_run + kSlack8;
-          any_up = __any_sync(0xFFFFFFFFu, up);
-          if (up) {
-            const float to = ceilf(mv);
-            if (mv_run != -INFINITY) al = fast_exp2(mv_run - to);
-            mv_run = to;
-          }
-          if (mt > m_run + kSlackSum) {
-            const float to = ceilf(mt);
-            if (m_run != -INFINITY) al_l = fast_exp2(m_run - to);
-            m_run = to;
-          }
+          any_up = raise(mt, mv, al, al_l);
           factors(lv, pc, pf);
         }
         uint64_t l2[2] = {0ull, 0ull};
@@ -654,38 +713,70 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           block_p(v[i + 1], w + 8, csk[i + 1], pc[i + 1], pf[i + 1], l2[1]);
           tmem_st16_async(sp_col + (uint32_t)(8 * i), w);
         }
-        if (any_up && i_own > 0) {
-          if (!wwait8(pv_done, (i_own - 1) & 1u, abort)) return false;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-            tmem_ld32(op + (uint32_t)c0, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st32_async(op + (uint32_t)c0, o);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
         float a0, a1, b0, b1;
         upk2(l2[0], a0, a1);
         upk2(l2[1], b0, b1);
-        l_run = l_run * al_l + ((a0 + a1) + (b0 + b1));
-        if (l_run > kMaxSum) {
-          const uint32_t k = min((__float_as_uint(l_run) >> 23) - 127u, 127u);
-          l_run *= __uint_as_float((127u - k) << 23);
-          m_run += (float)k;
+        return finish(any_up, al, al_l, (a0 + a1) + (b0 + b1));
+      };
+      // A tile whose tokens have exponents of their own: 16 scores at a time, from TMEM
+      // once for the references and once for P (whose columns are those of scores that
+      // have been taken).
+      const auto tile_tokens = [&](int j, uint32_t good, uint32_t sc) -> bool {
+        if (!wwait8(s_full, i_own & 1u, abort)) return false;
+        tc_fence_after();
+        const int64_t p0 = (int64_t)(j0 + j) * kT;
+        const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
+        const uint32_t tok = sb + G::kTokExp + (uint32_t)(j % kVSlots8 * kT);
+        // block i: its y (-inf where not attended), and its tokens' exponents, four in a word
+        const auto take = [&](int i, float (&y)[16], uint32_t (&e)[4]) {
+          uint32_t v[16];
+          tmem_ld16(sp_col + (uint32_t)(16 * i), v);
+          const float ck = cs * __uint_as_float(lds32(sc + (uint32_t)(8 * i)));
+          const int left = ((good >> i) & 1u) ? lim - 16 * i : 0;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) y[c] = c < left ? __uint_as_float(v[c]) * ck : -INFINITY;
+          const uint4 x = lds128(tok + (uint32_t)(16 * i));
+          e[0] = x.x, e[1] = x.y, e[2] = x.z, e[3] = x.w;
+        };
+        const auto exponent = [](const uint32_t (&e)[4], int c) { return __byte_perm(e[c >> 2], 0u, 0x4440u + (uint32_t)(c & 3)); };
+        float y[16], mt = -INFINITY, mv = -INFINITY, sum = 0.0f;
+        uint32_t e[4];
+#pragma unroll 1
+        for (int i = 0; i < kT / 16; ++i) {
+          take(i, y, e);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            mt = fmaxf(mt, y[c]);
+            mv = fmaxf(mv, y[c] + v_log2(exponent(e, c)));
+          }
         }
-        return true;
+        float al = 1.0f, al_l = 1.0f;
+        const bool any_up = raise(mt, mv, al, al_l);
+        const float mo = m_run == -INFINITY ? 0.0f : m_run;
+        const float r = fast_exp2(fminf(mo - (mv_run == -INFINITY ? 0.0f : mv_run), 126.0f));  // 2^(m - m')
+#pragma unroll 1
+        for (int i = 0; i < kT / 16; ++i) {
+          uint32_t w[8];
+          take(i, y, e);
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float p0 = fast_exp2(y[c] - mo), p1 = fast_exp2(y[c + 1] - mo);
+            sum += p0 + p1;
+            // the token's 2^exponent over 2^m'; finite, as p can be 0
+            const float f0 = fminf(__uint_as_float(exponent(e, c) << 23) * r, 3e38f);
+            const float f1 = fminf(__uint_as_float(exponent(e, c + 1) << 23) * r, 3e38f);
+            w[c / 2] = pack_f16x2(p0 * f0, p1 * f1);
+          }
+          tmem_st8_async(sp_col + (uint32_t)(8 * i), w);
+        }
+        return finish(any_up, al, al_l, sum);
       };
       for (int j = PAIR ? X : 0; j < ntiles; j += step, ++i_own) {
         // the tile's scales, ahead of its scores
         const int ks = j % kRing;
-        if (!(ok = wwait8(bars + 8 * (kScFull + ks), (uint32_t)(j / kRing) & 1u, abort))) break;
-        const uint32_t sc = sb + G::kSc + j % (2 * kRing) * 64;
+        const int is = j % (2 * kRing);
+        if (!(ok = wwait8(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u, abort))) break;
+        const uint32_t sc = sb + G::kSc + is * 64;
         float csk[8], lv[8], pc[8], pf[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -698,15 +789,20 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         factors(lv, pc, pf);
         const uint32_t good = kgood[ks];
         // some block's exponent is held at kMinFactor in some row
-        const bool held = __any_sync(0xFFFFFFFFu, __uint_as_float(emin[ks]) + m_run < mv_run + kMinFactor);
+        const float least = __uint_as_float(emin[is]);
+        const bool held = __any_sync(0xFFFFFFFFu, least + m_run < mv_run + kMinFactor);
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kKEmpty + ks));
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const bool fast = p0 + kT - 1 <= pos_min && good == 0xFFu;
-        if (fast)
+        if (fast) {
           ok = tile(std::false_type{}, j, good, csk, sc, pc, pf, held);
-        else
+        } else if (__builtin_expect(least == least, 1)) {
           ok = tile(std::true_type{}, j, good, csk, sc, pc, pf, held);
+        } else {  // the tokens' exponents come with V^
+          if (!(ok = wwait8(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
+          ok = tile_tokens(j, good, sc);
+        }
         if (!ok) break;
       }
       // the result once the last O_X += P_X V^ is done
@@ -779,6 +875,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // stores touch 128 contiguous bytes per eight lanes
     reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
+    uint32_t looked = 0;  // phases of kTok
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kVRing, slot = j % kVSlots8;
       const uint32_t codes = sb + G::kV8 + s * kT * D, dst = sb + G::kV + slot * kT * D * 2;
@@ -812,6 +909,42 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         sts128(at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         sts128(at + (D / 8) * 128, make_uint4(hi[0], hi[1], hi[2], hi[3]));
       }
+      if (__builtin_expect((int64_t)(j0 + j) * kT + kT - 1 > pos_min, 0)) {
+        const int is = j % (2 * kRing);
+        if (!wwait8(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u, abort)) break;
+        if (emin[is] == 0x7FC00000u) {  // the tokens have exponents of their own
+          // thread = token: its largest code
+          const int blk = dt >> 4;
+          const uint32_t row0 = codes + (uint32_t)(blk * D * 16 + block8_v_byte(dt & 15));
+          uint32_t top = 0u;
+#pragma unroll 4
+          for (int k = 0; k < D; ++k) {
+            const uint32_t x = lds8(row0 + 16u * (uint32_t)k) & 0x7Fu;
+            top = max(top, x == 0x7Fu ? 0u : x);
+          }
+          const uint32_t e = v_exponent(lds32(scale_at<GT>(sb + G::kVS + s * kScaleBytes, blk) + 4));
+          const int k = (int)(__float_as_uint(e4m3_to_f32(top)) >> 23) - 127;  // 2^k <= top < 2^(k+1)
+          const bool zero = top == 0u || !((good >> blk) & 1u) || dt >= valid;
+          // 2^up into V^: none where sV is next to fp32's smallest, or its largest with a rest of more than 2
+          const int up = zero || e == 247u ? 0 : min(kTokenTop - k, (int)e - 1);
+          sts8(sb + G::kTokExp + (uint32_t)(slot * kT + dt), zero ? 1u : e - (uint32_t)up);
+          sts16(sb + G::kTokMul + (uint32_t)(2 * dt), (uint32_t)(up + 15) << 10);
+          mbar_arrive(bars + 8 * kTok);
+          if (!wwait8(bars + 8 * kTok, looked++ & 1u, abort)) break;
+#pragma unroll 1
+          for (int t0 = 16 * (dt / D); t0 < kT; t0 += 16 * (32 * kExpWarps / D)) {  // the thread's own items
+#pragma unroll
+            for (int t = t0; t < t0 + 16; t += 8) {
+              const uint32_t at = dst + core_offset(c, (uint32_t)t, D);
+              const uint4 v = lds128(at), m = lds128(sb + G::kTokMul + (uint32_t)(2 * t));
+              sts128(at, make_uint4(hmul2_u32(v.x, m.x), hmul2_u32(v.y, m.y), hmul2_u32(v.z, m.z), hmul2_u32(v.w, m.w)));
+            }
+          }
+          // (one array of factors: every thread is done with it before the next such tile)
+          mbar_arrive(bars + 8 * kTok);
+          if (!wwait8(bars + 8 * kTok, looked++ & 1u, abort)) break;
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (kV8Empty + s));
       fence_async_smem();
@@ -839,16 +972,22 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // ------------------------------------------------------------ scales
     // what every row's softmax needs of the tile's 8 blocks: sK and log2 of sV's power
     // of two (once here instead of in 256 rows)
+    uint32_t least = 255u;  // the smallest exponent so far
     for (int j = 0; j < ntiles; ++j) {
-      const int ks = j % kRing;
+      const int ks = j % kRing, is = j % (2 * kRing);
       if (!wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u, abort)) break;
       const uint2 sc = lds64(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, lane & 7));
-      const uint32_t e = v_exponent(sc.y);
-      if (lane < 8) sts64(sb + G::kSc + j % (2 * kRing) * 64 + 8 * lane, sc.x, __float_as_uint(v_log2(e)));
-      const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, e);
-      if (lane == 0) emin[ks] = __float_as_uint(v_log2(least));
+      const uint32_t e = v_exponent(sc.y), here = __reduce_min_sync(0xFFFFFFFFu, e);
+      // (a scale of 2^-126 and less is that of zeros)
+      const int64_t p0 = (int64_t)(j0 + j) * kT;
+      const bool counts = ((kgood[ks] >> (lane & 7)) & 1u) && p0 + 16 * (lane & 7) < limit && e > 1u;
+      least = min(least, __reduce_min_sync(0xFFFFFFFFu, counts ? e : 255u));
+      const bool tokens =
+          __reduce_max_sync(0xFFFFFFFFu, counts ? e : 0u) > least + kScaleSpread && p0 + kT - 1 > pos_min;
+      if (lane < 8) sts64(sb + G::kSc + is * 64 + 8 * lane, sc.x, __float_as_uint(v_log2(e)));
+      if (lane == 0) emin[is] = tokens ? 0x7FC00000u : __float_as_uint(v_log2(here));
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (kScFull + ks));
+      if (lane == 0) mbar_arrive(bars + 8 * (kScFull + is));
     }
    } else if (warp - kMWarp < nx) {
     // ----------------------------------------------------------- tensor cores

@@ -127,3 +127,38 @@ def test_values_of_every_scale(d, n):
             out = kvq.prefill_attn(cache, _ints([T]), x)
             assert torch.isfinite(out).all()
             check(cache, T, x[0], out[0], torch.arange(T - n, T))
+
+
+@pytest.mark.parametrize("d,page,T,n", [(128, 64, 300, 5), (64, 16, 135, 40), (128, 32, 1000, 150), (64, 64, 700, 300),
+                                        (128, 64, 20, 7)])
+@pytest.mark.parametrize("larger", [2.0 ** 12, 2.0 ** 16, 2.0 ** 30, 2.0 ** 100])
+@pytest.mark.parametrize("behind", [0, 3])
+def test_a_larger_value_in_the_same_block(d, page, T, n, larger, behind):
+    """A row that sees a part of a block whose scale a later token has set: the block
+    is what the cache holds of it (its codes may all be 0 there), the row's other
+    blocks count as ever.  behind: tokens of the chunk after the large one."""
+    H, G = 2, 4
+    cache = filled(T, H, d, page, seed=5)
+    at = T - 1 - behind
+    k, v = (torch.randn((1, 1 + behind, H, d), generator=_gen(8 + i), device="cuda") for i in range(2))
+    v[:, 0] *= larger
+    kvq.append(cache, _ints([at]), k.to(BF), v.to(BF))
+    q = torch.randn((1, n, H * G, d), generator=_gen(7), device="cuda").to(BF)
+    last = torch.arange(T - n, T)
+    out = kvq.prefill_attn(cache, _ints([T]), q)
+    K, V = kvq.dequant(cache, _ints([T]), T)
+    t = torch.arange(T)
+    part = ((t // 16)[None] == (last // 16)[:, None]) & ((last + 1) % 16 != 0)[:, None]   # the row's own block, in part
+    for h in range(H):
+        rows = slice(h * G, (h + 1) * G)
+        x, vmax = q[0, :, rows], V[0, :, h].abs().amax(-1).double()
+        own = vmax / 2.0 ** 5                                  # a token with an exponent of its own: its values under 2^6 of it
+        vs = torch.where(part.cuda(), own, torch.maximum(value_scales(cache, T)[:, h].double(), own))
+        want, p = attn_bounds.attend(x, K[0, :, h], V[0, :, h], 1 / math.sqrt(d), last)
+        for i in range(n):
+            tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d), vs[i])
+            off = (out[0, i:i + 1, rows].double() - want[i:i + 1]).abs()
+            assert (off <= tol).all(), (h, i, (off / tol).max().item())
+            dec_tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d))
+            if T - n + i < at:  # and within eight times what a decode of the row may be off
+                assert (off <= 8 * dec_tol).all(), (h, i, (off / dec_tol).max().item())
