@@ -25,7 +25,9 @@
 // A block that a row sees in part can owe its scale to a token behind the row.  In a
 // tile that some row sees in part, with a scale 2^kScaleSpread over the smallest so far,
 // each token's own largest code therefore goes into P's exponent instead of its block's
-// scale, and out of V^ (exactly, too).
+// scale, and out of V^ (exactly, too).  NaN values of such a tile are taken out of V^
+// (a product would carry them to the rows that do not see them) and noted by channel;
+// the rows from the first one on are NaN there.
 //
 // What bounds it: the tensor pipe, 4 Hq d flop per attended pair.  Work split:
 // a CTA takes 256 query rows (G heads x 256/G tokens) of one kv head as two
@@ -54,7 +56,8 @@
 // what follows from the scales alone is computed ahead of the scores, by one warp for
 // all rows where it does not depend on the row (1493 behind the scores, 1466 by every
 // row).  The form with exponents for single tokens beside it: 1468 (1247), in code that
-// these cases do not enter (1505 with every partly attended tile looked at).
+// these cases do not enter (1505 with every partly attended tile looked at).  The look for NaN
+// values: 1475 (1249).
 // Slower: two threads per row 1.72; S of the next tile started before O of this
 // one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
 // loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
@@ -160,8 +163,9 @@ struct P8Geo {
   static constexpr int kSc = kVS + kVRing * kScaleBytes;
   static constexpr int kTokExp = kSc + 2 * kKRing * 64;    // [kVSlots8][128] a token's exponent, biased
   static constexpr int kTokMul = kTokExp + kVSlots8 * kT;  // [128] a token's factor in V^, f16
-  static constexpr int kBar = kTokMul + kT * 2;
-  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, (unused), masks, exponents
+  static constexpr int kNan = kTokMul + kT * 2;  // [D] per channel the first position (of the CTA's) whose value is NaN
+  static constexpr int kBar = kNan + 4 * D;
+  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, first NaN, masks, exponents
   static constexpr int kMiscEnd = kMisc + 4 * (3 + 3 * kKRing + kVRing);
   // where a half's rows are turned for coalesced stores: 128 bytes a row.  At
   // head_dim 128 that is query memory that no product reads any more: the half's
@@ -460,6 +464,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     *abort = 0;
     fence_barrier_init();
   }
+  int* nan_first = reinterpret_cast<int*>(base + G::kNan);
+  int* nan_least = reinterpret_cast<int*>(misc + 2);  // the smallest of them
   if (warp == 0) tmem_alloc(smem_addr(tslot), kTmem8);
   tc_fence_before();
   __syncthreads();
@@ -830,6 +836,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         uint8_t* ob = partial ? reinterpret_cast<uint8_t*>(p.part_o + (part * rows_all + row0) * D)
                               : static_cast<uint8_t*>(p.out) + row0 * D * (bf ? 2 : 4);
         const int row_b = D * (bf ? 2 : 4);
+        // NaN values that the row has seen and V^ has not (noted before the expansion that
+        // this half's last product waited for)
+        const int seen_to = row_ok ? (int)min(pos_r - (int64_t)j0 * kT, (int64_t)INT32_MAX - 1) : -1;
+        const bool nans = __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(nan_least) <= seen_to);
 #pragma unroll 1
         for (int c0 = 0; c0 < row_b; c0 += 128) {
           if (bf) {
@@ -857,6 +867,15 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
               sts128(st_w + (uint32_t)((i ^ (lane & 7)) * 16), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
+          if (__builtin_expect(nans, 0)) {  // into the thread's own row
+            const int size = bf ? 2 : 4;
+#pragma unroll 1
+            for (int i = 0; i < 128; i += size) {
+              const uint32_t at = st_w + (uint32_t)((((i >> 4) ^ (lane & 7)) << 4) + (i & 15));
+              if (*reinterpret_cast<volatile int*>(nan_first + (c0 + i) / size) > seen_to) continue;
+              sts16(at + (uint32_t)size - 2u, 0x7FC0u);  // the upper half of an fp32 NaN, or a bf16 one
+            }
+          }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -875,6 +894,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // stores touch 128 contiguous bytes per eight lanes
     reg_dec<kRegsExpand>();
     const int dt = tid - 32 * kSmWarps;
+    // (ahead of the CTA's barrier, behind the queries' loads, these stores cost 4%)
+    if (dt < D) nan_first[dt] = INT32_MAX;
+    if (dt == 0) *nan_least = INT32_MAX;
+    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kExpWarps) : "memory");
     uint32_t looked = 0;  // phases of kTok
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kVRing, slot = j % kVSlots8;
@@ -909,7 +932,26 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         sts128(at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         sts128(at + (D / 8) * 128, make_uint4(hi[0], hi[1], hi[2], hi[3]));
       }
-      if (__builtin_expect((int64_t)(j0 + j) * kT + kT - 1 > pos_min, 0)) {
+      if (__builtin_expect((int64_t)(j0 + j) * kT + kT - 1 > pos_min, 0)) {  // some row sees it in part
+        uint32_t nan = 0u;  // bit 7 of a byte: the code is NaN's, 0x7F or 0xFF
+#pragma unroll
+        for (int i = 0; i < kT / 16 * D / (32 * kExpWarps); ++i) {
+          const uint4 w = lds128(codes + ((uint32_t)((dt / D + i * (32 * kExpWarps / D)) * D) + c) * 16);
+          nan |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                 ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+        }
+        if (__builtin_expect((nan & 0x80808080u) != 0u, 0)) {
+#pragma unroll 1
+          for (int t = 0; t < valid; ++t) {
+            const int blk = t >> 4;
+            if (((good >> blk) & 1u) == 0u || blk % (32 * kExpWarps / D) != dt / D) continue;  // not the thread's item
+            const uint32_t x = lds8(codes + ((uint32_t)(blk * D) + c) * 16 + (uint32_t)block8_v_byte(t & 15));
+            if ((x & 0x7Fu) != 0x7Fu) continue;
+            sts16(dst + core_offset(c, (uint32_t)t, D), 0u);
+            atomicMin(nan_first + c, j * kT + t);
+            atomicMin(nan_least, j * kT + t);
+          }
+        }
         const int is = j % (2 * kRing);
         if (!wwait8(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u, abort)) break;
         if (emin[is] == 0x7FC00000u) {  // the tokens have exponents of their own

@@ -162,3 +162,44 @@ def test_a_larger_value_in_the_same_block(d, page, T, n, larger, behind):
             dec_tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d))
             if T - n + i < at:  # and within eight times what a decode of the row may be off
                 assert (off <= 8 * dec_tol).all(), (h, i, (off / dec_tol).max().item())
+
+
+@pytest.mark.parametrize("d,page,T,n,at", [
+    (128, 64, 300, 5, 297), (64, 16, 135, 40, 120), (128, 32, 1000, 150, 900), (64, 64, 700, 300, 500),
+    (128, 64, 20, 7, 16), (128, 256, 2600, 128, 2495), (64, 32, 900, 33, 100), (128, 64, 300, 200, 299)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_nan_values_reach_the_rows_that_see_them(d, page, T, n, at, dtype):
+    """A NaN value of one token and channel: NaN in that channel for the rows from the
+    token on, no change for those before it."""
+    H, G, ch = 2, 4, d // 2 + 3
+    cache = filled(T, H, d, page, seed=5)
+    m = 16 - at % 16 if at + 16 <= T else 1                 # and the rest of its block again, so that it is as appended
+    k, v = (torch.randn((1, min(m, T - at), H, d), generator=_gen(8 + i), device="cuda") for i in range(2))
+    v[0, 0, 1, ch] = float("nan")
+    err = _ints([0])
+    kvq.append(cache, _ints([at]), k.to(BF), v.to(BF), err=err)
+    assert err.item() == kvq.FLAG_NONFINITE
+    q = torch.randn((1, n, H * G, d), generator=_gen(7), device="cuda").to(BF)
+    out = torch.empty(q.shape, dtype=dtype, device="cuda")
+    kvq.prefill_attn(cache, _ints([T]), q, out=out)
+    last = torch.arange(T - n, T)
+    sees = (last >= at).cuda()
+    nan = out[0].isnan()
+    want = torch.zeros_like(nan)
+    want[sees, G:, ch] = True
+    assert torch.equal(nan, want)
+    # the rows before it, and the other kv head's, within their bounds
+    K, V = kvq.dequant(cache, _ints([T]), T)
+    V = V.nan_to_num(0.0)
+    for h in range(H):
+        rows = slice(h * G, (h + 1) * G)
+        seen_scale = value_scales(cache, T)[:, h].clone().double()
+        seen_scale[at // 16 * 16:at // 16 * 16 + 16] = V[0, at // 16 * 16:at // 16 * 16 + 16, h].abs().amax(-1).double() / 2 ** 5
+        for i in range(n):
+            if h == 1 and sees[i]:
+                continue
+            ref, p = attn_bounds.attend(q[0, i:i + 1, rows], K[0, :, h], V[0, :, h], 1 / math.sqrt(d), last[i:i + 1])
+            tol = attn_bounds.bound(q[0, i:i + 1, rows], K[0, :, h], V[0, :, h], p, 1 / math.sqrt(d),
+                                    torch.maximum(seen_scale, V[0, :, h].abs().amax(-1).double() / 2 ** 5), dtype, ref)
+            off = (out[0, i:i + 1, rows].double() - ref).abs()
+            assert (off <= tol).all(), (h, i, (off / tol).max().item())
