@@ -58,12 +58,23 @@ struct Decode8Params {
   int64_t n_slots;
   void* out;                          // direct: the result, else nullptr
   int32_t out_bf16;
+  uint64_t wait_ns;                   // a test's limit of the work waits, or 0
 };
 
 // Positions of sequence b: no more than its pages can hold (a longer length is
 // flagged where its last chunk is read).
 __device__ __forceinline__ int32_t walk_len(const Decode8Params& p, int b) {
   return (int32_t)min((int64_t)__ldg(p.lens + b), (int64_t)p.c.max_pages_per_seq * p.c.page_size);
+}
+
+// A consumer's wait for a stage to land and the producer's for a free one: the
+// library's limit or, in the instantiation for tests, theirs.
+template <bool TEST>
+__device__ __forceinline__ bool work_wait8(const Decode8Params& p, uint32_t bar, uint32_t parity) {
+  if constexpr (TEST)
+    return mbar_wait_limit(bar, parity, p.wait_ns);
+  else
+    return mbar_wait(bar, parity);
 }
 
 // Compile-time view of one group of GT tokens (see Block8Layout).
@@ -141,7 +152,7 @@ __device__ __forceinline__ void f16x2x2_from_e4m3x4(uint32_t w, uint32_t& lo, ui
 // next 32 ahead of their use, so that no copy waits for a lookup (a lookup per
 // copy bound the pages of 16 tokens to 0.78 of the rate).  Tokens of a group
 // whose page is not valid are left out: its slices lose their bit.
-template <int D, int GT>
+template <int D, int GT, bool TEST>
 __device__ void producer8(const Decode8Params& p, Smem8<D>& sm, Walker wk, int64_t v1) {
   using R = Grp8<D, GT>;
   constexpr int C = chunk8<D>();
@@ -184,7 +195,7 @@ __device__ void producer8(const Decode8Params& p, Smem8<D>& sm, Walker wk, int64
                       p.flag);
     const uint32_t got = __ballot_sync(0xFFFFFFFFu, ok);
     bool live = true;
-    if (it >= (uint32_t)stages8<D>() && !mbar_wait(smem_addr(&sm.empty[s]), ((it / stages8<D>()) + 1) & 1)) {
+    if (it >= (uint32_t)stages8<D>() && !work_wait8<TEST>(p, smem_addr(&sm.empty[s]), ((it / stages8<D>()) + 1) & 1)) {
       set_flag(p.flag, KVQ_FLAG_TIMEOUT);
       *reinterpret_cast<volatile int*>(sm.abort) = 1;
       live = false;
@@ -474,7 +485,7 @@ __device__ __forceinline__ bool plan_short(const Decode8Params& p, uint32_t idx,
 // DIRECT: one CTA per unit, which walks all of its chunks and writes the result
 // itself (caches of few chunks); else the equal ranges and partials described
 // above.
-template <int D, int GT, bool DIRECT>
+template <int D, int GT, bool DIRECT, bool TEST>
 __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(const Decode8Params p) {
   using G = Geo8<D>;
   extern __shared__ uint8_t smem8_raw[];
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
   }
   if (v0 >= v1) return;
   if (warp == kB8Warps) {
-    producer8<D, GT>(p, sm, wk, v1);
+    producer8<D, GT, TEST>(p, sm, wk, v1);
     return;
   }
   const uint32_t stages = smem_addr(sm.stages);
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
     }
     if (dead) continue;
     const uint32_t s = it % stages8<D>();
-    bool ok = !*reinterpret_cast<volatile int*>(sm.abort) && mbar_wait(smem_addr(&sm.full[s]), (it / stages8<D>()) & 1);
+    bool ok = !*reinterpret_cast<volatile int*>(sm.abort) && work_wait8<TEST>(p, smem_addr(&sm.full[s]), (it / stages8<D>()) & 1);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (!ok) {
       dead = true;
@@ -571,13 +582,13 @@ __global__ void __launch_bounds__(kB8Threads, ctas8<D>()) decode_block8_kernel(c
 }
 
 // ------------------------------------------------------------------ host side
-template <int D, int GT, bool DIRECT>
+template <int D, int GT, bool DIRECT, bool TEST>
 kvq_status launch_decode8(const Decode8Params& dp, cudaStream_t s, int ctas) {
   static DeviceOnce attr_set;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
   if (attr_set.pending(dev)) {
-    if (cudaFuncSetAttribute(decode_block8_kernel<D, GT, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_block8_kernel<D, GT, DIRECT, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Geo8<D>::kSmemBytes) != cudaSuccess)
       return KVQ_ERR_CUDA;
     attr_set.mark(dev);
@@ -592,16 +603,17 @@ kvq_status launch_decode8(const Decode8Params& dp, cudaStream_t s, int ctas) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_block8_kernel<D, GT, DIRECT>, dp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, decode_block8_kernel<D, GT, DIRECT, TEST>, dp) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 template <int D, bool DIRECT>
 kvq_status launch_decode8_d(const Decode8Params& dp, cudaStream_t s, int ctas) {
   switch (dp.c.page_size) {
-    case 16: return launch_decode8<D, 16, DIRECT>(dp, s, ctas);
-    case 32: return launch_decode8<D, 32, DIRECT>(dp, s, ctas);
-    default: return launch_decode8<D, 64, DIRECT>(dp, s, ctas);
+    case 16: return launch_decode8<D, 16, DIRECT, false>(dp, s, ctas);
+    case 32: return launch_decode8<D, 32, DIRECT, false>(dp, s, ctas);
+    default: break;
   }
+  return dp.wait_ns == 0 ? launch_decode8<D, 64, DIRECT, false>(dp, s, ctas) : launch_decode8<D, 64, DIRECT, true>(dp, s, ctas);
 }
 
 // One CTA per unit, without partials and their merge, when the cache's capacity
@@ -666,6 +678,7 @@ extern "C" kvq_status kvq_fp8_block_decode_attn(const kvq_cache* cache, int32_t 
   dp.hq = num_q_heads;
   dp.qk_log2 = softmax_scale * kLog2e;
   dp.n_slots = n_slots;
+  dp.wait_ns = test_wait_limit_ns();
   if (units <= INT32_MAX &&
       (unit_chunks <= kDirectChunks || (unit_chunks <= kDirectChunksFull && units >= (int64_t)sms))) {
     dp.out = out;

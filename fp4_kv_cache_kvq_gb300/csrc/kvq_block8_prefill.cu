@@ -146,6 +146,7 @@ struct Prefill8Params {
   int32_t parts;   // partials per row: splits, or twice that for a pair
   uint32_t g_inv;  // 2^16 / g rounded up: row / g is row * g_inv >> 16 for rows < 512
   float qk_log2;
+  uint64_t wait_ns;  // a test's limit of the waits, or 0
 };
 
 template <int D>
@@ -165,8 +166,8 @@ struct P8Geo {
   static constexpr int kTokMul = kTokExp + kVSlots8 * kT;  // [128] a token's factor in V^, f16
   static constexpr int kNan = kTokMul + kT * 2;  // [D] per channel the first position (of the CTA's) whose value is NaN
   static constexpr int kBar = kNan + 4 * D;
-  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, first NaN, masks, exponents
-  static constexpr int kMiscEnd = kMisc + 4 * (3 + 3 * kKRing + kVRing);
+  static constexpr int kMisc = kBar + 8 * kBars8;        // TMEM slot, abort, first NaN, masks, exponents, ends
+  static constexpr int kMiscEnd = kMisc + 4 * (3 + 3 * kKRing + kVRing + 2 + 2 * kXTiles);
   // where a half's rows are turned for coalesced stores: 128 bytes a row.  At
   // head_dim 128 that is query memory that no product reads any more: the half's
   // own tile's, for a pair the second tile's, which holds no queries
@@ -180,22 +181,32 @@ struct P8Geo {
   static_assert(kBar % 8 == 0 && kBytes <= 227 * 1024, "shared-memory layout");
 };
 
-__device__ __forceinline__ bool pwait8(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *abort = 1;
-      return false;
+// A wait of the whole warp with one outcome (TMEM accesses are warp-collective); it
+// gives up after the library's limit, or with any other wait of the CTA.  TEST: the
+// instantiation with a test's limit, which polls (a suspending wait could outlast it).
+template <bool TEST>
+struct Waits {
+  volatile int* abort;
+  uint64_t limit;  // TEST, ns
+  __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) const {
+    return TEST ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  }
+  __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) const {
+    if (look(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (true) {
+      if (look(bar, parity)) return true;
+      if (*abort) return false;
+      if (global_ns() - t0 > (TEST ? limit : kWaitLimitNs)) {
+        *abort = 1;
+        return false;
+      }
     }
   }
-}
-// one outcome for the whole warp (TMEM accesses are warp-collective)
-__device__ __forceinline__ bool wwait8(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, pwait8(bar, parity, abort));
-}
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity));
+  }
+};
 
 __device__ __forceinline__ uint64_t pk2(float lo, float hi) {
   uint64_t r;
@@ -345,7 +356,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // PAIR: few rows: both halves of the CTA serve one query tile, every second cache
 // tile each.
-template <int D, int GT, bool PAIR>
+template <int D, int GT, bool PAIR, bool TEST>
 __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Prefill8Params p) {
   using G = P8Geo<D>;
   // K slots in use.  A pair's half sees every second tile only: with two slots it
@@ -362,9 +373,13 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
   uint32_t* tslot = misc;
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
+  const Waits<TEST> wait{abort, p.wait_ns};
   volatile uint32_t* kgood = misc + 3;             // [kKRing] bit i: block i of the tile lies in a valid page
   volatile uint32_t* vgood = misc + 3 + kKRing;    // [kVRing]
   volatile uint32_t* emin = misc + 3 + kKRing + kVRing;  // [2 kKRing] the smallest log2 sV of the tile; NaN: its tokens have exponents of their own
+  // what can still be on its way at the end: the loader's K and V tiles so far, and each
+  // MMA warp's last commit (barrier and parity)
+  volatile uint32_t* ends = misc + 3 + 3 * kKRing + kVRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int sp = (int)(blockIdx.x % (unsigned)p.splits);
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
   // The loader warp's copies of tile j: lane i < kGroups takes group i, K codes
   // and scales, then V codes and scales.  The lanes look up the groups of 32 /
   // kGroups tiles at once.
-  int kiss = 0, viss = 0;
+  int kiss = 0, viss = 0;  // tiles so far
   const uint8_t* src_l = nullptr;
   const auto load_tile = [&](int j) -> bool {
     const int ks = j % kRing, vs = j % kVRing;
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     for (int i = 0; i < kGroups; ++i)
       if ((got >> i) & 1u) good |= ((1u << (GT / 16)) - 1u) << (i * (GT / 16));
     const uint32_t bytes = (uint32_t)__popc(got) * (uint32_t)(GT * D + kGroupScale);
-    if (j >= kRing && !wwait8(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kRing - 1) & 1u, abort)) return false;
+    if (j >= kRing && !wait(bars + 8 * (kKEmpty + ks), (uint32_t)(j / kRing - 1) & 1u)) return false;
     if (lane == 0) {
       kgood[ks] = good;
       mbar_arrive_expect_tx(bars + 8 * (kKFull + ks), bytes);
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
                bars + 8 * (kKFull + ks));
     }
     kiss = j + 1;
-    if (j >= kVRing && !wwait8(bars + 8 * (kV8Empty + vs), (uint32_t)(j / kVRing - 1) & 1u, abort)) return false;
+    if (j >= kVRing && !wait(bars + 8 * (kV8Empty + vs), (uint32_t)(j / kVRing - 1) & 1u)) return false;
     if (lane == 0) {
       vgood[vs] = good;
       mbar_arrive_expect_tx(bars + 8 * (kV8Full + vs), bytes);
@@ -634,7 +649,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       // P is on its way to TMEM: O_X rescaled, P handed over, l.
       const auto finish = [&](bool any_up, float al, float al_l, float sum) -> bool {
         if (any_up && i_own > 0) {
-          if (!wwait8(pv_done, (i_own - 1) & 1u, abort)) return false;
+          if (!wait(pv_done, (i_own - 1) & 1u)) {
+            tmem_wait_st();  // P's stores end before the TMEM does
+            return false;
+          }
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -665,7 +683,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         float csk[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) csk[i] = csk_in[i];
-        if (!wwait8(s_full, i_own & 1u, abort)) return false;
+        if (!wait(s_full, i_own & 1u)) return false;
         tc_fence_after();
         // the row's 128 scores in registers, each block's maximum with them
         uint32_t v[8][16], vm[8];
@@ -728,7 +746,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       // once for the references and once for P (whose columns are those of scores that
       // have been taken).
       const auto tile_tokens = [&](int j, uint32_t good, uint32_t sc) -> bool {
-        if (!wwait8(s_full, i_own & 1u, abort)) return false;
+        if (!wait(s_full, i_own & 1u)) return false;
         tc_fence_after();
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
@@ -781,7 +799,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         // the tile's scales, ahead of its scores
         const int ks = j % kRing;
         const int is = j % (2 * kRing);
-        if (!(ok = wwait8(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u, abort))) break;
+        if (!(ok = wait(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u))) break;
         const uint32_t sc = sb + G::kSc + is * 64;
         float csk[8], lv[8], pc[8], pf[8];
 #pragma unroll
@@ -806,13 +824,13 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
         } else if (__builtin_expect(least == least, 1)) {
           ok = tile(std::true_type{}, j, good, csk, sc, pc, pf, held);
         } else {  // the tokens' exponents come with V^
-          if (!(ok = wwait8(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
+          if (!(ok = wait(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u))) break;
           ok = tile_tokens(j, good, sc);
         }
         if (!ok) break;
       }
       // the result once the last O_X += P_X V^ is done
-      if (ok) ok = wwait8(pv_done, (i_own - 1) & 1u, abort);
+      if (ok) ok = wait(pv_done, (i_own - 1) & 1u);
       if (ok) {
         tc_fence_after();
         const bool partial = p.parts > 1;
@@ -903,8 +921,8 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       const int s = j % kVRing, slot = j % kVSlots8;
       const uint32_t codes = sb + G::kV8 + s * kT * D, dst = sb + G::kV + slot * kT * D * 2;
       const int valid = (int)min((int64_t)kT, limit - (int64_t)(j0 + j) * kT);
-      if (!wwait8(bars + 8 * (kV8Full + s), (uint32_t)(j / kVRing) & 1u, abort)) break;
-      if (j >= kVSlots8 && !wwait8(bars + 8 * (kVEmpty + slot), (uint32_t)(j / kVSlots8 - 1) & 1u, abort)) break;
+      if (!wait(bars + 8 * (kV8Full + s), (uint32_t)(j / kVRing) & 1u)) break;
+      if (j >= kVSlots8 && !wait(bars + 8 * (kVEmpty + slot), (uint32_t)(j / kVSlots8 - 1) & 1u)) break;
       const uint32_t good = vgood[s];
       const bool whole = valid == kT && good == 0xFFu;
       const uint32_t c = dt % D;
@@ -953,7 +971,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           }
         }
         const int is = j % (2 * kRing);
-        if (!wwait8(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u, abort)) break;
+        if (!wait(bars + 8 * (kScFull + is), (uint32_t)(j / (2 * kRing)) & 1u)) break;
         if (emin[is] == 0x7FC00000u) {  // the tokens have exponents of their own
           // thread = token: its largest code
           const int blk = dt >> 4;
@@ -972,7 +990,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           sts8(sb + G::kTokExp + (uint32_t)(slot * kT + dt), zero ? 1u : e - (uint32_t)up);
           sts16(sb + G::kTokMul + (uint32_t)(2 * dt), (uint32_t)(up + 15) << 10);
           mbar_arrive(bars + 8 * kTok);
-          if (!wwait8(bars + 8 * kTok, looked++ & 1u, abort)) break;
+          if (!wait(bars + 8 * kTok, looked++ & 1u)) break;
 #pragma unroll 1
           for (int t0 = 16 * (dt / D); t0 < kT; t0 += 16 * (32 * kExpWarps / D)) {  // the thread's own items
 #pragma unroll
@@ -984,7 +1002,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           }
           // (one array of factors: every thread is done with it before the next such tile)
           mbar_arrive(bars + 8 * kTok);
-          if (!wwait8(bars + 8 * kTok, looked++ & 1u, abort)) break;
+          if (!wait(bars + 8 * kTok, looked++ & 1u)) break;
         }
       }
       __syncwarp();
@@ -998,17 +1016,9 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     // ------------------------------------------------------------ bulk copies
     for (int j = 0; j < ntiles; ++j)
       if (!load_tile(j)) break;
-    if (*abort) {  // copies still in flight land before the shared memory goes away
-      const auto drain = [&](int bar, int ring, int issued) {
-        for (int j = max(0, issued - ring); j < issued; ++j) {
-          const uint64_t t0 = global_ns();
-          while (!mbar_try_wait_hint(bars + 8 * (bar + j % ring), (uint32_t)(j / ring) & 1u, kPoll8) &&
-                 global_ns() - t0 < 20000000ull) {
-          }
-        }
-      };
-      drain(kKFull, kRing, kiss);
-      drain(kV8Full, kVRing, viss);
+    if (lane == 0) {
+      ends[0] = (uint32_t)kiss;
+      ends[1] = (uint32_t)viss;
     }
    } else if (warp == kScWarp) {
     // ------------------------------------------------------------ scales
@@ -1017,7 +1027,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     uint32_t least = 255u;  // the smallest exponent so far
     for (int j = 0; j < ntiles; ++j) {
       const int ks = j % kRing, is = j % (2 * kRing);
-      if (!wwait8(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u, abort)) break;
+      if (!wait(bars + 8 * (kKFull + ks), (uint32_t)(j / kRing) & 1u)) break;
       const uint2 sc = lds64(scale_at<GT>(sb + G::kKS + ks * kScaleBytes, lane & 7));
       const uint32_t e = v_exponent(sc.y), here = __reduce_min_sync(0xFFFFFFFFu, e);
       // (a scale of 2^-126 and less is that of zeros)
@@ -1060,10 +1070,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       }
       __syncwarp();
     };
-    uint32_t last_bar = 0, last_par = 0;
+    uint32_t last_bar = 0, last_par = 0;  // the last commit
     int j = PAIR ? x : 0;              // this half's first tile (x < nx <= ntiles for a pair)
     asm volatile("bar.sync 2, %0;\n" ::"r"(32 * (kSmWarps + nx)) : "memory");  // the queries are written
-    bool ok = wwait8(bars + 8 * (kKFull + j), 0u, abort);
+    bool ok = wait(bars + 8 * (kKFull + j), 0u);
     if (ok) {
       tc_fence_after();
       issue_s(j);
@@ -1073,12 +1083,12 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
     for (uint32_t i = 0; j < ntiles && ok; j += step, ++i) {
       const int jn = j + step, kr = jn % kRing, vslot = j % kVSlots8;
       const bool more = jn < ntiles;
-      if (more && !(ok = wwait8(bars + 8 * (kKFull + kr), (uint32_t)(jn / kRing) & 1u, abort))) break;
-      if (!(ok = wwait8(bars + 8 * (kVFull + vslot), (uint32_t)(j / kVSlots8) & 1u, abort))) break;
-      if (!(ok = wwait8(p_full, i & 1u, abort))) break;
+      if (more && !(ok = wait(bars + 8 * (kKFull + kr), (uint32_t)(jn / kRing) & 1u))) break;
+      if (!(ok = wait(bars + 8 * (kVFull + vslot), (uint32_t)(j / kVSlots8) & 1u))) break;
+      if (!(ok = wait(p_full, i & 1u))) break;
       // A(0), B(0), A(1), ..: the tiles take turns, so that one's softmax runs
       // beside the other's products
-      if (turns && (x > 0 || i > 0) && !(ok = wwait8(bars + 8 * (kTurn + x), (x > 0 ? i : i - 1) & 1u, abort))) break;
+      if (turns && (x > 0 || i > 0) && !(ok = wait(bars + 8 * (kTurn + x), (x > 0 ? i : i - 1) & 1u))) break;
       tc_fence_after();
       const uint64_t dv = dv0 + (uint64_t)(vslot * (kT * D * 2 / 16));
       if (elect_one()) {
@@ -1093,7 +1103,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       last_par = i & 1u;
       if (more) {
         // P lives in S's columns: the next scores follow the product that reads it
-        if (!(ok = wwait8(pv_done, i & 1u, abort))) break;
+        if (!(ok = wait(pv_done, i & 1u))) break;
         tc_fence_after();
         issue_s(kr);
         last_bar = s_full;
@@ -1101,17 +1111,35 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       }
       if (turns && lane == 0) mbar_arrive(bars + 8 * (kTurn + (x ^ 1)));
     }
-    if (*abort && last_bar != 0) {  // MMAs still running when the CTA gave up
-      const uint64_t t0 = global_ns();
-      while (!mbar_try_wait_hint(last_bar, last_par, kPoll8) && global_ns() - t0 < 20000000ull) {
-      }
+    if (lane == 0) {
+      ends[2 + 2 * x] = last_bar;
+      ends[3 + 2 * x] = last_par;
     }
    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && *abort) set_flag(p.flag, KVQ_FLAG_TIMEOUT);
+  // A wait gave up (every role is past its last one here, so the word is final): copies
+  // and products still on their way land before shared memory and TMEM go away.
+  if (*abort) {
+    const auto land = [&](uint32_t bar, uint32_t parity) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait_hint(bar, parity, kPoll8) && global_ns() - t0 < 20000000ull) {
+      }
+    };
+    if (warp == kLdWarp) {
+      const int k = (int)ends[0], v = (int)ends[1];
+      for (int j = max(0, k - kRing); j < k; ++j) land(bars + 8 * (kKFull + j % kRing), (uint32_t)(j / kRing) & 1u);
+      for (int j = max(0, v - kVRing); j < v; ++j) land(bars + 8 * (kV8Full + j % kVRing), (uint32_t)(j / kVRing) & 1u);
+    } else if (warp >= kMWarp && warp - kMWarp < nx && ends[2 + 2 * (warp - kMWarp)] != 0u) {
+      land(ends[2 + 2 * (warp - kMWarp)], ends[3 + 2 * (warp - kMWarp)]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) set_flag(p.flag, KVQ_FLAG_TIMEOUT);
+  }
   if (warp == 0) tmem_dealloc(tmem, kTmem8);
 }
 
@@ -1187,18 +1215,18 @@ size_t part_bytes(int64_t parts, int64_t rows, int d) {
   return parts > 1 ? (size_t)parts * (size_t)rows * (size_t)(d + 2) * sizeof(float) : 16;
 }
 
-template <int D, int GT, bool PAIR>
+template <int D, int GT, bool PAIR, bool TEST>
 kvq_status launch_prefill8(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
   static DeviceOnce attr_set;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
   if (attr_set.pending(dev)) {
-    if (cudaFuncSetAttribute(prefill_block8_kernel<D, GT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(prefill_block8_kernel<D, GT, PAIR, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              P8Geo<D>::kBytes) != cudaSuccess)
       return KVQ_ERR_CUDA;
     attr_set.mark(dev);
   }
-  prefill_block8_kernel<D, GT, PAIR><<<grid, kP8Threads, P8Geo<D>::kBytes, s>>>(pp);
+  prefill_block8_kernel<D, GT, PAIR, TEST><<<grid, kP8Threads, P8Geo<D>::kBytes, s>>>(pp);
   const kvq_status st = launch_status();
   if (st != KVQ_OK || pp.parts == 1) return st;
   const int64_t rows = (int64_t)pp.batch * pp.chunk * pp.hq;
@@ -1217,10 +1245,11 @@ kvq_status launch_prefill8(const Prefill8Params& pp, cudaStream_t s, unsigned gr
 template <int D, bool PAIR>
 kvq_status launch_prefill8_d(const Prefill8Params& pp, cudaStream_t s, unsigned grid) {
   switch (pp.c.page_size) {
-    case 16: return launch_prefill8<D, 16, PAIR>(pp, s, grid);
-    case 32: return launch_prefill8<D, 32, PAIR>(pp, s, grid);
-    default: return launch_prefill8<D, 64, PAIR>(pp, s, grid);
+    case 16: return launch_prefill8<D, 16, PAIR, false>(pp, s, grid);
+    case 32: return launch_prefill8<D, 32, PAIR, false>(pp, s, grid);
+    default: break;
   }
+  return pp.wait_ns == 0 ? launch_prefill8<D, 64, PAIR, false>(pp, s, grid) : launch_prefill8<D, 64, PAIR, true>(pp, s, grid);
 }
 
 }  // namespace
@@ -1291,6 +1320,7 @@ extern "C" kvq_status kvq_fp8_block_prefill_attn(const kvq_cache* cache, int32_t
   pp.nqb = (int32_t)nqb;
   pp.out_bf16 = out_dtype == KVQ_DTYPE_BF16;
   pp.qk_log2 = softmax_scale * 1.4426950408889634f;
+  pp.wait_ns = test_wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)(ctas * splits);
   if (pair) return D == 128 ? launch_prefill8_d<128, true>(pp, s, grid) : launch_prefill8_d<64, true>(pp, s, grid);

@@ -138,7 +138,7 @@ kvq_status decode_attn(const kvq_cache* global, const kvq_cache* swa, int32_t ba
   dp.head_dim = D;
   dp.pool_bytes = global->num_pages * (int64_t)hkv * global->page_size * 9 * D / 8;
   dp.n_slots = (int64_t)batch * hkv + ctas;
-  dp.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  dp.wait_ns = test_wait_limit_ns();
   dp.qk_log2 = softmax_scale * kLog2e;
   dp.k_new = fused ? static_cast<const uint16_t*>(k_new) : nullptr;
   dp.v_new = fused ? static_cast<const uint16_t*>(v_new) : nullptr;
@@ -267,3 +267,5 @@ extern "C" kvq_status kvq_decode_attn_noalloc(const kvq_cache* global, const kvq
 }
 
 extern "C" void kvq_test_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns, std::memory_order_relaxed); }
+
+uint64_t kvq::test_wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }

@@ -89,6 +89,9 @@ inline kvq_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+// The limit that kvq_test_set_wait_limit_ns has set, ns; 0: none (kvq_decode_api.cu).
+uint64_t test_wait_limit_ns();
+
 // kvq_append's FP4 / NVFP4 launches (kvq_append.cu): n_new tokens per
 // sequence from position start_pos[b] + sp_offset; sp_offset -1 reads the
 // lengths of a decode step (a zero length appends nothing).

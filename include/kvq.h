@@ -316,8 +316,11 @@ kvq_status kvq_decode_attn_tc(const kvq_cache *global, const kvq_cache *swa, int
  * about 2 s) for the copies it already issued, and the call's output is
  * undefined.  A non-zero limit selects a separate instantiation of the
  * kernel that reads the limit at run time; 0 selects the production one,
- * whose limit is a compile-time constant.  Process-wide; not for production
- * use.
+ * whose limit is a compile-time constant.  The attention over an 8-bit block
+ * cache (kvq_fp8_block_decode_attn, kvq_fp8_block_prefill_attn) takes the limit
+ * the same way for page sizes of 64 and more; there the prefill's CTA ends once
+ * its copies and products in flight have landed (each awaited for at most 20
+ * ms).  Process-wide; not for production use.
  */
 void kvq_test_set_wait_limit_ns(uint64_t ns);
 
