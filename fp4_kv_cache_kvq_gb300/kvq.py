@@ -289,14 +289,11 @@ class Fp8BlockCache:
                                       0, None, None, None, None, None)
 
     def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqCacheStruct:
-        """The kvq_cache description of the cache as it is now; a page_table
-        argument overrides the cache's own for one call."""
-        if page_table is not None:
-            return KvqCacheStruct(FORMAT_FP8_BLOCK, self.num_kv_heads, self.head_dim, self.page_size, self.num_pages,
-                                  self.max_pages_per_seq, 0, page_table.data_ptr(), self.pool.data_ptr(), None, None,
-                                  None)
-        s = self._struct
-        s.page_table, s.data = _ptr(self.page_table), self.pool.data_ptr()
+        """The kvq_cache description of the cache as it is now, a new one each time
+        (calls from several threads do not share it); a page_table argument
+        overrides the cache's own for one call."""
+        s = KvqCacheStruct.from_buffer_copy(self._struct)
+        s.page_table, s.data = _ptr(self.page_table if page_table is None else page_table), self.pool.data_ptr()
         return s
 
     @property
