@@ -208,17 +208,16 @@ class Fp4Cache:
         self.v_gscale = torch.ones(num_kv_heads, dtype=torch.float32, device=device) if nvfp4 else None
 
     def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqCacheStruct:
-        """The kvq_cache description (kept between calls while the tensors it
-        points at are the same objects; a page_table argument overrides the
-        cache's own for one call)."""
+        """The kvq_cache description (kept between calls while the pointers in
+        it are those of the tensors; a page_table argument overrides the cache's
+        own for one call)."""
         pt = self.page_table if page_table is None else page_table
-        key = (id(self.pool), id(pt), id(self.k_gscale), id(self.v_gscale))
+        key = (_ptr(pt), _ptr(self.pool), _ptr(self.k_gscale), _ptr(self.v_gscale))
         cached = self.__dict__.get("_struct")
         if cached is not None and cached[0] == key:
             return cached[1]
         s = KvqCacheStruct(FORMAT_NVFP4 if self.nvfp4 else FORMAT_FP4, self.num_kv_heads, self.head_dim,
-                           self.page_size, self.num_pages, self.max_pages_per_seq, 0, _ptr(pt), _ptr(self.pool),
-                           None, _ptr(self.k_gscale), _ptr(self.v_gscale))
+                           self.page_size, self.num_pages, self.max_pages_per_seq, 0, key[0], key[1], None, *key[2:])
         if page_table is None:
             self._struct = (key, s)
         return s
@@ -245,13 +244,13 @@ class Fp8WindowCache:
         self.v_scales = torch.ones_like(self.k_scales)
 
     def struct(self) -> KvqCacheStruct:
-        """The kvq_cache description (kept while the tensors are the same objects)."""
-        key = (id(self.k_codes), id(self.v_codes), id(self.k_scales), id(self.v_scales))
+        """The kvq_cache description (kept while the pointers in it are those of
+        the tensors)."""
+        key = (_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales), _ptr(self.v_scales))
         cached = self.__dict__.get("_struct")
         if cached is not None and cached[0] == key:
             return cached[1]
-        s = KvqCacheStruct(FORMAT_FP8, self.num_kv_heads, self.head_dim, self.window, self.num_seqs, 0, 0,
-                           None, _ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales), _ptr(self.v_scales))
+        s = KvqCacheStruct(FORMAT_FP8, self.num_kv_heads, self.head_dim, self.window, self.num_seqs, 0, 0, None, *key)
         self._struct = (key, s)
         return s
 
