@@ -10,7 +10,7 @@
 // for o: so codes enter the products as they are (E4M3 -> f16 is exact), and
 // a slice costs one multiply per score for sK and one FMA per accumulator for
 // sV, which also folds the slice's sum into o.  q is scaled by a power of two
-// per head, so its bf16 values are exact in f16; p = 2^(y - m) is rounded to
+// per head, so its bf16 values are exact in f16 down to 2^-31 of the row's largest; p = 2^(y - m) is rounded to
 // f16 (2^-11 relative) for the second product.
 //
 // What bounds it: HBM, 2 Hkv (d + 1/4) bytes a position against 4 Hq d flop.
@@ -254,6 +254,7 @@ __device__ __forceinline__ void begin_unit8(const Decode8Params& p, State8<D>& s
   amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
   // power-of-two prescale: max |q| * 2^k in [2^14, 2^15) keeps bf16 values exact in f16
+  // from 2^-17 up (f16's smallest step is 2^-24)
   int k = 0;
   if (amax > 0u && amax < 0x7F800000u) k = min(100, max(-113, 14 - ((int)(amax >> 23) - 127)));
   const float up = __uint_as_float((uint32_t)(k + 127) << 23);

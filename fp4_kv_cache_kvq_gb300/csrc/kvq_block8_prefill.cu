@@ -8,9 +8,9 @@
 //   O = sum P code_V,  l = sum P / sV,  out = O / l.
 // S takes the cached K codes as they are: q, scaled per row by a power of two
 // to [2^7, 2^8), is the sum of two E4M3 values hi = RNE(q) and lo = q - hi
-// (a bf16 value has 8 significant bits and an E4M3 value 4; lo is exact down
-// to 2^-10 of the row's largest element and off by at most 2^-18 of it under
-// that), so S = hi . K + lo . K are two fp8 products, which together cost one
+// (a bf16 value has 8 significant bits and an E4M3 value 4; lo, whose smallest step
+// is 2^-9, is exact down to 2^-9 of the row's largest element and off by at most
+// 2^-17 of it under that), so S = hi . K + lo . K are two fp8 products, which together cost one
 // f16 product and need no expansion of K.  The V scale of a block goes into P's
 // exponent, beside the softmax's own, so V^ is the codes themselves (exact in
 // f16; a scale that is no power of two leaves its significand, [1, 2), to V^,

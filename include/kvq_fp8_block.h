@@ -144,7 +144,10 @@ kvq_status kvq_fp8_block_dequant(const kvq_cache *cache, int32_t batch, const in
  * kvq_fp8_block_decode_attn -- kvq_decode_attn over an 8-bit block cache:
  *   out[b][h][:] = sum_t softmax_t(softmax_scale * q[b][h] . K^[b][t]) V^[b][t],
  * t = 0 .. d_seq_lens[b] - 1 (a length of 0 gives a zero row).  q enters the
- * products exactly, the weights as f16, sums and softmax statistics are fp32.
+ * products exactly down to 2^-31 of its row's largest element, and off by at
+ * most 2^-39 of that below (2^-125 in rows whose largest is under 2^-86); the
+ * weights as f16, off by at most 2^-11 of a weight or 2^-25 of the row's
+ * largest; sums and softmax statistics are fp32.
  *   num_q_heads  a multiple of num_kv_heads, at most 8 per kv head.
  *   q            device bf16 [batch][num_q_heads][head_dim], 16-byte aligned.
  *   out          device [batch][num_q_heads][head_dim] of out_dtype.
@@ -169,8 +172,9 @@ kvq_status kvq_fp8_block_decode_attn(const kvq_cache *cache, int32_t batch, int3
  *   num_q_heads  a multiple of num_kv_heads, at most 8 per kv head.
  *   q, out       device [batch][chunk][num_q_heads][head_dim], q bf16, out of
  *                out_dtype; 16-byte aligned.
- * q enters the products exactly or off by at most 2^-18 of its row's largest
- * element.  A weight enters the second product times its block's value scale, as
+ * q enters the products exactly down to 2^-9 of its row's largest element, and
+ * off by at most 2^-17 of that below (2^-110 in rows whose largest is under
+ * 2^-93).  A weight enters the second product times its block's value scale, as
  * f16: off by at most 2^-11 of that, or 2^-25 of the largest such product that
  * the row attends (a block flagged NONFINITE has a scale of 2^120, beside which
  * no other is seen).  Where scales differ by more than 2^10, a token of the last

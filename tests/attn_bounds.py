@@ -8,8 +8,9 @@ what the row sums up, not against the largest value of the cache:
             and a code is at most 448.
   scores    (d + 8) half steps of fp32 of sum |q_c k_c|, in the log2 domain; the
             prefill holds q in two E4M3 parts, off by at most 2^-17 of the
-            row's largest element.  A score off by e changes numerator and
-            denominator by ln 2 * e each.
+            row's largest element (scaled to 2^7 .. 2^8, half of a smallest step
+            of 2^-9), the decode in f16, 2^-39 (2^14 .. 2^15, 2^-24).  A score
+            off by e changes numerator and denominator by ln 2 * e each.
   sums      one half step of fp32 for each of the T / 16 products' sums, and
             2^-20 for the exponentials and the joins.
 """
@@ -40,10 +41,10 @@ def bound(q, k, v, p, scale, v_scale=None, out=torch.float32, ref=None, v_rel=0.
     x, kk, vv = q.double().abs(), k.double().abs(), v.double().abs()
     reach = (torch.einsum("rgd,td->rgt", x, kk) * seen).amax(-1)
     score = (d + 8) * 2.0 ** -24 * scale * LOG2E * reach
+    score = score + 2.0 ** (-39 if v_scale is None else -17) * scale * LOG2E * x.amax(-1) * (kk.sum(1) * seen).amax(-1)
     if v_scale is None:
         w, code = p, vv
     else:
-        score = score + 2.0 ** -17 * scale * LOG2E * x.amax(-1) * (kk.sum(1) * seen).amax(-1)
         w = p * v_scale.double()
         code = torch.where(v_scale[:, None] > 0, vv / v_scale.double().clamp(min=2.0 ** -149)[:, None], 0.0)
     small = seen & (w < 2.0 ** -14 * w.amax(-1, keepdim=True))

@@ -203,3 +203,26 @@ def test_nan_values_reach_the_rows_that_see_them(d, page, T, n, at, dtype):
                                     torch.maximum(seen_scale, V[0, :, h].abs().amax(-1).double() / 2 ** 5), dtype, ref)
             off = (out[0, i:i + 1, rows].double() - ref).abs()
             assert (off <= tol).all(), (h, i, (off / tol).max().item())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("small", [2.0 ** -10, 2.0 ** -14, 2.0 ** -33])
+def test_small_query_elements(d, small):
+    """Elements next to the last bit that a query keeps beside its row's largest, 1
+    (which meets zeros): scores of +-1 and +-4 come from them alone, so what they lose
+    shows.  small (1 + 2^-7) is off by 2^-17 of the largest in the prefill."""
+    T, H, G, n = 40, 1, 4, 6
+    cache = kvq.Fp8BlockCache(H, d, 64, 1, 1)
+    k = torch.zeros((1, T, H, d), device="cuda")
+    k[..., 5] = (torch.arange(T, device="cuda") % 2 * 2.0 - 1.0)[:, None] * math.sqrt(d) / small
+    v = torch.randn((1, T, H, d), generator=_gen(4), device="cuda")
+    kvq.append(cache, _ints([0]), k.to(BF), v.to(BF))
+    q = torch.zeros((1, n, H * G, d), device="cuda")
+    q[..., 0] = 1.0
+    q[..., 5] = small * torch.tensor([1 + 2.0 ** -7, 1 - 2.0 ** -8, 4 + 2.0 ** -5, -1 - 2.0 ** -6], device="cuda")
+    q = q.to(BF)
+    last = torch.arange(T - n, T)
+    out = kvq.prefill_attn(cache, _ints([T]), q)
+    check(cache, T, q[0], out[0], last)
+    dec = kvq.decode_attn(cache, _ints([T]), q[:, -1].contiguous())
+    check(cache, T, q[0, -1:], dec, last[-1:], prefill=False)
