@@ -1,11 +1,13 @@
 // kvq_block8_dequant.cu -- dense values of the 8-bit block cache.
 //
 // value = fp32(E4M3(code) * scale), the scale shared by the 16 tokens of a
-// block of one kv head.  Bound by HBM: one byte read per 2 or 4 written.  One
-// thread per 16 channels of one token: a K item is one 16-byte read; the V
-// bytes of a token lie 16 apart, so the 16 lanes that take the same channels
-// of a block's tokens read the same 256 bytes, which L1 serves after the first.
-// Lanes run over the channels first, so the stores of a row are contiguous.
+// block of one kv head.  One thread per 16 channels of one token: a K item is one
+// 16-byte read; the V bytes of a token lie 16 apart, so a thread reads single bytes
+// and each of a block's 16 tokens, num_kv_heads * head_dim / 16 threads apart, reads
+// the same 256 bytes again, from L1 or L2.  Lanes run over the channels first, so the
+// stores of a row are contiguous.  By its bytes HBM would bound it (one read per 2 or
+// 4 written); measured, 8 x 8192 positions of 8 heads of 128: 158 us to bf16, 2.56
+// TB/s (0.38 of the copy rate), 229 us to fp32, 2.93 TB/s (0.43).
 #include <cuda_bf16.h>
 
 #include "kvq_block8.cuh"

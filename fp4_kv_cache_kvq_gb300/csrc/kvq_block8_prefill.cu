@@ -42,22 +42,23 @@
 //             O_X += P_X(j) V^(j)                    kind::f16, P_X from TMEM
 //             the two tiles in turn: O_A(j), S_A(j+1), O_B(j), S_B(j+1)
 // Measured (1024 tokens over 16384 positions, 4 sequences, 64 query and 8 kv heads
-// of 128, page 64): 1.43 ms, 1.49 PFLOP/s, 0.78 of the bf16 GEMM rate.  From 2.09:
-// a row's scores in registers with the maxima that the TMEM load takes 1.99; the
-// issuing warp uniform 1.75; one issuing warp per query tile, in turns 1.67; the
-// running maximum raised only past 2^15 1.52; queries read by four lanes a row and
-// results stored through shared memory (a thread per row touches 32 lines an
-// access), and no CTA-wide wait before the first product 1.46; a kernel of its own
-// for pairs 1.43 (4096 tokens over nothing, 2 sequences: 548 -> 469 us).
-// Per tile of both query tiles 2980 cycles, 2048 of them products: each query
-// tile's chain is P V^ 890, S 890 (512 and a wait each), softmax 1090, and the other
-// tile's fills the gaps.  V's scales in P's exponent instead of a factor relative to
-// the largest of the CTA's positions: 1407 -> 1450 us (head_dim 64: 1200 -> 1224);
-// what follows from the scales alone is computed ahead of the scores, by one warp for
-// all rows where it does not depend on the row (1493 behind the scores, 1466 by every
-// row).  The form with exponents for single tokens beside it: 1468 (1247), in code that
-// these cases do not enter (1505 with every partly attended tile looked at).  The look for NaN
-// values: 1475 (1249).
+// of 128, page 64; calls in a row, L2 flushed): 1485 us, 1.43 PFLOP/s, 0.75 of the bf16
+// GEMM rate; 1560 us (0.71) among other kernels' calls.  head_dim 64: 1243.
+// From 2.09 ms: a row's scores in registers with the maxima that the TMEM load takes
+// 1.99; the issuing warp uniform 1.75; one issuing warp per query tile, in turns 1.67;
+// the running maximum raised only past 2^15 1.52; queries read by four lanes a row and
+// results stored through shared memory (a thread per row touches 32 lines an access),
+// and no CTA-wide wait before the first product 1.46; a kernel of its own for pairs 1.41.
+// What precision costs of that: V's scales in P's exponent instead of a factor relative
+// to the largest of the CTA's positions 1407 -> 1450 us (head_dim 64: 1200 -> 1224), with
+// what follows from the scales alone computed ahead of the scores, by one warp for all
+// rows where it does not depend on the row (1493 behind the scores, 1466 by every row);
+// the form with exponents for single tokens 1468 (1247), beside code that these cases do
+// not enter (1505 with every partly attended tile looked at); the look for NaN values
+// 1478 (1249).
+// Before these, a tile of both query tiles took 2980 cycles, 2048 of them products: each
+// query tile's chain was P V^ 890, S 890 (512 and a wait each), softmax 1090, and the
+// other tile's filled the gaps.
 // Slower: two threads per row 1.72; S of the next tile started before O of this
 // one's turn ends 1.58; P stored in halves with O started on the first 1.57; P in a
 // loop over TMEM instead of registers 1.58 (each against 1.52); S in two halves of
