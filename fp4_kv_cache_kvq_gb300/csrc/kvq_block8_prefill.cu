@@ -15,7 +15,7 @@
 // exponent, beside the softmax's own, so V^ is the codes themselves (exact in
 // f16; a scale that is no power of two leaves its significand, [1, 2), to V^,
 // rounded to f16 there).  P is rounded to f16: 2^-11 relative, or 2^-25 of 2^m',
-// where m' runs over the largest y + log2 sV that the row has attended.  So what
+// where m' is at most the largest y + log2 sV that the row has attended, rounded up.  So what
 // a row loses is measured by what it attends itself, and no value behind its last
 // position, however large, reaches it.  l takes P's fp32 value back to 2^(y - m),
 // m a second reference, with one factor per block: weights on blocks of tiny values

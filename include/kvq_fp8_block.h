@@ -175,7 +175,7 @@ kvq_status kvq_fp8_block_decode_attn(const kvq_cache *cache, int32_t batch, int3
  * q enters the products exactly down to 2^-9 of its row's largest element, and
  * off by at most 2^-17 of that below (2^-110 in rows whose largest is under
  * 2^-93).  A weight enters the second product times its block's value scale, as
- * f16: off by at most 2^-11 of that, or 2^-25 of the largest such product that
+ * f16: off by at most 2^-11 of that, or 2^-24 of the largest such product that
  * the row attends (a block flagged NONFINITE has a scale of 2^120, beside which
  * no other is seen).  Where scales differ by more than 2^10, a token of the last
  * 128 and more positions before the row's has its own largest value over 2^5 in

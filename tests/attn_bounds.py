@@ -2,10 +2,12 @@
 
 The bound counts the roundings of the 8-bit block cache's attention against
 what the row sums up, not against the largest value of the cache:
-  weights   f16, half a step: 2^-11 of a weight, or 2^-25 of the row's largest
-            one where that is more (weights under 2^-14 of it).  The prefill
-            rounds weight * value scale, so there the largest is that product's,
-            and a code is at most 448.
+  weights   f16, half a step: 2^-11 of a weight, or 2^-25 of the reference where
+            that is more (weights under 2^-14 of it).  The decode's reference is
+            at most the row's largest weight.  The prefill rounds weight * value
+            scale against a power of two that is at most twice the largest such
+            product that the row attends; what a product loses reaches the result
+            times the value's code, |v| over the scale.
   scores    (d + 8) half steps of fp32 of sum |q_c k_c|, in the log2 domain; the
             prefill holds q in two E4M3 parts, off by at most 2^-17 of the
             row's largest element (scaled to 2^7 .. 2^8, half of a smallest step
@@ -33,9 +35,10 @@ def attend(q, k, v, scale, last):
     return torch.einsum("rgt,td->rgd", p, v.double()), p
 
 
-def bound(q, k, v, p, scale, v_scale=None, out=torch.float32, ref=None, v_rel=0.0):
+def bound(q, k, v, p, scale, v_scale=None, out=torch.float32, ref=None, v_rel=0.0, v_least=None):
     """Largest |error| of each output element [rows][g][d]; v_scale [T]: the value
-    scales, given for the prefill; v_rel: a relative rounding of its values."""
+    scales, given for the prefill, or the most that they can be (v_least: the least;
+    v_scale when not given); v_rel: a relative rounding of its values."""
     d, T = k.shape[1], k.shape[0]
     seen = p > 0
     x, kk, vv = q.double().abs(), k.double().abs(), v.double().abs()
@@ -43,14 +46,17 @@ def bound(q, k, v, p, scale, v_scale=None, out=torch.float32, ref=None, v_rel=0.
     score = (d + 8) * 2.0 ** -24 * scale * LOG2E * reach
     score = score + 2.0 ** (-39 if v_scale is None else -17) * scale * LOG2E * x.amax(-1) * (kk.sum(1) * seen).amax(-1)
     if v_scale is None:
-        w, code = p, vv
+        most, code, top = p, vv, p.amax(-1, keepdim=True)
+        least = p
     else:
-        w = p * v_scale.double()
-        code = torch.where(v_scale[:, None] > 0, vv / v_scale.double().clamp(min=2.0 ** -149)[:, None], 0.0)
-    small = seen & (w < 2.0 ** -14 * w.amax(-1, keepdim=True))
+        v_least = v_scale if v_least is None else v_least
+        most, least = p * v_scale.double(), p * v_least.double()
+        code = torch.where(v_least[:, None] > 0, vv / v_least.double().clamp(min=2.0 ** -149)[:, None], 0.0)
+        top = 2 * most.amax(-1, keepdim=True)
+    small = seen & (least < 2.0 ** -14 * top)
     total = torch.einsum("rgt,td->rgd", p, vv)
     e = total * (2.0 ** -11 + v_rel + (2 * math.log(2) * score + T / 16 * 2.0 ** -24 + 2.0 ** -20)[..., None])
-    e = e + 2.0 ** -25 * w.amax(-1)[..., None] * torch.einsum("rgt,td->rgd", small.double(), code)
+    e = e + 2.0 ** -25 * top * torch.einsum("rgt,td->rgd", small.double(), code)
     if out == torch.bfloat16:
         e = e + 2.0 ** -8 * (ref.abs() + e)
     return e

@@ -152,11 +152,12 @@ def test_a_larger_value_in_the_same_block(d, page, T, n, larger, behind):
     for h in range(H):
         rows = slice(h * G, (h + 1) * G)
         x, vmax = q[0, :, rows], V[0, :, h].abs().amax(-1).double()
-        own = vmax / 2.0 ** 5                                  # a token with an exponent of its own: its values under 2^6 of it
-        vs = torch.where(part.cuda(), own, torch.maximum(value_scales(cache, T)[:, h].double(), own))
+        own = vmax / 2.0 ** 5                                  # a token's own exponent: at most this, and over half of it
+        block = value_scales(cache, T)[:, h].double()
+        vs, least = torch.where(part.cuda(), own, torch.maximum(block, own)), torch.minimum(block, own / 2)
         want, p = attn_bounds.attend(x, K[0, :, h], V[0, :, h], 1 / math.sqrt(d), last)
         for i in range(n):
-            tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d), vs[i])
+            tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d), vs[i], v_least=least)
             off = (out[0, i:i + 1, rows].double() - want[i:i + 1]).abs()
             assert (off <= tol).all(), (h, i, (off / tol).max().item())
             dec_tol = attn_bounds.bound(x[i:i + 1], K[0, :, h], V[0, :, h], p[i:i + 1], 1 / math.sqrt(d))
@@ -193,14 +194,16 @@ def test_nan_values_reach_the_rows_that_see_them(d, page, T, n, at, dtype):
     V = V.nan_to_num(0.0)
     for h in range(H):
         rows = slice(h * G, (h + 1) * G)
-        seen_scale = value_scales(cache, T)[:, h].clone().double()
-        seen_scale[at // 16 * 16:at // 16 * 16 + 16] = V[0, at // 16 * 16:at // 16 * 16 + 16, h].abs().amax(-1).double() / 2 ** 5
+        own = V[0, :, h].abs().amax(-1).double() / 2 ** 5      # a token's own exponent, as above
+        block = value_scales(cache, T)[:, h].double()
+        most = torch.maximum(block, own)
+        most[at // 16 * 16:at // 16 * 16 + 16] = own[at // 16 * 16:at // 16 * 16 + 16]
         for i in range(n):
             if h == 1 and sees[i]:
                 continue
             ref, p = attn_bounds.attend(q[0, i:i + 1, rows], K[0, :, h], V[0, :, h], 1 / math.sqrt(d), last[i:i + 1])
-            tol = attn_bounds.bound(q[0, i:i + 1, rows], K[0, :, h], V[0, :, h], p, 1 / math.sqrt(d),
-                                    torch.maximum(seen_scale, V[0, :, h].abs().amax(-1).double() / 2 ** 5), dtype, ref)
+            tol = attn_bounds.bound(q[0, i:i + 1, rows], K[0, :, h], V[0, :, h], p, 1 / math.sqrt(d), most, dtype, ref,
+                                    v_least=torch.minimum(block, own / 2))
             off = (out[0, i:i + 1, rows].double() - ref).abs()
             assert (off <= tol).all(), (h, i, (off / tol).max().item())
 
