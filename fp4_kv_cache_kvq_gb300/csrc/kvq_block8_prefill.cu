@@ -749,6 +749,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
       const auto tile_tokens = [&](int j, uint32_t good, uint32_t sc) -> bool {
         if (!wait(s_full, i_own & 1u)) return false;
         tc_fence_after();
+        // The tokens' exponents come with V^.  Behind the scores: they follow this half's
+        // last product, so the slot's phase before this tile's is over (ahead of them a
+        // pair's half could find the barrier a whole phase behind, and pass).
+        if (!wait(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u)) return false;
         const int64_t p0 = (int64_t)(j0 + j) * kT;
         const int lim = row_ok ? (int)min((int64_t)kT, max((int64_t)0, pos_r - p0 + 1)) : 0;
         const uint32_t tok = sb + G::kTokExp + (uint32_t)(j % kVSlots8 * kT);
@@ -824,8 +828,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) prefill_block8_kernel(const Pre
           ok = tile(std::false_type{}, j, good, csk, sc, pc, pf, held);
         } else if (__builtin_expect(least == least, 1)) {
           ok = tile(std::true_type{}, j, good, csk, sc, pc, pf, held);
-        } else {  // the tokens' exponents come with V^
-          if (!(ok = wait(bars + 8 * (kVFull + j % kVSlots8), (uint32_t)(j / kVSlots8) & 1u))) break;
+        } else {
           ok = tile_tokens(j, good, sc);
         }
         if (!ok) break;

@@ -229,3 +229,31 @@ def test_small_query_elements(d, small):
     check(cache, T, q[0], out[0], last)
     dec = kvq.decode_attn(cache, _ints([T]), q[:, -1].contiguous())
     check(cache, T, q[0, -1:], dec, last[-1:], prefill=False)
+
+
+@pytest.mark.parametrize("d,T,n", [(128, 2569, 10), (64, 1290, 12), (128, 3 * 128 + 9, 10), (64, 5 * 128 + 40, 40)])
+def test_token_exponents_repeat(d, T, n):
+    """A pair whose half meets a tile with exponents of single tokens as its second or a
+    later one, in many CTAs at once: every call gives the first one's bits."""
+    B, H, G, page = 5, 3, 3, 64
+    mp = -(-T // page)
+    cache = kvq.Fp8BlockCache(H, d, page, B * mp, mp)
+    k, v = (torch.randn((B, T, H, d), generator=_gen(20 + i), device="cuda") for i in range(2))
+    v *= torch.exp2(25 * torch.randn((B, -(-T // 16), H, 1), generator=_gen(22), device="cuda")).repeat_interleave(16, 1)[:, :T]
+    v = v.clamp(-1e30, 1e30)
+    kvq.append(cache, _ints([0] * B), k.to(BF), v.to(BF))
+    q = torch.randn((B, n, H * G, d), generator=_gen(23), device="cuda").to(BF)
+    lens = _ints([T - 3 * b for b in range(B)])
+    first = kvq.prefill_attn(cache, lens, q)
+    noise = torch.empty(1 << 26, device="cuda")
+    for i in range(200):
+        if i % 2:
+            noise.fill_(float(i))  # the caches out of L2, so that copies come late
+        assert torch.equal(kvq.prefill_attn(cache, lens, q), first)
+    K, V = kvq.dequant(cache, lens, T)
+    for b in range(B):
+        L = T - 3 * b
+        for i in (0, n - 1):
+            want, p = attn_bounds.attend(q[b, i:i + 1, :G], K[b, :L, 0], V[b, :L, 0], 1 / math.sqrt(d), torch.tensor([L - n + i]))
+            off = (first[b, i, :G].double() - want[0]).norm(dim=-1) / want[0].norm(dim=-1)
+            assert (off < 0.02).all()
