@@ -177,13 +177,14 @@ kvq_status kvq_fp8_block_decode_attn(const kvq_cache *cache, int32_t batch, int3
  * 2^-93).  A weight enters the second product times its block's value scale, as
  * f16: off by at most 2^-11 of that, or 2^-24 of the largest such product that
  * the row attends (a block flagged NONFINITE has a scale of 2^120, beside which
- * no other is seen).  Where scales differ by more than 2^10, a token of the last
- * 128 and more positions before the row's has its own largest value over 2^5 in
- * the place of its block's scale, which a token behind the row may have set.
- * Value codes enter exactly; a value scale that is no power of two (the append
- * makes none) is off by at most 2^-11, and so is its product with a code.  No
- * value behind a row's last position, NaN neither, reaches the row, but for what
- * the append made of the block that they share.
+ * no other is seen).  A block that a row attends in part can owe its scale to a
+ * token behind the row: where the value scales read differ by more than 2^10,
+ * the tokens of such a tile of 128 positions have each its own largest value
+ * over 2^5 in the place of its block's scale.  Value codes enter exactly; a
+ * value scale that is no power of two (the append makes none) is off by at most
+ * 2^-11, and so is its product with a code.  No value behind a row's last
+ * position, NaN neither, reaches the row, but for what the append made of the
+ * block that they share.
  *   workspace    kvq_fp8_block_prefill_workspace_bytes(...) bytes, 16-byte
  *                aligned, not shared by calls that may overlap.
  * Device flags: BAD_LENGTH (n_b outside 0..chunk: the sequence is skipped;
