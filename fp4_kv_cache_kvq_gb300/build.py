@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
 SOURCES = ["kvq_append.cu", "kvq_dequant.cu", "kvq_decode.cu", "kvq_decode_test_wait.cu", "kvq_decode_tc.cu", "kvq_merge.cu", "kvq_decode_api.cu", "kvq_sweep.cu", "kvq_prefill.cu", "kvq_replay.cu",
-           "kvq_rope_append.cu", "kvq_block8_dequant.cu", "kvq_block8_decode.cu", "kvq_block8_prefill.cu"]
+           "kvq_rope_append.cu", "kvq_block8_dequant.cu", "kvq_block8_decode.cu", "kvq_block8_prefill.cu",
+           "kvq_latent_append.cu", "kvq_latent_attn.cu", "kvq_expanded_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177"]
@@ -38,7 +39,7 @@ def _stale(lib: str) -> bool:
         return True
     t = os.path.getmtime(lib)
     inputs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
-        os.path.join(HERE, "..", "include", "kvq.h"), os.path.join(HERE, "..", "include", "kvq_fp8_block.h"),
+        os.path.join(HERE, "..", "include", h) for h in ("kvq.h", "kvq_fp8_block.h", "kvq_latent.h")] + [
         os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in inputs if os.path.exists(p))
 

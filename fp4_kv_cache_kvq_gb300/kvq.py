@@ -1,5 +1,5 @@
-"""Thin Python binding of libkvq (the C ABI declared in include/kvq.h and
-include/kvq_fp8_block.h).
+"""Thin Python binding of libkvq (the C ABI declared in include/kvq.h,
+include/kvq_fp8_block.h and include/kvq_latent.h).
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libkvq.so.  PyTorch is used for device memory and streams.  There is no CPU
@@ -10,7 +10,9 @@ Names follow the header: ``append`` (kvq_append), ``fp8_set_scales``
 (kvq_dequant), ``decode_workspace_bytes`` (kvq_decode_workspace_bytes),
 ``rope_append`` (kvq_rope_append).  ``append``, ``decode_attn``,
 ``prefill_attn`` and ``dequant`` take an ``Fp8BlockCache`` as well and then call
-kvq_fp8_block_append, _decode_attn, _prefill_attn and _dequant.
+kvq_fp8_block_append, _decode_attn, _prefill_attn and _dequant; the last three
+take a ``LatentCache`` too (kvq_latent_attn, kvq_latent_dequant), which
+``latent_append`` fills.  ``expanded_attn`` is kvq_expanded_attn.
 """
 from __future__ import annotations
 
@@ -66,8 +68,21 @@ class KvqCacheStruct(ctypes.Structure):
     ]
 
 
+class KvqLatentStruct(ctypes.Structure):
+    _fields_ = [
+        ("latent_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("data", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _CP = ctypes.POINTER(KvqCacheStruct)
+_LP = ctypes.POINTER(KvqLatentStruct)
 _I32, _I64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
@@ -137,6 +152,20 @@ def load() -> ctypes.CDLL:
             L.kvq_fp8_block_prefill_attn.restype = ctypes.c_int
             L.kvq_fp8_block_prefill_attn.argtypes = [_CP, _I32, _I32, _I32, _P, _P, _P, _F, _P, _I32, _P,
                                                      ctypes.c_size_t, _P, _P]
+            L.kvq_latent_pool_bytes.restype = ctypes.c_size_t
+            L.kvq_latent_pool_bytes.argtypes = [_I64, _I32, _I32, _I32]
+            L.kvq_latent_append.restype = ctypes.c_int
+            L.kvq_latent_append.argtypes = [_LP, _I32, _I32, _P, _P, _I32, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                            _I32, _P, _I64, _I64, _P, _P, _P]
+            L.kvq_latent_dequant.restype = ctypes.c_int
+            L.kvq_latent_dequant.argtypes = [_LP, _I32, _P, _I32, _I32, _P, _P, _P, _P]
+            L.kvq_latent_attn_workspace_bytes.restype = ctypes.c_size_t
+            L.kvq_latent_attn_workspace_bytes.argtypes = [_I32] * 4
+            L.kvq_latent_attn.restype = ctypes.c_int
+            L.kvq_latent_attn.argtypes = [_LP, _I32, _I32, _I32, _P, _P, _P, _F, _P, _I32, _P, ctypes.c_size_t, _P, _P]
+            L.kvq_expanded_attn.restype = ctypes.c_int
+            L.kvq_expanded_attn.argtypes = [_I32] * 6 + [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _F, _P,
+                                                         _I32, _P, _P]
             _lib = L
     return _lib
 
@@ -300,14 +329,55 @@ class Fp8BlockCache:
         return self.pool.numel()
 
 
+class LatentCache:
+    """8-bit paged cache of one latent vector per token, key and value of all
+    heads at once, and of the key's rotated position part: E4M3 codes (two per
+    value of the position part) with one power-of-two scale per token.
+    latent_dim 128, 256 or 512, rope_dim 32 or 64.
+
+    pool  uint8 [num_pages][page_size / G][G * (latent_dim + 2 * rope_dim + 1)],
+          G = min(page_size, 64) (the byte layout is documented in
+          include/kvq_latent.h); one given by the caller is used as it is.
+    page_table int32 [batch][max_pages_per_seq] or None (contiguous).
+    """
+
+    def __init__(self, latent_dim: int, rope_dim: int, page_size: int, num_pages: int, max_pages_per_seq: int,
+                 page_table: Optional[torch.Tensor] = None, device="cuda", pool: Optional[torch.Tensor] = None):
+        self.latent_dim, self.rope_dim, self.page_size = latent_dim, rope_dim, page_size
+        self.num_pages, self.max_pages_per_seq = num_pages, max_pages_per_seq
+        self.group = min(page_size, 64)
+        nbytes = load().kvq_latent_pool_bytes(num_pages, page_size, latent_dim, rope_dim)
+        if nbytes == 0:
+            raise ValueError("invalid latent cache geometry (latent_dim 128/256/512, rope_dim 32/64, page_size 16..256)")
+        shape = (num_pages, page_size // self.group, self.group * (latent_dim + 2 * rope_dim + 1))
+        if pool is None:
+            pool = torch.zeros(shape, dtype=torch.uint8, device=device)
+        _need(pool, torch.uint8, "pool")
+        if tuple(pool.shape) != shape:
+            raise ValueError(f"pool must have shape {shape}")
+        if page_table is not None:
+            _need_table(page_table, max_pages_per_seq)
+        self.pool, self.page_table = pool, page_table
+
+    def struct(self, page_table: Optional[torch.Tensor] = None) -> KvqLatentStruct:
+        """The kvq_latent_cache description of the cache as it is now, a new one
+        each time; a page_table argument overrides the cache's own for one call."""
+        return KvqLatentStruct(self.latent_dim, self.rope_dim, self.page_size, self.max_pages_per_seq, self.num_pages,
+                               _ptr(self.page_table if page_table is None else page_table), self.pool.data_ptr())
+
+    @property
+    def nbytes(self) -> int:
+        return self.pool.numel()
+
+
 def _need_table(t: torch.Tensor, max_pages: int) -> None:
     _need(t, torch.int32, "page_table")
     if t.dim() != 2 or t.shape[1] != max_pages:
         raise ValueError("page_table must have shape [batch, max_pages_per_seq]")
 
 
-# Checks of the calls on an Fp8BlockCache and of rope_append: a few hundred
-# nanoseconds each, since a decode step makes them once a layer.
+# Checks of the calls on an Fp8BlockCache or LatentCache and of rope_append: a few
+# hundred nanoseconds each, since a decode step makes them once a layer.
 def _device(cache) -> int:
     """The cache's device, which has to be the current one."""
     dev = cache.pool.get_device()
@@ -482,6 +552,85 @@ def rope_append(cache, start_pos: torch.Tensor, q: Optional[torch.Tensor], k: to
     return q_out
 
 
+def _row_strides(dev: int, t: torch.Tensor, name: str, heads: bool):
+    """Elements from token to token and from head to head of a bf16
+    [batch][n][heads][width] (or [batch][n][width]) tensor whose rows are
+    contiguous and whose tokens are evenly spaced, and its shape."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or len(shape) != (4 if heads else 3):
+        raise ValueError(f"{name} must be a bfloat16 tensor [batch, n, {'heads, ' if heads else ''}width] on cuda:{dev}")
+    B, n, H, w = shape if heads else (shape[0], shape[1], 1, shape[2])
+    if t.is_contiguous():
+        return H * w, w, shape
+    st = t.stride()
+    sb, sn, sh, sw = st if heads else (st[0], st[1], w, st[2])
+    if H == 1:
+        sh = w
+    step = sn if n > 1 else sb if B > 1 else H * max(sh, w)
+    if t.numel() and not (sw == 1 and sh >= w and step >= (H - 1) * sh + w and (n == 1 or B == 1 or sb == n * sn)):
+        raise ValueError(f"{name}: rows must be contiguous, heads and tokens evenly spaced and without overlap")
+    return step, sh, shape
+
+
+def latent_append(cache: LatentCache, start_pos: torch.Tensor, q: Optional[torch.Tensor], c: torch.Tensor,
+                  k: torch.Tensor, table: Optional[torch.Tensor], interleaved: bool = False,
+                  new_lens: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None,
+                  page_table: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """kvq_latent_append: rotate the query parts q, bf16 [batch][n_new][heads][rope_dim],
+    and key parts k, bf16 [batch][n_new][rope_dim], by their positions start_pos[b]
+    + t and append latents c, bf16 [batch][n_new][latent_dim], and key parts to a
+    LatentCache.  Returns the rotated query parts (q_out, made when not given; None
+    without q); k_out, when given, receives the rotated key parts.  q, c, k and q_out
+    may be parts of larger tensors (a packed projection; the tails of the absorbed
+    queries, which is where q_out belongs for decode_attn and prefill_attn).  table:
+    rope_table(n, rope_dim, ...); None: no rotation.  new_lens, int32 [batch]: the new
+    tokens of each sequence of a padded batch."""
+    if not isinstance(cache, LatentCache):
+        raise ValueError("latent_append needs a LatentCache")
+    dev = _device(cache)
+    L, R = cache.latent_dim, cache.rope_dim
+    (cs, _, shape), (ks, _, k_shape) = _row_strides(dev, c, "c", False), _row_strides(dev, k, "k", False)
+    B, n, w = shape
+    if w != L or k_shape[0] != B or k_shape[1] != n or k_shape[2] != R:
+        raise ValueError("c and k must have shape [batch, n_new, latent_dim] and [batch, n_new, rope_dim]")
+    hq = qt = qh = ot = oh = 0
+    q_ptr = out_ptr = None
+    if q is not None:
+        qt, qh, q_shape = _row_strides(dev, q, "q", True)
+        hq = q_shape[2]
+        if q_shape[0] != B or q_shape[1] != n or hq < 1 or q_shape[3] != R:
+            raise ValueError("q must have shape [batch, n_new, num_q_heads, rope_dim]")
+        if q_out is None:
+            q_out = _alloc(stream, q_shape, torch.bfloat16, dev)
+        ot, oh, o_shape = _row_strides(dev, q_out, "q_out", True)
+        if o_shape != q_shape:
+            raise ValueError("q_out must have q's shape")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        _on(dev, k_out, torch.bfloat16, "k_out")
+        if k_out.shape != k_shape:
+            raise ValueError("k_out must have k's shape")
+    rows = 0
+    if table is not None:
+        _on(dev, table, torch.float32, "table")
+        if table.dim() != 2 or table.shape[1] != R:
+            raise ValueError("table must have shape [positions, rope_dim]")
+        rows = table.shape[0]
+    _table_rows(dev, cache, page_table, B)
+    _per_seq(dev, start_pos, B, "start_pos")
+    if new_lens is not None:
+        _per_seq(dev, new_lens, B, "new_lens")
+    s = cache.struct(page_table)
+    st = load().kvq_latent_append(ctypes.byref(s), B, n, start_pos.data_ptr(), _ptr(new_lens), hq, q_ptr, qt, qh,
+                                  c.data_ptr(), cs, k.data_ptr(), ks, _ptr(table), rows, 1 if interleaved else 0,
+                                  out_ptr, ot, oh, _ptr(k_out), _err_ptr(dev, err), _stream_on(dev, stream))
+    _check(st, "kvq_latent_append")
+    return q_out
+
+
 def fp8_set_scales(cache, k: torch.Tensor, v: torch.Tensor,
                    err: Optional[torch.Tensor] = None, stream=None) -> None:
     """kvq_fp8_set_scales over k, v bf16 [batch][n][Hkv][D]: an FP8 window
@@ -507,9 +656,16 @@ def decode_attn(cache: Fp4Cache, seq_lens: torch.Tensor, q: torch.Tensor, softma
     kernel="tcgen05" calls kvq_decode_attn_tc instead (head_dim 128: both
     products on the tensor-memory MMA; a measured, slower alternative).
     An Fp8BlockCache (kvq_fp8_block_decode_attn) takes a float32 or bfloat16
-    out and neither swa nor kernel="tcgen05"."""
+    out and neither swa nor kernel="tcgen05".  So does a LatentCache
+    (kvq_latent_attn), with q [batch][Hq][latent_dim + rope_dim], out
+    [batch][Hq][latent_dim], a workspace of latent_workspace_bytes(...) bytes and a
+    softmax_scale, which the latent does not show."""
     if kernel not in ("mma", "tcgen05"):
         raise ValueError(f"unknown decode kernel {kernel!r}")
+    if isinstance(cache, LatentCache):
+        if swa is not None or kernel != "mma":
+            raise ValueError("a LatentCache takes neither swa nor kernel=\"tcgen05\"")
+        return _attend_latent(cache, seq_lens, q, softmax_scale, out, err, stream, None, workspace, False)
     if isinstance(cache, Fp8BlockCache):
         if swa is not None or kernel != "mma":
             raise ValueError("an Fp8BlockCache takes neither swa nor kernel=\"tcgen05\"")
@@ -632,6 +788,80 @@ def _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_l
     return out
 
 
+def latent_workspace_bytes(batch: int, num_q_heads: int, latent_dim: int, chunk: int = 1) -> int:
+    """kvq_latent_attn_workspace_bytes."""
+    return int(load().kvq_latent_attn_workspace_bytes(batch, num_q_heads, latent_dim, chunk))
+
+
+def _out_like(dev: int, out: Optional[torch.Tensor], shape, zero: bool, stream):
+    """(out, its KVQ_DTYPE_*), made as float32 when not given."""
+    if out is None:  # rows of a padded batch's padding are not written
+        out = _alloc(stream, shape, torch.float32, dev, zero=zero)
+    code = _OUT_DTYPES.get(out.dtype)
+    if code is None or out.get_device() != dev or not out.is_contiguous() or out.shape != shape:
+        raise ValueError(f"out must be a contiguous float32 or bfloat16 tensor of shape {list(shape)} on cuda:{dev}")
+    return out, code
+
+
+def _attend_latent(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace, chunked) -> torch.Tensor:
+    dev = _device(cache)
+    shape = q.shape
+    if len(shape) != (4 if chunked else 3) or shape[-1] != cache.latent_dim + cache.rope_dim:
+        raise ValueError(f"q must have shape [batch, {'chunk, ' if chunked else ''}num_q_heads, latent_dim + rope_dim]")
+    if softmax_scale is None:
+        raise ValueError("a LatentCache needs softmax_scale")
+    _on(dev, q, torch.bfloat16, "q")
+    out, code = _out_like(dev, out, shape[:-1] + (cache.latent_dim,), chunk_lens is not None, stream)
+    B, chunk, hq = shape[0], shape[1] if chunked else 1, shape[-2]
+    _per_seq(dev, seq_lens, B, "seq_lens")
+    if chunk_lens is not None:
+        _per_seq(dev, chunk_lens, B, "chunk_lens")
+    _table_rows(dev, cache, None, B)
+    ws = _workspace(dev, workspace, stream, latent_workspace_bytes, B, hq, cache.latent_dim, chunk)
+    s = cache.struct()
+    st = load().kvq_latent_attn(ctypes.byref(s), B, hq, chunk, seq_lens.data_ptr(), _ptr(chunk_lens), q.data_ptr(),
+                                float(softmax_scale), out.data_ptr(), code, ws.data_ptr(), ws.nbytes,
+                                _err_ptr(dev, err), _stream_on(dev, stream))
+    _check(st, "kvq_latent_attn")
+    return out
+
+
+def expanded_attn(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,
+                  softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  err: Optional[torch.Tensor] = None, stream=None,
+                  chunk_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """kvq_expanded_attn: causal attention of a chunk over keys and values multiplied
+    out per head.  q bf16 [batch][chunk][heads][d + 64], k and v bf16
+    [batch][max_len][heads][d] (parts of one packed projection as they are), k_rope
+    bf16 [batch][max_len][64], shared by the heads, rotated as q's last 64 values are;
+    sequence b holds seq_lens[b] positions, the chunk's included.  Returns out
+    [batch][chunk][heads][d], float32 unless a bfloat16 out is given.  chunk_lens,
+    int32 [batch]: the chunk's tokens of each sequence of a padded batch, whose other
+    rows of out are left as they were (0 in an out made here)."""
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"q must be on the current device, cuda:{torch.cuda.current_device()}")
+    _on(dev, q, torch.bfloat16, "q")
+    (kt, kh, shape), (vt, vh, v_shape) = _row_strides(dev, k, "k", True), _row_strides(dev, v, "v", True)
+    rt, _, r_shape = _row_strides(dev, k_rope, "k_rope", False)
+    if q.dim() != 4:
+        raise ValueError("q must have shape [batch, chunk, heads, head_dim + rope_dim]")
+    B, chunk, H, w = q.shape
+    d, T = shape[3], shape[1]
+    if shape != v_shape or shape[0] != B or shape[2] != H or tuple(r_shape) != (B, T, w - d):
+        raise ValueError("k and v must have shape [batch, max_len, heads, head_dim], k_rope [batch, max_len, rope_dim]")
+    out, code = _out_like(dev, out, q.shape[:-1] + (d,), chunk_lens is not None, stream)
+    _per_seq(dev, seq_lens, B, "seq_lens")
+    if chunk_lens is not None:
+        _per_seq(dev, chunk_lens, B, "chunk_lens")
+    st = load().kvq_expanded_attn(B, H, d, w - d, chunk, T, seq_lens.data_ptr(), _ptr(chunk_lens), q.data_ptr(),
+                                  k.data_ptr(), kt, kh, k_rope.data_ptr(), rt, v.data_ptr(), vt, vh,
+                                  1.0 / math.sqrt(w) if softmax_scale is None else float(softmax_scale),
+                                  out.data_ptr(), code, _err_ptr(dev, err), _stream_on(dev, stream))
+    _check(st, "kvq_expanded_attn")
+    return out
+
+
 def prefill_attn(cache, seq_lens: torch.Tensor, q: torch.Tensor, softmax_scale: Optional[float] = None,
                  out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None,
                  chunk_lens: Optional[torch.Tensor] = None,
@@ -641,7 +871,12 @@ def prefill_attn(cache, seq_lens: torch.Tensor, q: torch.Tensor, softmax_scale: 
     An Fp8BlockCache (kvq_fp8_block_prefill_attn) takes a float32 or bfloat16
     out, a workspace of prefill_workspace_bytes(...) bytes, and chunk_lens, int32
     [batch]: the chunk's tokens of each sequence of a padded batch, whose other
-    rows of out are left as they were (0 in an out made here)."""
+    rows of out are left as they were (0 in an out made here).  So does a LatentCache
+    (kvq_latent_attn), with q [batch][chunk][Hq][latent_dim + rope_dim], out
+    [batch][chunk][Hq][latent_dim], a workspace of latent_workspace_bytes(...) bytes
+    and a softmax_scale."""
+    if isinstance(cache, LatentCache):
+        return _attend_latent(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace, True)
     if isinstance(cache, Fp8BlockCache):
         return _prefill_block8(cache, seq_lens, q, softmax_scale, out, err, stream, chunk_lens, workspace)
     if chunk_lens is not None or workspace is not None:
@@ -685,10 +920,29 @@ def swa_replay(w: torch.Tensor, emb: torch.Tensor, n_win: int, want_hidden: bool
     return states, hidden
 
 
+def _dequant_latent(cache, seq_lens, max_len, dtype, err, stream):
+    dev = _device(cache)
+    B = seq_lens.numel()
+    _per_seq(dev, seq_lens, B, "seq_lens")
+    _table_rows(dev, cache, None, B)
+    if dtype not in _OUT_DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    c, k = (_alloc(stream, (B, max_len, w), dtype, dev) for w in (cache.latent_dim, cache.rope_dim))
+    s = cache.struct()
+    st = load().kvq_latent_dequant(ctypes.byref(s), B, seq_lens.data_ptr(), max_len, _OUT_DTYPES[dtype], c.data_ptr(),
+                                   k.data_ptr(), _err_ptr(dev, err), _stream_on(dev, stream))
+    _check(st, "kvq_latent_dequant")
+    return c, k
+
+
 def dequant(cache, seq_lens: Optional[torch.Tensor], max_len: int, dtype: torch.dtype = torch.float32,
             err: Optional[torch.Tensor] = None, stream=None):
     """kvq_dequant: dense K, V [batch][max_len][Hkv][head_dim] (FP8 ring: max_len
-    == window, slot order; Fp8BlockCache: kvq_fp8_block_dequant)."""
+    == window, slot order; Fp8BlockCache: kvq_fp8_block_dequant).  LatentCache:
+    kvq_latent_dequant, latents [batch][max_len][latent_dim] and key parts
+    [batch][max_len][rope_dim]."""
+    if isinstance(cache, LatentCache):
+        return _dequant_latent(cache, seq_lens, max_len, dtype, err, stream)
     block8 = isinstance(cache, Fp8BlockCache)
     if block8:
         dev = _device(cache)
