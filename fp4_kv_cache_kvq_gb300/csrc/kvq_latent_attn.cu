@@ -1,14 +1,68 @@
 // kvq_latent_attn.cu -- attention over the latent cache (absorbed form), one
-// token per sequence or a chunk of them, and its C entry points.
-//   y = softmax_scale log2 e (q . [c, k]),  out = sum 2^(y - m) c / sum 2^(y - m)
-// with the tokens' values as the cache holds them.
-#include "kvq_attn_rows.cuh"
+// token per sequence or a chunk of them, on the 5th-generation tensor cores
+// (tcgen05, accumulators in TMEM), and its C entry points.
+//
+// Mathematics.  With a token's codes and its scale s = 2^e,
+//   S = q . codes,  y = S s (softmax_scale log2 e),  x = 2^(y + e - ref),
+//   out = 2^(ref - m) sum x code / l,  l = sum 2^(y - m).
+// The values' scale is a power of two and stands in x's exponent beside the
+// softmax's own, so the codes enter both products as the cache holds them: a tile
+// is copied once and read twice, as K-major operand (tokens x channels) for S and
+// as MN-major operand (channels x tokens) for the sums.  ref and m are references
+// of a row's own (the largest y + e and y so far), so neither tiny nor huge values
+// beside others make x or l leave their range.
+//   q   scaled per row by a power of two to [2^7, 2^8), is the sum of two E4M3
+//       values hi = RNE(q), lo = RNE(q - hi): exact down to 2^-9 of the row's
+//       largest element, off by at most 2^-17 of it below.  hi and lo are rows of
+//       one operand (128 rows for 64 queries); their scores are added in fp32.
+//   x   reaches 2^5 .. 2^8 in every row and is rounded to f16, then hi = E4M3(x),
+//       lo = E5M2(x - hi): 2^-8 of x, or 2^-14 under 2^-6, where hi's steps end
+//       and lo's range (down to 2^-17) takes over.  Two products of 8-bit operands
+//       cost what one of 16-bit ones costs and need no expansion of the values.
+// Sums, maxima and accumulators are fp32.
+//
+// Work.  A row is a query head of a token; a unit is 64 rows of one sequence and
+// all its positions.  A CTA holds 64 rows: sum^T is 4 accumulators of 128
+// channels x 64 rows (256 TMEM columns at latent_dim 512), q 144 columns, S 64.
+// Few units: the positions of all sequences, laid end to end, are split evenly over
+// the CTAs, the row tiles of a sequence side by side so that they read the same
+// tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
+// the longest first.
+// Six warps: softmax (4; thread = two rows x 16 positions), loader, MMA issue,
+// joined by mbarriers (every wait bounded):
+//   loader    bulk copies of 64-token tiles into a ring
+//   MMA       S(j) = q K(j)^T                 kind::f8f6f4, q from TMEM
+//             O^T += K(j)^T x(j)              kind::f8f6f4, twice (hi, lo)
+//             in the order S(j + 1), O(j)
 #include "kvq_latent.cuh"
+#include "kvq_tc.cuh"
 
 #include <cuda_bf16.h>
 
 namespace kvq {
 namespace {
+
+constexpr int kLT = 64;     // positions per tile
+constexpr int kLRows = 64;  // query rows per unit
+constexpr int kLSoftmax = 128, kLThreads = 192;
+constexpr int kLdWarpL = 4;  // and the MMA warp behind it
+constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
+constexpr int kMinTiles = 4;           // least tiles of a split range
+// x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
+// the references are raised only past the slack, since that rescales O.
+constexpr float kTop = 5.0f, kSlackL = 3.0f;
+
+enum : int {
+  kLFull = 0,               // [stages] codes and exponents landed
+  kLEmpty = kLFull + 8,     // [stages] the tile's sums done (commit)
+  kLSFull = kLEmpty + 8,    // S in TMEM
+  kLSFree = kLSFull + 1,    // S taken by the softmax warps
+  kLQFull = kLSFree + 1,    // q in TMEM
+  kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
+  kLPvDone = kLPFull + 2,   // [2] O += done
+  kLDrain = kLPvDone + 2,   // the MMA warp's last commit
+  kLBars = kLDrain + 1
+};
 
 struct LatentAttnParams {
   kvq_latent_cache c;
@@ -16,67 +70,771 @@ struct LatentAttnParams {
   const int32_t* chunk_lens;
   const uint16_t* q;
   void* out;
+  float* part_o;    // [ctas][2][64][L]: a part's own result
+  float* part_lse;  // [ctas][2][64]: log2 of its sum of weights
+  int2* rec;        // [batch * tpb]: first CTA and number of parts of a unit
   int32_t* flag;
-  int32_t batch, hq, chunk, out_bf16, tiles;
+  int32_t batch, hq, chunk, out_bf16;
+  int32_t tpb;      // row tiles per sequence
+  int32_t groups;   // CTAs per row tile that share the positions; 0: a unit per CTA
   float scale_log2;
+  uint64_t wait_ns; // a test's limit of the waits, or 0
 };
 
-struct LatentSrc {
-  const LatentAttnParams& p;
-  LatentLayout lay;
-  int b, r0;
-  int64_t first;  // position of the chunk's token 0
-  __device__ int64_t row(int r) const { return (int64_t)b * p.chunk * p.hq + r0 + r; }
-  __device__ float query(int r, int c) const {
-    return __uint_as_float((uint32_t)p.q[row(r) * (lay.L + lay.R) + c] << 16);
+template <int L, int R>
+struct LGeo {
+  static constexpr int kRow = L + 2 * R;
+  static constexpr int kTile = kLT * kRow;
+  static constexpr int kStages = kTile * 5 + 4 * kPBytes > 220 * 1024 ? 4 : 5;
+  static constexpr int kP = kStages * kTile;              // [2][hi, lo]
+  static constexpr int kExp = kP + 4 * kPBytes;           // [stages][64]
+  static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
+  static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns
+  static constexpr int kBar = kAlpha + 2 * 4 * kLRows;
+  static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, plan
+  static constexpr int kUsed = kMisc + 128 + 128;
+  static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;  // one CTA per SM: it holds all of TMEM
+  static constexpr int kOCol = 0, kQCol = L / 2, kSCol = kQCol + (L + R) / 4;
+  static_assert(kSCol + kLT <= 512 && kUsed <= 227 * 1024 && kBar % 8 == 0 && kStages <= 8, "layout");
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// Instruction descriptors: fp32 accumulators, M = 128, N = 64, A E4M3, B E4M3 or E5M2.
+constexpr uint32_t kIdS = (1u << 4) | (kLT / 8 << 17) | (128u / 16 << 24);
+constexpr uint32_t kIdOHi = (1u << 4) | (1u << 15) | (kLRows / 8 << 17) | (128u / 16 << 24);  // A MN-major
+constexpr uint32_t kIdOLo = kIdOHi | (1u << 10);
+
+// 16 lanes x 64 columns of TMEM: register 4j + 2i + e holds row lane/4 + 8i, column 8j + 2(lane%4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256b_x1(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+// Named barrier 1 of the softmax warps; true when any thread's v is.
+__device__ __forceinline__ bool softmax_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// A wait of the whole warp with one outcome; it gives up after the library's limit
+// (or a test's, which polls: a suspending wait could outlast it), or with any other
+// wait of the CTA.
+struct LWaits {
+  volatile int* abort;
+  uint64_t limit;  // a test's, ns, or 0
+  __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) const {
+    return limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
   }
-  __device__ int64_t last(int r) const { return first + (r0 + r) / p.hq; }
-  __device__ int64_t group(int64_t pos, int32_t* flag) const { return latent_group(p.c, lay, b, pos, flag); }
-  __device__ bool attends(int64_t pos) const { return pos >= 0 && pos <= first + p.chunk && group(pos, p.flag) >= 0; }
-  __device__ void load(int64_t pos, float* k, float* v, int lane) const {
-    const int64_t grp = pos < 0 ? -1 : group(pos, p.flag);
-    const uint8_t* base = static_cast<const uint8_t*>(p.c.data) + grp;
-    const int slot = (int)(pos & (lay.G - 1));
-    const float s = grp < 0 ? 0.0f : latent_scale(base[lay.exponent(slot)]);
-    for (int c = lane; c < lay.L + lay.R; c += 32) {
-      float x = 0.0f;
-      if (grp >= 0) {
-        x = e4m3_to_f32(base[lay.unit(slot, c >> 4) + (c & 15)]);
-        if (c >= lay.L) x += e4m3_to_f32(base[lay.unit(slot, (c + lay.R) >> 4) + (c & 15)]);
-        x *= s;
+  __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) const {
+    if (look(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (true) {
+      if (look(bar, parity)) return true;
+      if (*abort) return false;
+      if (global_ns() - t0 > (limit ? limit : kWaitLimitNs)) {
+        *abort = 1;
+        return false;
       }
-      k[c] = x;
-      if (c < lay.L) v[c] = x;
     }
   }
-  __device__ void store(int r, int c, float x) const {
-    const int64_t at = row(r) * lay.L + c;
-    if (p.out_bf16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-    else
-      static_cast<float*>(p.out)[at] = x;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity));
   }
 };
 
-__global__ void __launch_bounds__(kThreadsR) latent_attn_kernel(const LatentAttnParams p) {
-  extern __shared__ float sm[];
-  const int b = blockIdx.x / p.tiles, r0 = blockIdx.x % p.tiles * kRowsR;
-  const int32_t T = __ldg(p.lens + b), n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
-  const bool decode = p.chunk == 1 && p.chunk_lens == nullptr;
-  if (n < 0 || n > p.chunk || T < (decode ? 0 : n)) {
-    if (threadIdx.x == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
-    if (n < 0 || n > p.chunk) return;
+__device__ __forceinline__ int64_t capacity(const kvq_latent_cache& c) { return (int64_t)c.max_pages_per_seq * c.page_size; }
+
+// Tiles that sequence b takes on the line of all sequences' positions (1 at least).
+__device__ __forceinline__ int64_t line_tiles(const LatentAttnParams& p, int b) {
+  const int64_t t = min((int64_t)max(__ldg(p.lens + b), 0), capacity(p.c));
+  return max((int64_t)1, (t + kLT - 1) / kLT);
+}
+
+// One CTA's share of a unit: tiles [t0, t1) of the nt that its rows attend.
+struct Unit {
+  int b, r, rows, n, t0, t1;
+  int64_t first, limit;  // position of the chunk's token 0; positions read
+  bool whole;
+  int slot;
+};
+
+struct Plan {
+  int64_t lo, hi, base;  // range on the line, and where sequence b starts on it
+  int64_t per;
+  int b;
+};
+
+// The CTA's units in order; every role walks them alike.
+struct Walk {
+  const LatentAttnParams& p;
+  int64_t lo, hi, base, per, i;
+  int b;
+  __device__ Walk(const LatentAttnParams& p_, const Plan& pl)
+      : p(p_), lo(pl.lo), hi(pl.hi), base(pl.base), per(pl.per), i(blockIdx.x), b(pl.b) {}
+  __device__ void rows_of(Unit& u, int32_t* flag) const {
+    const int32_t T = __ldg(p.lens + u.b), n = p.chunk_lens ? __ldg(p.chunk_lens + u.b) : p.chunk;
+    const bool decode = p.chunk == 1 && p.chunk_lens == nullptr;
+    const bool bad_n = n < 0 || n > p.chunk;
+    if ((bad_n || T < (decode ? 0 : n)) && u.r == 0) set_flag(flag, KVQ_FLAG_BAD_LENGTH);
+    u.n = bad_n ? 0 : n;
+    u.rows = (int)max((int64_t)0, min((int64_t)kLRows, (int64_t)u.n * p.hq - (int64_t)u.r * kLRows));
+    u.first = (int64_t)T - u.n;
+    u.limit = 0;
+    if (u.rows > 0 && u.first >= 0) {
+      u.limit = u.first + (u.r * kLRows + u.rows - 1) / p.hq + 1;
+      if (u.limit > capacity(p.c)) {
+        u.limit = capacity(p.c);
+        set_flag(flag, KVQ_FLAG_PAGE_OOB);
+      }
+    }
   }
-  const int rows = min(kRowsR, n * p.hq - r0);
-  if (rows <= 0) return;
-  LatentSrc src{p, LatentLayout(p.c), b, r0, (int64_t)T - n};
-  const int64_t cap = (int64_t)p.c.max_pages_per_seq * p.c.page_size;
-  int64_t limit = T < n ? 0 : src.last(rows - 1) + 1;
-  if (limit > cap) {
-    if (threadIdx.x == 0) set_flag(p.flag, KVQ_FLAG_PAGE_OOB);
-    limit = cap;
+  // flag: where bad lengths are reported (one role does)
+  __device__ bool next(Unit& u, int32_t* flag) {
+    while (true) {
+      if (p.groups == 0) {
+        if (i >= (int64_t)p.batch * p.tpb) return false;
+        u.r = p.tpb - 1 - (int)(i / p.batch);
+        u.b = (int)(i % p.batch);
+        i += gridDim.x;
+        rows_of(u, flag);
+        u.t0 = 0;
+        u.t1 = (int)((u.limit + kLT - 1) / kLT);
+        u.whole = true;
+        u.slot = 0;
+      } else {
+        if (base >= hi) return false;
+        const int64_t cost = line_tiles(p, b);
+        const int64_t s0 = max(lo - base, (int64_t)0), s1 = min(hi - base, cost);
+        u.b = b;
+        u.r = (int)(blockIdx.x % (unsigned)p.tpb);
+        rows_of(u, flag);
+        const int nt = (int)((u.limit + kLT - 1) / kLT);
+        u.t0 = (int)min(s0, (int64_t)nt);
+        u.t1 = (int)min(s1, (int64_t)nt);
+        u.whole = s0 == 0 && s1 == cost;
+        u.slot = s0 > 0 ? 0 : 1;
+        if (flag == p.flag && s0 == 0 && threadIdx.x == 0)
+          p.rec[(int64_t)b * p.tpb + u.r] = make_int2((int)blockIdx.x, (int)((base + cost - 1) / per - base / per + 1));
+        base += cost;
+        ++b;
+      }
+      if (u.rows > 0) return true;
+    }
   }
-  attend_rows(src, RowsShape{p.c.latent_dim + p.c.rope_dim, p.c.latent_dim}, rows, limit, p.scale_log2, sm);
+};
+
+template <int L, int R>
+__global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentAttnParams p) {
+  using G = LGeo<L, R>;
+  constexpr int kM = L / 128, kSteps = (L + R) / 32;
+  extern __shared__ uint8_t lat_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lat_raw) + 127) & ~uintptr_t(127));
+  const uint32_t sb = smem_addr(base), bars = sb + G::kBar;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
+  Plan* plan = reinterpret_cast<Plan*>(misc + 2);
+  int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [6]
+  volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
+  const LWaits wait{abort, p.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < G::kStages; ++s) {
+      mbar_init(bars + 8 * (kLFull + s), 1);
+      mbar_init(bars + 8 * (kLEmpty + s), 1);
+    }
+    mbar_init(bars + 8 * kLSFull, 1);
+    mbar_init(bars + 8 * kLSFree, 4);
+    mbar_init(bars + 8 * kLQFull, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (kLPFull + i), 4);
+      mbar_init(bars + 8 * (kLPvDone + i), 1);
+    }
+    mbar_init(bars + 8 * kLDrain, 1);
+    *abort = 0;
+    plan->lo = plan->hi = plan->base = 0;
+    plan->b = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(smem_addr(misc), 512);
+  if (p.groups > 0) {  // where the CTA's range of the line lies
+    const int each = (p.batch + kLThreads - 1) / kLThreads, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) own += line_tiles(p, b);
+    int64_t pre = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    if (lane == 31) sums[warp] = pre;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kLThreads / 32; ++w) {
+      if (w < warp) pre += sums[w];
+      total += sums[w];
+    }
+    const int64_t per = max((int64_t)kMinTiles, (total + p.groups - 1) / p.groups);
+    const int64_t lo = (int64_t)(blockIdx.x / (unsigned)p.tpb) * per;
+    int64_t at = pre - own;
+    if (lo >= at && lo < pre) {
+      int b = b0;
+      for (; b < b1; ++b) {
+        const int64_t c = line_tiles(p, b);
+        if (lo < at + c) break;
+        at += c;
+      }
+      plan->lo = lo;
+      plan->hi = min(lo + per, total);
+      plan->base = at;
+      plan->per = per;
+      plan->b = b;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+  Walk walk(p, *plan);
+  Unit u;
+  bool failed = false;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ softmax
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t tw = tmem + ((uint32_t)(32 * warp) << 16);
+    const int lr[2] = {16 * warp + g, 16 * warp + g + 8};
+    float* alpha = reinterpret_cast<float*>(base + G::kAlpha);  // [64], then a second factor [64]
+    uint32_t it = 0, sph = 0;  // tiles so far
+    while (walk.next(u, tid == 0 ? p.flag : nullptr)) {
+      const int64_t row0 = (int64_t)u.b * p.chunk * p.hq + (int64_t)u.r * kLRows;
+      if (u.t0 >= u.t1) {  // nothing attended: a zero row, or a part without weight
+        if (u.whole) {
+          for (int i = tid; i < u.rows * (L / 4); i += kLSoftmax) {
+            const int64_t at = row0 * L + 4 * (int64_t)i;
+            if (p.out_bf16)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(0u, 0u);
+            else
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        } else if (tid < kLRows) {
+          p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + tid] = -INFINITY;
+        }
+        continue;
+      }
+      // q: a warp takes 16 rows, four lanes a row's 64-byte pieces; hi to lanes 0..15, lo
+      // to lanes 16..31 of the warp's TMEM lanes
+      uint4 qv[2][kSteps];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          qv[i][s] = make_uint4(0u, 0u, 0u, 0u);
+          if (lr[i] < u.rows)
+            qv[i][s] = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + lr[i]) * (L + R) + 32 * s + 8 * t));
+        }
+      float xs[2];       // S to log2 units, before the token's scale
+      int64_t last[2];   // last position that the row attends
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t am = 0u;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const uint32_t w[4] = {qv[i][s].x, qv[i][s].y, qv[i][s].z, qv[i][s].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) am = max(am, max(w[k] << 16 & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+        }
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+        const int ex = max((int)(am >> 23), 8);  // times 2^(134 - ex): to [2^7, 2^8)
+        const bool bad = am >= 0x7F800000u;      // an Inf or NaN: the row's scores are NaN, its codes 0
+        const float mul = __uint_as_float((uint32_t)(261 - min(ex, 254)) << 23);
+        xs[i] = bad ? __uint_as_float(0x7FFFFFFFu) : p.scale_log2 * __uint_as_float((uint32_t)(min(ex, 254) - 7) << 23);
+        if (bad) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) qv[i][s] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        last[i] = lr[i] < u.rows ? u.first + (u.r * kLRows + lr[i]) / p.hq : -1;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {  // in place: x, y the hi codes, z, w the lo codes
+          const uint32_t w[4] = {qv[i][s].x, qv[i][s].y, qv[i][s].z, qv[i][s].w};
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = bf16_lo(w[k]) * mul, x1 = bf16_hi(w[k]) * mul;
+            h[k] = e4m3x2_from_f32(x0, x1);
+            const float2 y = f16x2_to_float2(f16x2_from_e4m3x2(h[k]));
+            l[k] = e4m3x2_from_f32(x0 - y.x, x1 - y.y);
+          }
+          qv[i][s] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, l[0] | l[1] << 16, l[2] | l[3] << 16);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        tmem_st_16x256b_x1(tw + G::kQCol + 8 * s, qv[0][s].x, qv[0][s].y, qv[1][s].x, qv[1][s].y);
+        tmem_st_16x256b_x1(tw + (16u << 16) + G::kQCol + 8 * s, qv[0][s].z, qv[0][s].w, qv[1][s].z, qv[1][s].w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * kLQFull);
+
+      float ref[2] = {-INFINITY, -INFINITY}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
+      for (int j = u.t0; j < u.t1; ++j, ++it) {
+        const int st = (int)(it % G::kStages);
+        if (!failed) failed = !wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u);
+        if (!failed) failed = !wait(bars + 8 * kLSFull, sph & 1u);
+        ++sph;
+        tc_fence_after();
+        uint32_t v[32], lo[32];
+        tmem_ld_16x256b_x8(tw + G::kSCol, v);
+        tmem_ld_16x256b_x8(tw + (16u << 16) + G::kSCol, lo);
+        tmem_wait_ld(v);
+        tmem_wait_ld(lo);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
+        const uint64_t ok = vmask[st];
+        const int64_t p0 = (int64_t)j * kLT;
+        const bool part = ok != ~0ull || p0 + kLT > full_upto;  // some row sees the tile in part
+        float y[2][16], z[2][16], top[2] = {-INFINITY, -INFINITY}, my[2] = {m[0], m[1]};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t e2 = lds16(sb + G::kExp + st * kLT + 8 * k + 2 * t);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t ev = e ? e2 >> 8 : e2 & 0xFFu;
+            const float s = latent_scale(ev), es = (float)(int)(ev - 127u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float S = __uint_as_float(v[4 * k + 2 * i + e]) + __uint_as_float(lo[4 * k + 2 * i + e]);
+              float yy = S * (xs[i] * s);
+              if (part) {
+                const int c = 8 * k + 2 * t + e;
+                if (p0 + c > last[i] || !((ok >> c) & 1ull)) yy = -INFINITY;
+              }
+              const float zz = yy + es;
+              y[i][2 * k + e] = yy;
+              z[i][2 * k + e] = zz;
+              top[i] = fmaxf(top[i], zz);
+              my[i] = fmaxf(my[i], yy);
+            }
+          }
+        }
+        bool up = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+          my[i] = fmaxf(my[i], __shfl_xor_sync(0xFFFFFFFFu, my[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+          my[i] = fmaxf(my[i], __shfl_xor_sync(0xFFFFFFFFu, my[i], 2));
+          up |= top[i] > ref[i] + kSlackL;
+        }
+        if (softmax_or(up)) {
+          // raise the references; O's columns follow (none at the unit's first tile)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float to = fmaxf(ref[i], floorf(top[i]));
+            if (t == 0) alpha[lr[i]] = ref[i] == -INFINITY ? 0.0f : fast_exp2(ref[i] - to);
+            ref[i] = to;
+          }
+          named_barrier_sync(1, kLSoftmax);
+          if (j > u.t0) {
+            if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < kM * 2; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(tw + G::kOCol + 32 * cc, o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(alpha + 32 * (cc & 1) + 4 * k);
+                o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
+                o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
+                o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
+                o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * a.w);
+              }
+              tmem_st32_async(tw + G::kOCol + 32 * cc, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        // x in two parts to shared memory, [16 tokens][8 rows] core matrices
+        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float rf = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop;
+          const float mm = my[i] == -INFINITY ? 0.0f : my[i];
+          float sum = 0.0f;
+          const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16 + 2 * t);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sum += fast_exp2(y[i][2 * k] - mm) + fast_exp2(y[i][2 * k + 1] - mm);
+            const uint32_t h = pack_f16x2(fast_exp2(z[i][2 * k] - rf), fast_exp2(z[i][2 * k + 1] - rf));
+            const uint32_t hi = e4m3x2_of_f16x2(h);
+            const uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
+            const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
+            sts_u16(a, hi);
+            sts_u16(a + kPBytes, rest);
+          }
+          l[i] = l[i] * fast_exp2((m[i] == -INFINITY ? mm : m[i]) - mm) + sum;
+          m[i] = my[i];
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + (it & 1)));
+        if (*abort) failed = true;
+        if (softmax_or(failed)) {
+          failed = true;
+          break;
+        }
+      }
+      if (failed) break;
+      // the unit's result
+      float lse[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+        const float mm = m[i] == -INFINITY ? 0.0f : m[i];
+        const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm, half = rintf(0.5f * d);
+        lse[i] = l[i] == 0.0f ? -INFINITY : mm + log2f(l[i]);
+        if (t == 0) {  // two factors: 2^d alone can leave fp32's range
+          alpha[lr[i]] = fast_exp2(half);
+          alpha[kLRows + lr[i]] = l[i] == 0.0f ? 0.0f : fast_exp2(d - half) / l[i];
+        }
+      }
+      failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
+      if (softmax_or(failed)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      float* po = p.part_o + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows * L;
+      if (!u.whole && t == 0) {
+        float* pl = p.part_lse + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows;
+        pl[lr[0]] = lse[0];
+        pl[lr[1]] = lse[1];
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < kM * 2; ++cc) {
+        const int c0 = 32 * (cc & 1), ch = 128 * (cc >> 1) + 32 * warp + lane;
+        if (c0 >= u.rows) continue;
+        uint32_t o[32];
+        tmem_ld32(tw + G::kOCol + 32 * cc, o);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int r = c0 + c;
+          if (r < u.rows) {
+            const float f = alpha[kLRows + r];
+            const float x = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * alpha[r] * f;
+            if (!u.whole)
+              po[r * L + ch] = x;
+            else if (p.out_bf16)
+              static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * L + ch] = __float2bfloat16_rn(x);
+            else
+              static_cast<float*>(p.out)[(row0 + r) * L + ch] = x;
+          }
+        }
+      }
+      tc_fence_before();
+      named_barrier_sync(1, kLSoftmax);  // alpha is free again
+    }
+  } else if (warp == kLdWarpL) {
+    // ------------------------------------------------------------ loader
+    const LatentLayout lay(p.c);
+    const int gs = lay.G, ng = kLT / gs, tb = 32 / ng;  // groups per tile, tiles per lookup
+    const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
+    uint32_t it = 0;
+    while (!failed && walk.next(u, nullptr)) {
+      int64_t off = -1;
+      for (int j = u.t0; j < u.t1; ++j, ++it) {
+        const int st = (int)(it % G::kStages), k = (j - u.t0) % tb;
+        if (k == 0) {
+          const int64_t pos = (int64_t)(j + lane / ng) * kLT + lane % ng * gs;
+          off = pos < u.limit && j + lane / ng < u.t1 ? latent_group(p.c, lay, u.b, pos, p.flag) : -1;
+          if (off >= 0 && !KVQ_IN(off + lay.group_bytes() <= p.c.num_pages * lay.page_bytes(), p.flag)) off = -1;
+        }
+        const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (k * ng + lane) & 31);
+        const int cnt = lane < ng && src >= 0
+                            ? (int)max((int64_t)0, min((int64_t)gs, u.limit - ((int64_t)j * kLT + lane * gs)))
+                            : 0;
+        const uint32_t code_bytes = (uint32_t)((cnt + 7) & ~7) * G::kRow;
+        const uint32_t bytes = __reduce_add_sync(0xFFFFFFFFu, cnt > 0 ? code_bytes + (uint32_t)gs : 0u);
+        const uint64_t bits = cnt > 0 ? (cnt >= 64 ? ~0ull : ((1ull << cnt) - 1ull) << (lane * gs)) : 0ull;
+        const uint64_t ok = (uint64_t)__reduce_or_sync(0xFFFFFFFFu, (uint32_t)(bits >> 32)) << 32 |
+                            __reduce_or_sync(0xFFFFFFFFu, (uint32_t)bits);
+        if (it >= G::kStages && !wait(bars + 8 * (kLEmpty + st), (it / G::kStages - 1) & 1u)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
+          vmask[st] = ok;
+          mbar_arrive_expect_tx(bars + 8 * (kLFull + st), bytes);
+        }
+        __syncwarp();
+        if (cnt > 0) {
+          bulk_g2s(sb + st * G::kTile + lane * gs * G::kRow, pool + src, code_bytes, bars + 8 * (kLFull + st));
+          bulk_g2s(sb + G::kExp + st * kLT + lane * gs, pool + src + lay.exponent(0), gs, bars + 8 * (kLFull + st));
+        }
+      }
+    }
+    // no copy outlives the CTA
+    for (uint32_t s = it > G::kStages ? it - G::kStages : 0u; s < it; ++s) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait_hint(bars + 8 * (kLFull + s % G::kStages), (s / G::kStages) & 1u, 20000u) &&
+             global_ns() - t0 < 20000000ull) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ MMA issue
+    const uint64_t dk = smem_desc(sb, 128, 8 * G::kRow);           // tokens as rows: K-major
+    const uint64_t dv = smem_desc(sb, 8 * G::kRow, 128);           // channels as rows: MN-major
+    const uint64_t dp = smem_desc(sb + G::kP, 1024, 128);
+    uint32_t it = 0, un = 0;
+    const auto sums_of = [&](uint32_t i, bool first) {  // O^T (+)= K(i)^T x(i)
+      if (!wait(bars + 8 * (kLPFull + (i & 1)), (i >> 1) & 1u)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t a = dv + (uint64_t)((i % G::kStages) * (G::kTile >> 4));
+        const uint64_t b = dp + (uint64_t)((i & 1) * (2 * kPBytes >> 4));
+#pragma unroll
+        for (int mm = 0; mm < kM; ++mm)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {  // 32 tokens: four core matrices of V, two of x
+            const uint64_t am = a + (uint64_t)((mm * 1024 + s * 32 * G::kRow) >> 4);
+            mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)(s * 2048 >> 4), kIdOHi, !(first && s == 0));
+            mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)((s * 2048 + kPBytes) >> 4), kIdOLo, true);
+          }
+        tc_commit(bars + 8 * (kLEmpty + i % G::kStages));
+        tc_commit(bars + 8 * (kLPvDone + (i & 1)));
+      }
+      __syncwarp();
+      return true;
+    };
+    while (!failed && walk.next(u, nullptr)) {
+      if (u.t0 >= u.t1) continue;
+      if (!wait(bars + 8 * kLQFull, un & 1u)) break;
+      ++un;
+      for (int j = u.t0; j < u.t1; ++j, ++it) {
+        const int st = (int)(it % G::kStages);
+        if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u)) failed = true;
+        if (!failed && it > 0 && !wait(bars + 8 * kLSFree, (it - 1) & 1u)) failed = true;
+        if (failed) break;
+        const uint64_t ok = vmask[st];
+        if (ok != ~0ull) {  // rows without a token: whatever lies there must not meet a weight of 0 as NaN
+          const uint32_t tile = sb + st * G::kTile;
+          for (int i = lane; i < kLT * (L / 16); i += 32) {
+            const int tok = (i & 7) | (i / (8 * (L / 16))) << 3, un16 = i / 8 % (L / 16);
+            if (!((ok >> tok) & 1ull)) sts128(tile + (tok >> 3) * 8 * G::kRow + un16 * 128 + (tok & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t kd = dk + (uint64_t)(st * (G::kTile >> 4));
+#pragma unroll
+          for (int s = 0; s < kSteps + R / 32; ++s) {
+            const int a = s < kSteps ? s : s - R / 32;  // the key part's lo codes meet the same q
+            mma_f8_ta(tmem + G::kSCol, tmem + G::kQCol + 8 * a, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
+          }
+          tc_commit(bars + 8 * kLSFull);
+        }
+        __syncwarp();
+        if (j > u.t0 && !sums_of(it - 1, j - 1 == u.t0)) {
+          failed = true;
+          break;
+        }
+      }
+      if (failed) break;
+      if (!sums_of(it - 1, u.t1 - 1 == u.t0)) break;
+    }
+    // no product outlives the CTA
+    if (lane == 0) tc_commit(bars + 8 * kLDrain);
+    __syncwarp();
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait_hint(bars + 8 * kLDrain, 0u, 20000u) && global_ns() - t0 < 20000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) set_flag(p.flag, KVQ_FLAG_TIMEOUT);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of units that several CTAs worked on: a warp per row,
+// out = sum w_i o_i, w_i = 2^(lse_i - m) / sum 2^(lse_j - m).
+template <int L>
+__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParams p, int row_blocks) {
+  grid_dependency_wait();
+  const int unit = blockIdx.x / row_blocks, r = blockIdx.x % row_blocks * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int b = unit / p.tpb, rt = unit % p.tpb;
+  const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
+  if (n < 0 || n > p.chunk || r >= kLRows || (int64_t)rt * kLRows + r >= (int64_t)n * p.hq) return;
+  const int2 rec = p.rec[unit];
+  if (rec.y <= 1 || !KVQ_IN(rec.x >= 0 && (int64_t)rec.x + (int64_t)(rec.y - 1) * p.tpb < (int64_t)p.groups * p.tpb, p.flag)) return;
+  const auto at = [&](int i) { return ((int64_t)(rec.x + i * p.tpb) * 2 + (i == 0 ? 1 : 0)) * kLRows + r; };
+  float m = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < rec.y; i += 32) {
+    const float x = p.part_lse[at(i)];
+    m = fmaxf(m, x);
+    nan |= x != x;
+  }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  const float mm = m == -INFINITY ? 0.0f : m;
+  float acc[L / 32], l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < L / 32; ++c) acc[c] = 0.0f;
+  for (int i = 0; i < rec.y; ++i) {
+    const int64_t a = at(i);
+    const float x = p.part_lse[a];
+    if (x == -INFINITY) continue;
+    const float w = fast_exp2(x - mm);
+    l += w;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + a * L) + lane;
+#pragma unroll
+    for (int c = 0; c < L / 128; ++c) {
+      const float4 v = src[32 * c];
+      acc[4 * c] += w * v.x, acc[4 * c + 1] += w * v.y, acc[4 * c + 2] += w * v.z, acc[4 * c + 3] += w * v.w;
+    }
+  }
+  const float f = nan ? __uint_as_float(0x7FFFFFFFu) : l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t row = (int64_t)b * p.chunk * p.hq + (int64_t)rt * kLRows + r;
+#pragma unroll
+  for (int c = 0; c < L / 128; ++c) {
+    const float4 v = make_float4(acc[4 * c] * f, acc[4 * c + 1] * f, acc[4 * c + 2] * f, acc[4 * c + 3] * f);
+    if (p.out_bf16) {
+      uint2 w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w.x) : "f"(v.y), "f"(v.x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w.y) : "f"(v.w), "f"(v.z));
+      *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * L) + 32 * c + lane) = w;
+    } else {
+      *(reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * L) + 32 * c + lane) = v;
+    }
+  }
+}
+
+// How a call is cut: row tiles per sequence, CTAs, and CTAs per row tile (0: a unit
+// per CTA).  Sharing the positions costs the join, but fills the SMs where there are
+// few units; it is taken where it leaves fewer of them idle.
+struct LatentCut {
+  int64_t tpb, ctas;
+  int groups;
+};
+LatentCut latent_cut(int32_t batch, int32_t hq, int32_t chunk, int sms) {
+  LatentCut c;
+  c.tpb = ((int64_t)chunk * hq + kLRows - 1) / kLRows;
+  const int64_t units = c.tpb * batch;
+  const int64_t waves = (units + sms - 1) / sms;
+  const double alone = (double)units / (double)(waves * sms);
+  const int64_t groups = sms / c.tpb;
+  const double shared = (double)(groups * c.tpb) / sms;
+  if (groups > 1 && shared > alone) {
+    c.groups = (int)groups;
+    c.ctas = groups * c.tpb;
+  } else {
+    c.groups = 0;
+    c.ctas = units < sms ? units : sms;
+  }
+  return c;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct LatentWorkspace {
+  size_t rec, lse, o, bytes;
+  LatentWorkspace(const LatentCut& c, int32_t batch, int32_t L) : rec(0), lse(0), o(0), bytes(16) {
+    if (c.groups == 0) return;
+    lse = align256((size_t)batch * c.tpb * sizeof(int2));
+    o = lse + align256((size_t)c.ctas * 2 * kLRows * sizeof(float));
+    bytes = o + (size_t)c.ctas * 2 * kLRows * L * sizeof(float);
+  }
+};
+
+template <int L, int R>
+kvq_status launch_latent(const LatentAttnParams& p, const LatentCut& cut, cudaStream_t s) {
+  static DeviceOnce attr_set;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (attr_set.pending(dev)) {
+    if (cudaFuncSetAttribute(latent_attn_kernel<L, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, LGeo<L, R>::kBytes) !=
+        cudaSuccess)
+      return KVQ_ERR_CUDA;
+    attr_set.mark(dev);
+  }
+  latent_attn_kernel<L, R><<<(unsigned)cut.ctas, kLThreads, LGeo<L, R>::kBytes, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  if (cut.groups == 0) return KVQ_OK;
+  const int rows = (int)((int64_t)p.chunk * p.hq < kLRows ? (int64_t)p.chunk * p.hq : kLRows);
+  const int row_blocks = (rows + 3) / 4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.batch * p.tpb * row_blocks));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L>, p, row_blocks) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+bool latent_sizes_ok(int32_t batch, int32_t hq, int32_t chunk) {
+  return (double)batch * ((double)chunk * hq + kLRows) <= (double)(1 << 30);
 }
 
 }  // namespace
@@ -86,8 +844,11 @@ using namespace kvq;
 
 extern "C" size_t kvq_latent_attn_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t latent_dim,
                                                   int32_t chunk) {
-  if (batch < 1 || num_q_heads < 1 || chunk < 1 || !latent_dims_ok(16, latent_dim, 64)) return 0;
-  return 16;
+  if (batch < 1 || num_q_heads < 1 || chunk < 1 || !latent_dims_ok(16, latent_dim, 64) ||
+      !latent_sizes_ok(batch, num_q_heads, chunk))
+    return 0;
+  const int sms = device_sm_count();
+  return LatentWorkspace(latent_cut(batch, num_q_heads, chunk, sms > 0 ? sms : 148), batch, latent_dim).bytes;
 }
 
 extern "C" kvq_status kvq_latent_attn(const kvq_latent_cache* cache, int32_t batch, int32_t num_q_heads, int32_t chunk,
@@ -103,19 +864,31 @@ extern "C" kvq_status kvq_latent_attn(const kvq_latent_cache* cache, int32_t bat
   if (d_seq_lens == nullptr || q == nullptr || out == nullptr || workspace == nullptr || !aligned_to(q, 16) ||
       !aligned_to(out, 16) || !aligned_to(workspace, 16))
     return KVQ_ERR_INVALID_ARGUMENT;
-  if ((double)batch * chunk * num_q_heads > (double)(1 << 30)) return KVQ_ERR_UNSUPPORTED;
-  if (workspace_bytes < kvq_latent_attn_workspace_bytes(batch, num_q_heads, cache->latent_dim, chunk))
-    return KVQ_ERR_WORKSPACE;
+  if (!latent_sizes_ok(batch, num_q_heads, chunk)) return KVQ_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  const LatentCut cut = latent_cut(batch, num_q_heads, chunk, sms > 0 ? sms : 148);
+  const LatentWorkspace ws(cut, batch, cache->latent_dim);
+  if (workspace_bytes < ws.bytes) return KVQ_ERR_WORKSPACE;
+  if (sms <= 0) return KVQ_ERR_CUDA;
   LatentAttnParams p = {};
   p.c = *cache;
   p.lens = d_seq_lens, p.chunk_lens = d_chunk_lens;
   p.q = static_cast<const uint16_t*>(q), p.out = out, p.flag = d_err_flag;
   p.batch = batch, p.hq = num_q_heads, p.chunk = chunk, p.out_bf16 = out_dtype == KVQ_DTYPE_BF16;
-  p.tiles = (int32_t)(((int64_t)chunk * num_q_heads + kRowsR - 1) / kRowsR);
+  p.tpb = (int32_t)cut.tpb, p.groups = cut.groups;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  const size_t bytes = RowsShape{cache->latent_dim + cache->rope_dim, cache->latent_dim}.bytes();
-  if (cudaFuncSetAttribute(latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
-    return KVQ_ERR_CUDA;
-  latent_attn_kernel<<<(unsigned)(batch * p.tiles), kThreadsR, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return launch_status();
+  p.wait_ns = test_wait_limit_ns();
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.rec = reinterpret_cast<int2*>(w + ws.rec);
+  p.part_lse = reinterpret_cast<float*>(w + ws.lse);
+  p.part_o = reinterpret_cast<float*>(w + ws.o);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->rope_dim == 64) {
+    if (cache->latent_dim == 512) return launch_latent<512, 64>(p, cut, s);
+    if (cache->latent_dim == 256) return launch_latent<256, 64>(p, cut, s);
+    return launch_latent<128, 64>(p, cut, s);
+  }
+  if (cache->latent_dim == 512) return launch_latent<512, 32>(p, cut, s);
+  if (cache->latent_dim == 256) return launch_latent<256, 32>(p, cut, s);
+  return launch_latent<128, 32>(p, cut, s);
 }
