@@ -28,8 +28,8 @@
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
 // the longest first.
-// Six warps: softmax (4; thread = two rows x 16 positions), loader, MMA issue,
-// joined by mbarriers (every wait bounded):
+// Ten warps: softmax (8; thread = two rows x 8 positions of a tile), loader, MMA
+// issue, joined by mbarriers (every wait bounded):
 //   loader    bulk copies of 64-token tiles into a ring
 //   MMA       S(j) = q K(j)^T                 kind::f8f6f4, q from TMEM
 //             O^T += K(j)^T x(j)              kind::f8f6f4, twice (hi, lo)
@@ -44,8 +44,8 @@ namespace {
 
 constexpr int kLT = 64;     // positions per tile
 constexpr int kLRows = 64;  // query rows per unit
-constexpr int kLSoftmax = 128, kLThreads = 192;
-constexpr int kLdWarpL = 4;  // and the MMA warp behind it
+constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 64;
+constexpr int kLdWarpL = kLSmWarps;  // and the MMA warp behind it
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 4;           // least tiles of a split range
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
@@ -89,10 +89,11 @@ struct LGeo {
   static constexpr int kP = kStages * kTile;              // [2][hi, lo]
   static constexpr int kExp = kP + 4 * kPBytes;           // [stages][64]
   static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
-  static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns
-  static constexpr int kBar = kAlpha + 2 * 4 * kLRows;
+  static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns, [64] second ones
+  static constexpr int kTwo = kAlpha + 2 * 4 * kLRows;    // [3][2][64] what the two halves of a row exchange
+  static constexpr int kBar = kTwo + 3 * 2 * 4 * kLRows;
   static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, plan
-  static constexpr int kUsed = kMisc + 128 + 128;
+  static constexpr int kUsed = kMisc + 192 + 128;
   static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;  // one CTA per SM: it holds all of TMEM
   static constexpr int kOCol = 0, kQCol = L / 2, kSCol = kQCol + (L + R) / 4;
   static_assert(kSCol + kLT <= 512 && kUsed <= 227 * 1024 && kBar % 8 == 0 && kStages <= 8, "layout");
@@ -117,17 +118,54 @@ constexpr uint32_t kIdS = (1u << 4) | (kLT / 8 << 17) | (128u / 16 << 24);
 constexpr uint32_t kIdOHi = (1u << 4) | (1u << 15) | (kLRows / 8 << 17) | (128u / 16 << 24);  // A MN-major
 constexpr uint32_t kIdOLo = kIdOHi | (1u << 10);
 
-// 16 lanes x 64 columns of TMEM: register 4j + 2i + e holds row lane/4 + 8i, column 8j + 2(lane%4) + e.
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&v)[32]) {
+// 16 lanes x 32 columns of TMEM, without the wait: register 4j + 2i + e holds row
+// lane/4 + 8i, column 8j + 2(lane%4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+// Wait for the thread's TMEM loads; a and b pass through, so their uses stay behind it.
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
+               :
+               : "memory");
+}
+// Two fp32 values side by side.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 __device__ __forceinline__ void tmem_st_16x256b_x1(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -156,7 +194,7 @@ __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ bool softmax_or(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(v ? 1u : 0u)
       : "memory");
@@ -280,7 +318,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
   Plan* plan = reinterpret_cast<Plan*>(misc + 2);
-  int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [6]
+  int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [warps]
   volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
   const LWaits wait{abort, p.wait_ns};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -291,14 +329,15 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       mbar_init(bars + 8 * (kLEmpty + s), 1);
     }
     mbar_init(bars + 8 * kLSFull, 1);
-    mbar_init(bars + 8 * kLSFree, 4);
-    mbar_init(bars + 8 * kLQFull, 4);
+    mbar_init(bars + 8 * kLSFree, kLSmWarps);
+    mbar_init(bars + 8 * kLQFull, kLSmWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (kLPFull + i), 4);
+      mbar_init(bars + 8 * (kLPFull + i), kLSmWarps);
       mbar_init(bars + 8 * (kLPvDone + i), 1);
     }
     mbar_init(bars + 8 * kLDrain, 1);
     *abort = 0;
+    misc[32] = misc[33] = 0u;
     plan->lo = plan->hi = plan->base = 0;
     plan->b = 0;
     fence_barrier_init();
@@ -345,16 +384,24 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   Unit u;
   bool failed = false;
 
-  if (warp < 4) {
+  if (warp < kLSmWarps) {
     // ------------------------------------------------------------ softmax
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t tw = tmem + ((uint32_t)(32 * warp) << 16);
-    const int lr[2] = {16 * warp + g, 16 * warp + g + 8};
-    float* alpha = reinterpret_cast<float*>(base + G::kAlpha);  // [64], then a second factor [64]
-    uint32_t it = 0, sph = 0;  // tiles so far
+    // warp w: rows 16 (w & 3) .. + 15, whose scores lie in its 32 TMEM lanes, and the
+    // positions 32 (w >> 2) .. + 31 of a tile
+    const int g = lane >> 2, t = lane & 3, quad = warp & 3, half = warp >> 2;
+    const uint32_t tw = tmem + ((uint32_t)(32 * quad) << 16);
+    const int lr[2] = {16 * quad + g, 16 * quad + g + 8};
+    float* alpha = reinterpret_cast<float*>(base + G::kAlpha);
+    float* two = reinterpret_cast<float*>(base + G::kTwo) + half * kLRows;  // [3][2][64], this half's
+    const auto both = [&](int k, int r) {  // what the two halves put down for row r
+      const float* x = reinterpret_cast<const float*>(base + G::kTwo) + k * 2 * kLRows + r;
+      return make_float2(x[0], x[kLRows]);
+    };
+    volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 32;  // [2] a softmax wait did, by the tile's parity
+    uint32_t it = 0;  // tiles so far
     while (walk.next(u, tid == 0 ? p.flag : nullptr)) {
       const int64_t row0 = (int64_t)u.b * p.chunk * p.hq + (int64_t)u.r * kLRows;
-      if (u.t0 >= u.t1) {  // nothing attended: a zero row, or a part without weight
+      if (u.t0 >= u.t1) {  // nothing attended: zero rows, or a part without weight
         if (u.whole) {
           for (int i = tid; i < u.rows * (L / 4); i += kLSoftmax) {
             const int64_t at = row0 * L + 4 * (int64_t)i;
@@ -368,103 +415,138 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
         continue;
       }
-      // q: a warp takes 16 rows, four lanes a row's 64-byte pieces; hi to lanes 0..15, lo
-      // to lanes 16..31 of the warp's TMEM lanes
-      uint4 qv[2][kSteps];
+      // q: four lanes share a row's 64-byte pieces, the two halves take every second
+      // one; hi to lanes 0..15, lo to lanes 16..31 of the quarter's TMEM lanes
+      constexpr int kOwn = (kSteps + 1) / 2;
+      uint4 qv[2][kOwn];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          qv[i][s] = make_uint4(0u, 0u, 0u, 0u);
-          if (lr[i] < u.rows)
-            qv[i][s] = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + lr[i]) * (L + R) + 32 * s + 8 * t));
+        for (int k = 0; k < kOwn; ++k) {
+          const int s = 2 * k + half;
+          qv[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          if (lr[i] < u.rows && s < kSteps)
+            qv[i][k] = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + lr[i]) * (L + R) + 32 * s + 8 * t));
         }
-      float xs[2];       // S to log2 units, before the token's scale
-      int64_t last[2];   // last position that the row attends
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t am = 0u;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const uint32_t w[4] = {qv[i][s].x, qv[i][s].y, qv[i][s].z, qv[i][s].w};
+        for (int k = 0; k < kOwn; ++k) {
+          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) am = max(am, max(w[k] << 16 & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+          for (int c = 0; c < 4; ++c) am = max(am, max(w[c] << 16 & 0x7FFFFFFFu, w[c] & 0x7FFF0000u));
         }
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-        const int ex = max((int)(am >> 23), 8);  // times 2^(134 - ex): to [2^7, 2^8)
-        const bool bad = am >= 0x7F800000u;      // an Inf or NaN: the row's scores are NaN, its codes 0
-        const float mul = __uint_as_float((uint32_t)(261 - min(ex, 254)) << 23);
-        xs[i] = bad ? __uint_as_float(0x7FFFFFFFu) : p.scale_log2 * __uint_as_float((uint32_t)(min(ex, 254) - 7) << 23);
-        if (bad) {
+        if (t == 0) two[lr[i]] = __uint_as_float(am);
+      }
+      named_barrier_sync(1, kLSoftmax);
+      float xs[2];      // S to log2 units, before the token's scale
+      int64_t last[2];  // last position that the row attends
+      bool plain = true;  // the short form of scores and sums has the range it needs
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) qv[i][s] = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float2 ab = both(0, lr[i]);
+        const uint32_t am = max(__float_as_uint(ab.x), __float_as_uint(ab.y));
+        const int ex = min(max((int)(am >> 23), 8), 254);  // times 2^(134 - ex): to [2^7, 2^8)
+        const bool bad = am >= 0x7F800000u;  // an Inf or NaN: the row's scores are NaN, its codes 0
+        const float mul = __uint_as_float((uint32_t)(261 - ex) << 23);
+        xs[i] = bad ? __uint_as_float(0x7FFFFFFFu) : p.scale_log2 * __uint_as_float((uint32_t)(ex - 7) << 23);
+        plain = plain && !(xs[i] > 1.15e18f);  // (a NaN stays one in either form)
         last[i] = lr[i] < u.rows ? u.first + (u.r * kLRows + lr[i]) / p.hq : -1;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {  // in place: x, y the hi codes, z, w the lo codes
-          const uint32_t w[4] = {qv[i][s].x, qv[i][s].y, qv[i][s].z, qv[i][s].w};
+        for (int k = 0; k < kOwn; ++k) {  // in place: x, y the hi codes, z, w the lo codes
+          if (bad) qv[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
           uint32_t h[4], l[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = bf16_lo(w[k]) * mul, x1 = bf16_hi(w[k]) * mul;
-            h[k] = e4m3x2_from_f32(x0, x1);
-            const float2 y = f16x2_to_float2(f16x2_from_e4m3x2(h[k]));
-            l[k] = e4m3x2_from_f32(x0 - y.x, x1 - y.y);
+          for (int c = 0; c < 4; ++c) {
+            const float x0 = bf16_lo(w[c]) * mul, x1 = bf16_hi(w[c]) * mul;
+            h[c] = e4m3x2_from_f32(x0, x1);
+            const float2 y = f16x2_to_float2(f16x2_from_e4m3x2(h[c]));
+            l[c] = e4m3x2_from_f32(x0 - y.x, x1 - y.y);
           }
-          qv[i][s] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, l[0] | l[1] << 16, l[2] | l[3] << 16);
+          qv[i][k] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, l[0] | l[1] << 16, l[2] | l[3] << 16);
         }
       }
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        tmem_st_16x256b_x1(tw + G::kQCol + 8 * s, qv[0][s].x, qv[0][s].y, qv[1][s].x, qv[1][s].y);
-        tmem_st_16x256b_x1(tw + (16u << 16) + G::kQCol + 8 * s, qv[0][s].z, qv[0][s].w, qv[1][s].z, qv[1][s].w);
+      for (int k = 0; k < kOwn; ++k) {
+        const int s = 2 * k + half;
+        if (s < kSteps) {
+          tmem_st_16x256b_x1(tw + G::kQCol + 8 * s, qv[0][k].x, qv[0][k].y, qv[1][k].x, qv[1][k].y);
+          tmem_st_16x256b_x1(tw + (16u << 16) + G::kQCol + 8 * s, qv[0][k].z, qv[0][k].w, qv[1][k].z, qv[1][k].w);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * kLQFull);
 
-      float ref[2] = {-INFINITY, -INFINITY}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      // l counts 2^(y - m).  Short form: m is ref, and 2^(y - ref) is x 2^-e.  That would lose
+      // what scales far apart leave under fp32's range: from a tile with a scale outside
+      // 2^-40 .. 2^40 on, m is the thread's own largest y, with exponentials of its own.
+      float ref[2] = {-INFINITY, -INFINITY}, m[2] = {-INFINITY, -INFINITY};
+      uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
       for (int j = u.t0; j < u.t1; ++j, ++it) {
         const int st = (int)(it % G::kStages);
         if (!failed) failed = !wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u);
-        if (!failed) failed = !wait(bars + 8 * kLSFull, sph & 1u);
-        ++sph;
+        if (!failed) failed = !wait(bars + 8 * kLSFull, it & 1u);
         tc_fence_after();
-        uint32_t v[32], lo[32];
-        tmem_ld_16x256b_x8(tw + G::kSCol, v);
-        tmem_ld_16x256b_x8(tw + (16u << 16) + G::kSCol, lo);
-        tmem_wait_ld(v);
-        tmem_wait_ld(lo);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
+        uint32_t v[16], lo[16];
+        tmem_ld_16x256b_x4(tw + G::kSCol + 32 * half, v);
+        tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + 32 * half, lo);
+        // the tokens' scales: exponent, 2^e and 2^-e, two tokens side by side
+        uint32_t e2[4];
+        bool near = plain;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e2[k] = lds16(sb + G::kExp + st * kLT + 32 * half + 8 * k + 2 * t);
+          near = near && (e2[k] & 0xFFu) - 87u <= 80u && (e2[k] >> 8) - 87u <= 80u;  // 2^-40 .. 2^40
+        }
+        plain = near = __all_sync(0xFFFFFFFFu, near);  // (the long form up to the unit's end)
         const uint64_t ok = vmask[st];
         const int64_t p0 = (int64_t)j * kLT;
         const bool part = ok != ~0ull || p0 + kLT > full_upto;  // some row sees the tile in part
-        float y[2][16], z[2][16], top[2] = {-INFINITY, -INFINITY}, my[2] = {m[0], m[1]};
+        tmem_wait_ld2(v, lo);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
+        uint64_t z2[2][4];
+        float top[2] = {-INFINITY, -INFINITY}, my[2] = {m[0], m[1]};
+        uint64_t inv2[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t e2 = lds16(sb + G::kExp + st * kLT + 8 * k + 2 * t);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t ea = e2[k] & 0xFFu, eb = e2[k] >> 8;
+          const uint64_t s2 = pack2(latent_scale(ea), latent_scale(eb));
+          const uint64_t x2 = add2(pack2(__uint_as_float(0x4B000000u | ea), __uint_as_float(0x4B000000u | eb)),
+                                   pack2(-8388735.0f, -8388735.0f));  // the exponents as floats
+          inv2[k] = pack2(__uint_as_float((254u - ea) << 23), __uint_as_float((254u - eb) << 23));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t ev = e ? e2 >> 8 : e2 & 0xFFu;
-            const float s = latent_scale(ev), es = (float)(int)(ev - 127u);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float S = __uint_as_float(v[4 * k + 2 * i + e]) + __uint_as_float(lo[4 * k + 2 * i + e]);
-              float yy = S * (xs[i] * s);
-              if (part) {
-                const int c = 8 * k + 2 * t + e;
-                if (p0 + c > last[i] || !((ok >> c) & 1ull)) yy = -INFINITY;
-              }
-              const float zz = yy + es;
-              y[i][2 * k + e] = yy;
-              z[i][2 * k + e] = zz;
-              top[i] = fmaxf(top[i], zz);
-              my[i] = fmaxf(my[i], yy);
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t S = add2(pack2(__uint_as_float(v[4 * k + 2 * i]), __uint_as_float(v[4 * k + 2 * i + 1])),
+                                    pack2(__uint_as_float(lo[4 * k + 2 * i]), __uint_as_float(lo[4 * k + 2 * i + 1])));
+            uint64_t z;
+            if (near) {
+              z = fma2(mul2(S, pack2(xs[i], xs[i])), s2, x2);
+            } else {  // S xs alone could leave the range
+              const uint64_t y = mul2(S, mul2(pack2(xs[i], xs[i]), s2));
+              z = add2(y, x2);
+            }
+            if (part) {
+              const int c = 32 * half + 8 * k + 2 * t;
+              float2 f = unpack2(z);
+              if (p0 + c > last[i] || !((ok >> c) & 1ull)) f.x = -INFINITY;
+              if (p0 + c + 1 > last[i] || !((ok >> (c + 1)) & 1ull)) f.y = -INFINITY;
+              z = pack2(f.x, f.y);
+            }
+            z2[i][k] = z;
+            const float2 f = unpack2(z);
+            top[i] = fmaxf(top[i], fmaxf(f.x, f.y));
+            if (!near) {
+              const float2 x = unpack2(x2);
+              my[i] = fmaxf(my[i], fmaxf(f.x - x.x, f.y - x.y));
             }
           }
         }
@@ -472,104 +554,137 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-          my[i] = fmaxf(my[i], __shfl_xor_sync(0xFFFFFFFFu, my[i], 1));
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-          my[i] = fmaxf(my[i], __shfl_xor_sync(0xFFFFFFFFu, my[i], 2));
           up |= top[i] > ref[i] + kSlackL;
         }
-        if (softmax_or(up)) {
-          // raise the references; O's columns follow (none at the unit's first tile)
+        if (failed) gave_up[it & 1] = 1;
+        if (softmax_or(up || failed)) {
+          if (gave_up[it & 1]) {
+            failed = true;
+            break;
+          }
+          // raise the references of the rows that need it (what a row gives does not depend on
+          // others); O's columns follow (none at the unit's first tile)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (t == 0) two[2 * kLRows + lr[i]] = top[i];
+          named_barrier_sync(1, kLSoftmax);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float to = fmaxf(ref[i], floorf(top[i]));
-            if (t == 0) alpha[lr[i]] = ref[i] == -INFINITY ? 0.0f : fast_exp2(ref[i] - to);
+            const float2 ab = both(1, lr[i]);
+            const float most = fmaxf(ab.x, ab.y), to = most > ref[i] + kSlackL ? floorf(most) : ref[i];
+            const float a = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
+            if (t == 0 && half == 0) alpha[lr[i]] = a;
+            if (near) {
+              m[i] = to;
+              l2[i] = mul2(l2[i], pack2(a, a));
+            }
             ref[i] = to;
           }
           named_barrier_sync(1, kLSoftmax);
           if (j > u.t0) {
-            if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
+            failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < kM * 2; ++cc) {
+            for (int mm = 0; mm < kM; ++mm) {
               uint32_t o[32];
-              tmem_ld32(tw + G::kOCol + 32 * cc, o);
+              const uint32_t at = tw + G::kOCol + kLRows * mm + 32 * half;
+              tmem_ld32(at, o);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(alpha + 32 * (cc & 1) + 4 * k);
+                const float4 a = *reinterpret_cast<const float4*>(alpha + 32 * half + 4 * k);
                 o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
                 o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
                 o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
                 o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * a.w);
               }
-              tmem_st32_async(tw + G::kOCol + 32 * cc, o);
+              tmem_st32_async(at, o);
             }
             tmem_wait_st();
             tc_fence_before();
           }
         }
         // x in two parts to shared memory, [16 tokens][8 rows] core matrices
-        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes;
+        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(half * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float rf = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop;
-          const float mm = my[i] == -INFINITY ? 0.0f : my[i];
-          float sum = 0.0f;
-          const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16 + 2 * t);
+          const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
+          const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16);
+          if (!near) {
+            const float to = my[i], zero = to == -INFINITY ? 0.0f : to;
+            const float a = m[i] == -INFINITY ? 1.0f : fast_exp2(m[i] - to);
+            l2[i] = mul2(l2[i], pack2(a, a));
+            m[i] = to;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            sum += fast_exp2(y[i][2 * k] - mm) + fast_exp2(y[i][2 * k + 1] - mm);
-            const uint32_t h = pack_f16x2(fast_exp2(z[i][2 * k] - rf), fast_exp2(z[i][2 * k + 1] - rf));
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack2(z2[i][k]);
+              const float ea = (float)(int)((e2[k] & 0xFFu) - 127u), eb = (float)(int)((e2[k] >> 8) - 127u);
+              l2[i] = add2(l2[i], pack2(fast_exp2((f.x - ea) - zero), fast_exp2((f.y - eb) - zero)));
+            }
+          }
+          uint64_t sum = 0ull;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
+            const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
+            if (near) sum = fma2(pack2(xa, xb), inv2[k], sum);
+            const uint32_t h = pack_f16x2(xa, xb);
             const uint32_t hi = e4m3x2_of_f16x2(h);
             const uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
             const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
             sts_u16(a, hi);
             sts_u16(a + kPBytes, rest);
           }
-          l[i] = l[i] * fast_exp2((m[i] == -INFINITY ? mm : m[i]) - mm) + sum;
-          m[i] = my[i];
+          if (near) l2[i] = fma2(sum, pack2(0.03125f, 0.03125f), l2[i]);  // 2^-kTop
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + (it & 1)));
-        if (*abort) failed = true;
-        if (softmax_or(failed)) {
-          failed = true;
-          break;
-        }
       }
-      if (failed) break;
-      // the unit's result
-      float lse[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-        const float mm = m[i] == -INFINITY ? 0.0f : m[i];
-        const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm, half = rintf(0.5f * d);
-        lse[i] = l[i] == 0.0f ? -INFINITY : mm + log2f(l[i]);
-        if (t == 0) {  // two factors: 2^d alone can leave fp32's range
-          alpha[lr[i]] = fast_exp2(half);
-          alpha[kLRows + lr[i]] = l[i] == 0.0f ? 0.0f : fast_exp2(d - half) / l[i];
-        }
-      }
-      failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
+      // the unit's result: O / l, l over both halves and a reference of both
+      if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
       if (softmax_or(failed)) {
         failed = true;
         break;
       }
+      float l[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mm = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 2));
+        const float2 x = unpack2(l2[i]);
+        l[i] = (x.x + x.y) * (m[i] == -INFINITY ? 1.0f : fast_exp2(m[i] - mm));
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+        if (t == 0) {
+          two[2 * kLRows + lr[i]] = mm;
+          two[4 * kLRows + lr[i]] = l[i];
+        }
+      }
+      named_barrier_sync(1, kLSoftmax);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 ma = both(1, lr[i]), la = both(2, lr[i]);
+        const float top = fmaxf(ma.x, ma.y), mm = top == -INFINITY ? 0.0f : top;
+        const float lx = (ma.x == -INFINITY ? la.x : la.x * fast_exp2(ma.x - mm)) +
+                         (ma.y == -INFINITY ? la.y : la.y * fast_exp2(ma.y - mm));
+        const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm, h = rintf(0.5f * d);
+        if (t == 0 && half == 0) {  // two factors: 2^d alone can leave fp32's range
+          alpha[lr[i]] = fast_exp2(h);
+          alpha[kLRows + lr[i]] = lx == 0.0f ? 0.0f : fast_exp2(d - h) / lx;
+          if (!u.whole)
+            p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + lr[i]] = lx == 0.0f ? -INFINITY : mm + log2f(lx);
+        }
+      }
+      named_barrier_sync(1, kLSoftmax);
       tc_fence_after();
       float* po = p.part_o + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows * L;
-      if (!u.whole && t == 0) {
-        float* pl = p.part_lse + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows;
-        pl[lr[0]] = lse[0];
-        pl[lr[1]] = lse[1];
-      }
 #pragma unroll 1
-      for (int cc = 0; cc < kM * 2; ++cc) {
-        const int c0 = 32 * (cc & 1), ch = 128 * (cc >> 1) + 32 * warp + lane;
-        if (c0 >= u.rows) continue;
+      for (int mm = 0; mm < kM; ++mm) {
+        const int c0 = 32 * half, ch = 128 * mm + 32 * quad + lane;
+        if (c0 >= u.rows) break;
         uint32_t o[32];
-        tmem_ld32(tw + G::kOCol + 32 * cc, o);
+        tmem_ld32(tw + G::kOCol + kLRows * mm + c0, o);
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const int r = c0 + c;
@@ -586,7 +701,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
       }
       tc_fence_before();
-      named_barrier_sync(1, kLSoftmax);  // alpha is free again
+      named_barrier_sync(1, kLSoftmax);  // alpha and what the halves exchanged are free again
     }
   } else if (warp == kLdWarpL) {
     // ------------------------------------------------------------ loader
