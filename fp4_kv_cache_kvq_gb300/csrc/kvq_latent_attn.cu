@@ -28,12 +28,13 @@
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
 // the longest first.
-// Ten warps: softmax (8; thread = two rows x 8 positions of a tile), loader, MMA
-// issue, joined by mbarriers (every wait bounded):
+// Eleven warps: softmax (8; thread = two rows x 8 positions of a tile), loader, MMA
+// issue, scales, joined by mbarriers (every wait bounded):
 //   loader    bulk copies of 64-token tiles into a ring
 //   MMA       S(j) = q K(j)^T                 kind::f8f6f4, q from TMEM
 //             O^T += K(j)^T x(j)              kind::f8f6f4, twice (hi, lo)
 //             in the order S(j + 1), O(j)
+//   scales    2^e, e and 2^-e of a tile's tokens, once for all rows
 #include "kvq_latent.cuh"
 #include "kvq_tc.cuh"
 
@@ -44,8 +45,8 @@ namespace {
 
 constexpr int kLT = 64;     // positions per tile
 constexpr int kLRows = 64;  // query rows per unit
-constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 64;
-constexpr int kLdWarpL = kLSmWarps;  // and the MMA warp behind it
+constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 96;
+constexpr int kLdWarpL = kLSmWarps, kMmaWarpL = kLdWarpL + 1;  // and the scales' warp behind them
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 4;           // least tiles of a split range
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
@@ -60,7 +61,8 @@ enum : int {
   kLQFull = kLSFree + 1,    // q in TMEM
   kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
   kLPvDone = kLPFull + 2,   // [2] O += done
-  kLDrain = kLPvDone + 2,   // the MMA warp's last commit
+  kLScFull = kLPvDone + 2,  // [stages] what the softmax takes of a tile's tokens
+  kLDrain = kLScFull + 8,   // the MMA warp's last commit
   kLBars = kLDrain + 1
 };
 
@@ -91,7 +93,9 @@ struct LGeo {
   static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
   static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns, [64] second ones
   static constexpr int kTwo = kAlpha + 2 * 4 * kLRows;    // [3][2][64] what the two halves of a row exchange
-  static constexpr int kBar = kTwo + 3 * 2 * 4 * kLRows;
+  static constexpr int kSc = kTwo + 3 * 2 * 4 * kLRows;   // [stages][3][64] 2^e, e (-inf: no token), 2^-e
+  static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40
+  static constexpr int kBar = kNear + 4 * 8;
   static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, plan
   static constexpr int kUsed = kMisc + 192 + 128;
   static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;  // one CTA per SM: it holds all of TMEM
@@ -186,6 +190,14 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];\n" : "=l"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
@@ -319,6 +331,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
   Plan* plan = reinterpret_cast<Plan*>(misc + 2);
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [warps]
+  volatile int* near_s = reinterpret_cast<volatile int*>(base + G::kNear);
   volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
   const LWaits wait{abort, p.wait_ns};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -327,6 +340,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(bars + 8 * (kLFull + s), 1);
       mbar_init(bars + 8 * (kLEmpty + s), 1);
+      mbar_init(bars + 8 * (kLScFull + s), 1);
     }
     mbar_init(bars + 8 * kLSFull, 1);
     mbar_init(bars + 8 * kLSFree, kLSmWarps);
@@ -491,64 +505,54 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
       for (int j = u.t0; j < u.t1; ++j, ++it) {
         const int st = (int)(it % G::kStages);
-        if (!failed) failed = !wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u);
+        if (!failed) failed = !wait(bars + 8 * (kLScFull + st), (it / G::kStages) & 1u);
         if (!failed) failed = !wait(bars + 8 * kLSFull, it & 1u);
         tc_fence_after();
         uint32_t v[16], lo[16];
         tmem_ld_16x256b_x4(tw + G::kSCol + 32 * half, v);
         tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + 32 * half, lo);
-        // the tokens' scales: exponent, 2^e and 2^-e, two tokens side by side
-        uint32_t e2[4];
-        bool near = plain;
+        const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
+        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (32 * half + 2 * t));
+        uint64_t s2[4], x2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          e2[k] = lds16(sb + G::kExp + st * kLT + 32 * half + 8 * k + 2 * t);
-          near = near && (e2[k] & 0xFFu) - 87u <= 80u && (e2[k] >> 8) - 87u <= 80u;  // 2^-40 .. 2^40
+          s2[k] = lds_f32x2(sc + 32 * k);
+          x2[k] = lds_f32x2(sc + 4 * kLT + 32 * k);
         }
-        plain = near = __all_sync(0xFFFFFFFFu, near);  // (the long form up to the unit's end)
-        const uint64_t ok = vmask[st];
         const int64_t p0 = (int64_t)j * kLT;
-        const bool part = ok != ~0ull || p0 + kLT > full_upto;  // some row sees the tile in part
+        const bool part = p0 + kLT > full_upto;  // some row sees the tile in part
         tmem_wait_ld2(v, lo);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
         uint64_t z2[2][4];
-        float top[2] = {-INFINITY, -INFINITY}, my[2] = {m[0], m[1]};
-        uint64_t inv2[4];
+        float top[2], my[2] = {m[0], m[1]};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t ea = e2[k] & 0xFFu, eb = e2[k] >> 8;
-          const uint64_t s2 = pack2(latent_scale(ea), latent_scale(eb));
-          const uint64_t x2 = add2(pack2(__uint_as_float(0x4B000000u | ea), __uint_as_float(0x4B000000u | eb)),
-                                   pack2(-8388735.0f, -8388735.0f));  // the exponents as floats
-          inv2[k] = pack2(__uint_as_float((254u - ea) << 23), __uint_as_float((254u - eb) << 23));
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int k = 0; k < 4; ++k) {
             const uint64_t S = add2(pack2(__uint_as_float(v[4 * k + 2 * i]), __uint_as_float(v[4 * k + 2 * i + 1])),
                                     pack2(__uint_as_float(lo[4 * k + 2 * i]), __uint_as_float(lo[4 * k + 2 * i + 1])));
-            uint64_t z;
-            if (near) {
-              z = fma2(mul2(S, pack2(xs[i], xs[i])), s2, x2);
-            } else {  // S xs alone could leave the range
-              const uint64_t y = mul2(S, mul2(pack2(xs[i], xs[i]), s2));
-              z = add2(y, x2);
-            }
-            if (part) {
-              const int c = 32 * half + 8 * k + 2 * t;
-              float2 f = unpack2(z);
-              if (p0 + c > last[i] || !((ok >> c) & 1ull)) f.x = -INFINITY;
-              if (p0 + c + 1 > last[i] || !((ok >> (c + 1)) & 1ull)) f.y = -INFINITY;
-              z = pack2(f.x, f.y);
-            }
-            z2[i][k] = z;
-            const float2 f = unpack2(z);
-            top[i] = fmaxf(top[i], fmaxf(f.x, f.y));
-            if (!near) {
-              const float2 x = unpack2(x2);
-              my[i] = fmaxf(my[i], fmaxf(f.x - x.x, f.y - x.y));
+            z2[i][k] = near ? fma2(mul2(S, pack2(xs[i], xs[i])), s2[k], x2[k])
+                            : add2(mul2(S, mul2(pack2(xs[i], xs[i]), s2[k])), x2[k]);  // S xs could leave the range
+          }
+          if (part) {
+            const int lim = (int)max((int64_t)-1, min((int64_t)kLT, last[i] - p0)) - 32 * half - 2 * t;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack2(z2[i][k]);
+              z2[i][k] = pack2(8 * k > lim ? -INFINITY : f.x, 8 * k + 1 > lim ? -INFINITY : f.y);
             }
           }
+          if (!near) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
+              my[i] = fmaxf(my[i], fmaxf(x.x == -INFINITY ? x.x : f.x - x.x, x.y == -INFINITY ? x.y : f.y - x.y));
+            }
+          }
+          const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
+          top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
         bool up = false;
 #pragma unroll
@@ -617,9 +621,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             m[i] = to;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 f = unpack2(z2[i][k]);
-              const float ea = (float)(int)((e2[k] & 0xFFu) - 127u), eb = (float)(int)((e2[k] >> 8) - 127u);
-              l2[i] = add2(l2[i], pack2(fast_exp2((f.x - ea) - zero), fast_exp2((f.y - eb) - zero)));
+              const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
+              l2[i] = add2(l2[i], pack2(x.x == -INFINITY ? 0.0f : fast_exp2((f.x - x.x) - zero),
+                                        x.y == -INFINITY ? 0.0f : fast_exp2((f.y - x.y) - zero)));
             }
           }
           uint64_t sum = 0ull;
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           for (int k = 0; k < 4; ++k) {
             const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
-            if (near) sum = fma2(pack2(xa, xb), inv2[k], sum);
+            if (near) sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
             const uint32_t h = pack_f16x2(xa, xb);
             const uint32_t hi = e4m3x2_of_f16x2(h);
             const uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
              global_ns() - t0 < 20000000ull) {
       }
     }
-  } else {
+  } else if (warp == kMmaWarpL) {
     // ------------------------------------------------------------ MMA issue
     const uint64_t dk = smem_desc(sb, 128, 8 * G::kRow);           // tokens as rows: K-major
     const uint64_t dv = smem_desc(sb, 8 * G::kRow, 128);           // channels as rows: MN-major
@@ -785,10 +789,10 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         if (!failed && it > 0 && !wait(bars + 8 * kLSFree, (it - 1) & 1u)) failed = true;
         if (failed) break;
         const uint64_t ok = vmask[st];
-        if (ok != ~0ull) {  // rows without a token: whatever lies there must not meet a weight of 0 as NaN
+        if (ok != ~0ull) {  // rows without a token: no NaN there may reach a score or meet a weight of 0
           const uint32_t tile = sb + st * G::kTile;
-          for (int i = lane; i < kLT * (L / 16); i += 32) {
-            const int tok = (i & 7) | (i / (8 * (L / 16))) << 3, un16 = i / 8 % (L / 16);
+          for (int i = lane; i < kLT * (G::kRow / 16); i += 32) {
+            const int tok = (i & 7) | (i / (8 * (G::kRow / 16))) << 3, un16 = i / 8 % (G::kRow / 16);
             if (!((ok >> tok) & 1ull)) sts128(tile + (tok >> 3) * 8 * G::kRow + un16 * 128 + (tok & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
           }
           fence_async_smem();
@@ -818,6 +822,39 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     __syncwarp();
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait_hint(bars + 8 * kLDrain, 0u, 20000u) && global_ns() - t0 < 20000000ull) {
+    }
+  } else {
+    // ------------------------------------------------------------ scales
+    uint32_t it = 0;
+    while (!failed && walk.next(u, nullptr)) {
+      for (int j = u.t0; j < u.t1; ++j, ++it) {
+        const int st = (int)(it % G::kStages);
+        if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u)) {
+          failed = true;
+          break;
+        }
+        const uint64_t ok = vmask[st];
+        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 8 * lane);
+        const uint32_t e2 = lds16(sb + G::kExp + st * kLT + 2 * lane);
+        float s[2], x[2], inv[2];
+        bool near = true;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t e = i ? e2 >> 8 : e2 & 0xFFu;
+          const bool in = (ok >> (2 * lane + i)) & 1ull;
+          s[i] = in ? latent_scale(e) : 1.0f;
+          x[i] = in ? (float)((int)e - 127) : -INFINITY;
+          inv[i] = in ? __uint_as_float((254u - e) << 23) : 1.0f;
+          near = near && (!in || e - 87u <= 80u);  // 2^-40 .. 2^40
+        }
+        sts_f32x2(sc, s[0], s[1]);
+        sts_f32x2(sc + 4 * kLT, x[0], x[1]);
+        sts_f32x2(sc + 8 * kLT, inv[0], inv[1]);
+        near = __all_sync(0xFFFFFFFFu, near);
+        if (lane == 0) near_s[st] = near;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kLScFull + st));
+      }
     }
   }
   tc_fence_before();
