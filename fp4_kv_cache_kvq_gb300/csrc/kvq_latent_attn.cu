@@ -202,6 +202,13 @@ __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
+// One lane of a converged warp.  (A lane picked by its number makes the compiler treat
+// the descriptors as different from lane to lane: 70 cycles an MMA.)
+__device__ __forceinline__ bool elect_one_of_warp() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // Named barrier 1 of the softmax warps; true when any thread's v is.
 __device__ __forceinline__ bool softmax_or(bool v) {
   uint32_t r;
@@ -762,7 +769,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     const auto sums_of = [&](uint32_t i, bool first) {  // O^T (+)= K(i)^T x(i)
       if (!wait(bars + 8 * (kLPFull + (i & 1)), (i >> 1) & 1u)) return false;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one_of_warp()) {
         const uint64_t a = dv + (uint64_t)((i % G::kStages) * (G::kTile >> 4));
         const uint64_t b = dp + (uint64_t)((i & 1) * (2 * kPBytes >> 4));
 #pragma unroll
@@ -799,7 +806,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           __syncwarp();
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one_of_warp()) {
           const uint64_t kd = dk + (uint64_t)(st * (G::kTile >> 4));
 #pragma unroll
           for (int s = 0; s < kSteps + R / 32; ++s) {
