@@ -28,12 +28,12 @@
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
 // the longest first.
-// Eleven warps: softmax (8; thread = two rows x 8 positions of a tile), loader, MMA
-// issue, scales, joined by mbarriers (every wait bounded):
+// Twelve warps: softmax (8; thread = two rows x 8 positions of a tile), loader, two
+// that issue the products, scales, joined by mbarriers (every wait bounded):
 //   loader    bulk copies of 64-token tiles into a ring
-//   MMA       S(j) = q K(j)^T                 kind::f8f6f4, q from TMEM
-//             O^T += K(j)^T x(j)              kind::f8f6f4, twice (hi, lo)
-//             in the order S(j + 1), O(j)
+//   products  S(j) = q K(j)^T         kind::f8f6f4, q from TMEM
+//             O^T += K(j)^T x(j)      kind::f8f6f4, twice (hi, lo), from another warp:
+//             one's waits do not hold up the other's products
 //   scales    2^e, e and 2^-e of a tile's tokens, once for all rows
 #include "kvq_latent.cuh"
 #include "kvq_tc.cuh"
@@ -45,8 +45,8 @@ namespace {
 
 constexpr int kLT = 64;     // positions per tile
 constexpr int kLRows = 64;  // query rows per unit
-constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 96;
-constexpr int kLdWarpL = kLSmWarps, kMmaWarpL = kLdWarpL + 1;  // and the scales' warp behind them
+constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 128;
+constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 1;  // and the scales' warp
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 4;           // least tiles of a split range
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
@@ -62,7 +62,7 @@ enum : int {
   kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
   kLPvDone = kLPFull + 2,   // [2] O += done
   kLScFull = kLPvDone + 2,  // [stages] what the softmax takes of a tile's tokens
-  kLDrain = kLScFull + 8,   // the MMA warp's last commit
+  kLDrain = kLScFull + 8,   // the last commits of the two issuing warps
   kLBars = kLDrain + 1
 };
 
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       mbar_init(bars + 8 * (kLPFull + i), kLSmWarps);
       mbar_init(bars + 8 * (kLPvDone + i), 1);
     }
-    mbar_init(bars + 8 * kLDrain, 1);
+    mbar_init(bars + 8 * kLDrain, 2);
     *abort = 0;
     misc[32] = misc[33] = 0u;
     plan->lo = plan->hi = plan->base = 0;
@@ -615,7 +615,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             tc_fence_before();
           }
         }
-        // x in two parts to shared memory, [16 tokens][8 rows] core matrices
+        // x in two parts to shared memory, [16 tokens][8 rows] core matrices, once the sums
+        // of the tile before last have read theirs
+        if (it > 1 && !failed) failed = !wait(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
         const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(half * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -760,69 +762,77 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
              global_ns() - t0 < 20000000ull) {
       }
     }
-  } else if (warp == kMmaWarpL) {
-    // ------------------------------------------------------------ MMA issue
-    const uint64_t dk = smem_desc(sb, 128, 8 * G::kRow);           // tokens as rows: K-major
-    const uint64_t dv = smem_desc(sb, 8 * G::kRow, 128);           // channels as rows: MN-major
-    const uint64_t dp = smem_desc(sb + G::kP, 1024, 128);
-    uint32_t it = 0, un = 0;
-    const auto sums_of = [&](uint32_t i, bool first) {  // O^T (+)= K(i)^T x(i)
-      if (!wait(bars + 8 * (kLPFull + (i & 1)), (i >> 1) & 1u)) return false;
-      tc_fence_after();
-      if (elect_one_of_warp()) {
-        const uint64_t a = dv + (uint64_t)((i % G::kStages) * (G::kTile >> 4));
-        const uint64_t b = dp + (uint64_t)((i & 1) * (2 * kPBytes >> 4));
-#pragma unroll
-        for (int mm = 0; mm < kM; ++mm)
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {  // 32 tokens: four core matrices of V, two of x
-            const uint64_t am = a + (uint64_t)((mm * 1024 + s * 32 * G::kRow) >> 4);
-            mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)(s * 2048 >> 4), kIdOHi, !(first && s == 0));
-            mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)((s * 2048 + kPBytes) >> 4), kIdOLo, true);
+  } else if (warp == kSWarpL || warp == kOWarpL) {
+    uint32_t it = 0;
+    if (warp == kSWarpL) {
+      // ---------------------------------------------------------- scores
+      const uint64_t dk = smem_desc(sb, 128, 8 * G::kRow);  // tokens as rows: K-major
+      uint32_t un = 0;
+      while (!failed && walk.next(u, nullptr)) {
+        if (u.t0 >= u.t1) continue;
+        if (!wait(bars + 8 * kLQFull, un & 1u)) break;
+        ++un;
+        for (int j = u.t0; j < u.t1; ++j, ++it) {
+          const int st = (int)(it % G::kStages);
+          if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u) ||
+              (it > 0 && !wait(bars + 8 * kLSFree, (it - 1) & 1u))) {
+            failed = true;
+            break;
           }
-        tc_commit(bars + 8 * (kLEmpty + i % G::kStages));
-        tc_commit(bars + 8 * (kLPvDone + (i & 1)));
-      }
-      __syncwarp();
-      return true;
-    };
-    while (!failed && walk.next(u, nullptr)) {
-      if (u.t0 >= u.t1) continue;
-      if (!wait(bars + 8 * kLQFull, un & 1u)) break;
-      ++un;
-      for (int j = u.t0; j < u.t1; ++j, ++it) {
-        const int st = (int)(it % G::kStages);
-        if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u)) failed = true;
-        if (!failed && it > 0 && !wait(bars + 8 * kLSFree, (it - 1) & 1u)) failed = true;
-        if (failed) break;
-        const uint64_t ok = vmask[st];
-        if (ok != ~0ull) {  // rows without a token: no NaN there may reach a score or meet a weight of 0
-          const uint32_t tile = sb + st * G::kTile;
-          for (int i = lane; i < kLT * (G::kRow / 16); i += 32) {
-            const int tok = (i & 7) | (i / (8 * (G::kRow / 16))) << 3, un16 = i / 8 % (G::kRow / 16);
-            if (!((ok >> tok) & 1ull)) sts128(tile + (tok >> 3) * 8 * G::kRow + un16 * 128 + (tok & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+          const uint64_t ok = vmask[st];
+          if (ok != ~0ull) {  // rows without a token: no NaN there may reach a score or meet a weight of 0
+            const uint32_t tile = sb + st * G::kTile;
+            for (int i = lane; i < kLT * (G::kRow / 16); i += 32) {
+              const int tok = (i & 7) | (i / (8 * (G::kRow / 16))) << 3, unit = i / 8 % (G::kRow / 16);
+              if (!((ok >> tok) & 1ull))
+                sts128(tile + (tok >> 3) * 8 * G::kRow + unit * 128 + (tok & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_async_smem();
+            __syncwarp();
           }
-          fence_async_smem();
+          tc_fence_after();
+          if (elect_one_of_warp()) {
+            const uint64_t kd = dk + (uint64_t)(st * (G::kTile >> 4));
+#pragma unroll
+            for (int s = 0; s < kSteps + R / 32; ++s) {
+              const int a = s < kSteps ? s : s - R / 32;  // the key part's lo codes meet the same q
+              mma_f8_ta(tmem + G::kSCol, tmem + G::kQCol + 8 * a, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
+            }
+            tc_commit(bars + 8 * kLSFull);
+          }
           __syncwarp();
         }
-        tc_fence_after();
-        if (elect_one_of_warp()) {
-          const uint64_t kd = dk + (uint64_t)(st * (G::kTile >> 4));
-#pragma unroll
-          for (int s = 0; s < kSteps + R / 32; ++s) {
-            const int a = s < kSteps ? s : s - R / 32;  // the key part's lo codes meet the same q
-            mma_f8_ta(tmem + G::kSCol, tmem + G::kQCol + 8 * a, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
+      }
+    } else {
+      // ---------------------------------------------------------- sums: O^T (+)= K(j)^T x(j)
+      const uint64_t dv = smem_desc(sb, 8 * G::kRow, 128);  // channels as rows: MN-major
+      const uint64_t dp = smem_desc(sb + G::kP, 1024, 128);
+      while (!failed && walk.next(u, nullptr)) {
+        for (int j = u.t0; j < u.t1; ++j, ++it) {
+          if (!wait(bars + 8 * (kLPFull + (it & 1)), (it >> 1) & 1u)) {
+            failed = true;
+            break;
           }
-          tc_commit(bars + 8 * kLSFull);
-        }
-        __syncwarp();
-        if (j > u.t0 && !sums_of(it - 1, j - 1 == u.t0)) {
-          failed = true;
-          break;
+          tc_fence_after();
+          const int st = (int)(it % G::kStages);
+          const bool more = j > u.t0;
+          if (elect_one_of_warp()) {
+            const uint64_t a = dv + (uint64_t)(st * (G::kTile >> 4));
+            const uint64_t b = dp + (uint64_t)((it & 1) * (2 * kPBytes >> 4));
+#pragma unroll
+            for (int mm = 0; mm < kM; ++mm)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {  // 32 tokens: four core matrices of the tile, two of x
+                const uint64_t am = a + (uint64_t)((mm * 1024 + s * 32 * G::kRow) >> 4);
+                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)(s * 2048 >> 4), kIdOHi, more || s > 0);
+                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)((s * 2048 + kPBytes) >> 4), kIdOLo, true);
+              }
+            tc_commit(bars + 8 * (kLEmpty + st));
+            tc_commit(bars + 8 * (kLPvDone + (it & 1)));
+          }
+          __syncwarp();
         }
       }
-      if (failed) break;
-      if (!sums_of(it - 1, u.t1 - 1 == u.t0)) break;
     }
     // no product outlives the CTA
     if (lane == 0) tc_commit(bars + 8 * kLDrain);
