@@ -15,7 +15,7 @@
 //       values hi = RNE(q), lo = RNE(q - hi): exact down to 2^-9 of the row's
 //       largest element, off by at most 2^-17 of it below.  hi and lo are rows of
 //       one operand (128 rows for 64 queries); their scores are added in fp32.
-//   x   reaches 2^5 .. 2^8 in every row and is rounded to f16, then hi = E4M3(x),
+//   x   reaches 2^4 .. 2^8 in every row and is rounded to f16, then hi = E4M3(x),
 //       lo = E5M2(x - hi): 2^-8 of x, or 2^-14 under 2^-6, where hi's steps end
 //       and lo's range (down to 2^-17) takes over.  Two products of 8-bit operands
 //       cost what one of 16-bit ones costs and need no expansion of the values.
@@ -50,19 +50,19 @@ constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 4;           // least tiles of a split range
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
-// the references are raised only past the slack, since that rescales O.
-constexpr float kTop = 5.0f, kSlackL = 3.0f;
+// the references are raised only past the slack, since that rescales O.  (5 and 3: some
+// of 64 rows raised its own in every second tile, 1250 cycles each.)
+constexpr float kTop = 4.0f, kSlackL = 4.0f, kTopInv = 1.0f / 16.0f;
 
 enum : int {
   kLFull = 0,               // [stages] codes and exponents landed
   kLEmpty = kLFull + 8,     // [stages] the tile's sums done (commit)
-  kLSFull = kLEmpty + 8,    // S in TMEM
-  kLSFree = kLSFull + 1,    // S taken by the softmax warps
+  kLSFull = kLEmpty + 8,    // [stages] S in TMEM (commit), and the tile's scales ready
+  kLSFree = kLSFull + 8,    // S taken by the softmax warps
   kLQFull = kLSFree + 1,    // q in TMEM
   kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
   kLPvDone = kLPFull + 2,   // [2] O += done
-  kLScFull = kLPvDone + 2,  // [stages] what the softmax takes of a tile's tokens
-  kLDrain = kLScFull + 8,   // the last commits of the two issuing warps
+  kLDrain = kLPvDone + 2,   // the last commits of the two issuing warps
   kLBars = kLDrain + 1
 };
 
@@ -347,9 +347,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(bars + 8 * (kLFull + s), 1);
       mbar_init(bars + 8 * (kLEmpty + s), 1);
-      mbar_init(bars + 8 * (kLScFull + s), 1);
+      mbar_init(bars + 8 * (kLSFull + s), 2);
     }
-    mbar_init(bars + 8 * kLSFull, 1);
     mbar_init(bars + 8 * kLSFree, kLSmWarps);
     mbar_init(bars + 8 * kLQFull, kLSmWarps);
     for (int i = 0; i < 2; ++i) {
@@ -510,10 +509,10 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       float ref[2] = {-INFINITY, -INFINITY}, m[2] = {-INFINITY, -INFINITY};
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
+      bool ready = false;  // the next tile's scores are there
       for (int j = u.t0; j < u.t1; ++j, ++it) {
         const int st = (int)(it % G::kStages);
-        if (!failed) failed = !wait(bars + 8 * (kLScFull + st), (it / G::kStages) & 1u);
-        if (!failed) failed = !wait(bars + 8 * kLSFull, it & 1u);
+        if (!ready && !failed) failed = !wait(bars + 8 * (kLSFull + st), (it / G::kStages) & 1u);
         tc_fence_after();
         uint32_t v[16], lo[16];
         tmem_ld_16x256b_x4(tw + G::kSCol + 32 * half, v);
@@ -561,6 +560,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
           top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
+        // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
+        const bool x_free = it < 2 || wait.look(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
         bool up = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -617,7 +618,10 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
         // x in two parts to shared memory, [16 tokens][8 rows] core matrices, once the sums
         // of the tile before last have read theirs
-        if (it > 1 && !failed) failed = !wait(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
+        if (!__all_sync(0xFFFFFFFFu, x_free) && !failed)
+          failed = !wait(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
+        const uint32_t nx = it + 1;
+        ready = j + 1 < u.t1 && wait.look(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
         const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(half * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -648,8 +652,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             sts_u16(a, hi);
             sts_u16(a + kPBytes, rest);
           }
-          if (near) l2[i] = fma2(sum, pack2(0.03125f, 0.03125f), l2[i]);  // 2^-kTop
+          if (near) l2[i] = fma2(sum, pack2(kTopInv, kTopInv), l2[i]);
         }
+        ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
         __syncwarp();
         if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + (it & 1)));
@@ -798,7 +803,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               const int a = s < kSteps ? s : s - R / 32;  // the key part's lo codes meet the same q
               mma_f8_ta(tmem + G::kSCol, tmem + G::kQCol + 8 * a, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
             }
-            tc_commit(bars + 8 * kLSFull);
+            tc_commit(bars + 8 * (kLSFull + st));
           }
           __syncwarp();
         }
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         near = __all_sync(0xFFFFFFFFu, near);
         if (lane == 0) near_s[st] = near;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * (kLScFull + st));
+        if (lane == 0) mbar_arrive(bars + 8 * (kLSFull + st));
       }
     }
   }
