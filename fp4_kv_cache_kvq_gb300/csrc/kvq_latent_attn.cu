@@ -15,10 +15,12 @@
 //       values hi = RNE(q), lo = RNE(q - hi): exact down to 2^-9 of the row's
 //       largest element, off by at most 2^-17 of it below.  hi and lo are rows of
 //       one operand (128 rows for 64 queries); their scores are added in fp32.
-//   x   reaches 2^4 .. 2^8 in every row and is rounded to f16, then hi = E4M3(x),
-//       lo = E5M2(x - hi): 2^-8 of x, or 2^-14 under 2^-6, where hi's steps end
-//       and lo's range (down to 2^-17) takes over.  Two products of 8-bit operands
-//       cost what one of 16-bit ones costs and need no expansion of the values.
+//   x   reaches 2^5 .. 2^11 in every row and is rounded to f16, then held as a sum of
+//       an E4M3 and an E5M2 value: first the rounding to E4M3 (to E5M2 over 448, E4M3's
+//       end), then of the rest to the other: off by 2^-8 of x either way, or 2^-14
+//       under 2^-6, where E4M3's steps end and E5M2's range (down to 2^-17) takes
+//       over.  Two products of 8-bit operands cost what one of 16-bit ones costs
+//       and need no expansion of the values.
 // Sums, maxima and accumulators are fp32.
 //
 // Work.  A row is a query head of a token; a unit is 64 rows of one sequence and
@@ -49,10 +51,12 @@ constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax +
 constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 1;  // and the scales' warp
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 4;           // least tiles of a split range
-// x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): E4M3 holds 2^8.8, and
-// the references are raised only past the slack, since that rescales O.  (5 and 3: some
-// of 64 rows raised its own in every second tile, 1250 cycles each.)
-constexpr float kTop = 4.0f, kSlackL = 4.0f, kTopInv = 1.0f / 16.0f;
+// x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): over 2^11.8 the rest
+// behind E5M2 would leave E4M3.  The references are raised only past the slack, since
+// that rescales O (a slack of 3: among 64 rows some raised its own in every second
+// tile, 1100 cycles each).
+constexpr float kTop = 5.0f, kSlackL = 6.0f, kTopInv = 1.0f / 32.0f;
+constexpr float kE4m3End = 8.80f;  // a little under log2 448
 
 enum : int {
   kLFull = 0,               // [stages] codes and exponents landed
@@ -186,6 +190,11 @@ __device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t v) {
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(v));
   return r;
 }
+__device__ __forceinline__ uint32_t f16x2_of_e5m2x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
@@ -198,6 +207,11 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
 }
 __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ __half2 u32_half2(uint32_t v) {
+  __half2 h;
+  *reinterpret_cast<uint32_t*>(&h) = v;
+  return h;
 }
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
@@ -626,6 +640,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
+          const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448
           const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16);
           if (!near) {
             const float to = my[i], zero = to == -INFINITY ? 0.0f : to;
@@ -646,8 +661,14 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
             if (near) sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
             const uint32_t h = pack_f16x2(xa, xb);
-            const uint32_t hi = e4m3x2_of_f16x2(h);
-            const uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
+            uint32_t hi = e4m3x2_of_f16x2(h);
+            uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
+            if (large) {
+              const uint32_t r = e5m2x2_of_f16x2(h), q = e4m3x2_of_f16x2(hsub2(h, f16x2_of_e5m2x2(r)));
+              const uint32_t over = prmt(__hgt2_mask(u32_half2(h), u32_half2(0x5F005F00u)), 0u, 0x4420u);  // 448
+              hi = (hi & ~over) | (q & over);
+              rest = (rest & ~over) | (r & over);
+            }
             const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
             sts_u16(a, hi);
             sts_u16(a + kPBytes, rest);
