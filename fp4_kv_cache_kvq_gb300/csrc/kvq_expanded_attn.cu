@@ -1,75 +1,460 @@
 // kvq_expanded_attn.cu -- causal attention of a chunk over dense keys and values
-// whose key's position part is shared by all heads, and its C entry point.
-//   y = softmax_scale log2 e (q[:d] . k + q[d:] . k_rope),
-//   out = sum 2^(y - m) v / sum 2^(y - m)
-#include "kvq_attn_rows.cuh"
-#include "kvq_host.cuh"
+// whose key's position part is shared by all heads, on the 5th-generation tensor
+// cores (tcgen05, accumulators in TMEM), and its C entry point.
+//
+// Mathematics.  Query token i of n sits at position T - n + i and attends 0 .. T - n + i,
+//   y = softmax_scale log2 e (q[:d] . k + q[d:] . k_rope),  P = 2^(y - m),
+//   out = sum P v / sum P.
+// q, k and v enter the products as they are (bf16); P is rounded to bf16, which has
+// fp32's range, so the reference m of a row is raised only when a score passes it by
+// 2^kSlackE; sums, maxima and accumulators are fp32.
+//
+// What bounds it: the tensor pipe, 2 (2 d + 64) flop per attended pair and head; a
+// unit's tiles come from L2, 61 KB per 96 positions at d = 128.
+// Work: a CTA takes 256 query tokens of a head as two 128-row tiles that share each
+// tile of 96 positions (two of them in flight, with both query tiles, is what shared
+// memory holds at d = 128); the longest first, 16 heads at a time so that their keys
+// and values stay in L2.
+// Eleven warps: softmax (2 x 4, thread = row), loader (TMA, 128-byte swizzle), MMA
+// issue (one per query tile, so that one's softmax runs beside the other's products),
+// joined by mbarriers (every wait bounded):
+//   S_X(j) = q_X K(j)^T    both from shared memory; the key's position part is one
+//                          more 64-channel slab behind the head's own
+//   O_X += P_X(j) V(j)     P from TMEM over S's columns, V as MN-major operand
 #include "../../include/kvq_latent.h"
+#include "kvq_common.cuh"
+#include "kvq_host.cuh"
+#include "kvq_roles.cuh"
+#include "kvq_tc.cuh"
 
 #include <cuda_bf16.h>
 
 namespace kvq {
 namespace {
 
+constexpr int kET = 96;       // positions per tile
+constexpr int kERows = 128;   // rows of a query tile
+constexpr int kERope = 64;
+constexpr int kESoftmax = 8, kELoad = kESoftmax, kEMma = kELoad + 1, kEThreads = 32 * (kEMma + 2);
+constexpr int kQSlab = kERows * 128, kTSlab = kET * 128;  // 64 channels of a query tile, of a tile
+constexpr int kHeadsAtOnce = 16;
+constexpr float kSlackE = 20.0f;
+
+enum : int {
+  kEQ = 0,              // queries landed
+  kEKFull = 1,          // [ring]
+  kEKEmpty = kEKFull + 4,
+  kEVFull = kEKEmpty + 4,
+  kEVEmpty = kEVFull + 4,
+  kESFull = kEVEmpty + 4,   // [2] S_X in TMEM
+  kEPFull = kESFull + 2,    // [2] P_X in TMEM, O_X rescaled
+  kEPvDone = kEPFull + 2,   // [2] O_X += done
+  kEDrain = kEPvDone + 2,   // [2] an MMA warp's last commit
+  kEBars = kEDrain + 2
+};
+
 struct ExpandedParams {
   const int32_t* lens;
   const int32_t* chunk_lens;
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* kr;
-  const uint16_t* v;
   void* out;
   int32_t* flag;
-  int64_t k_ts, k_hs, kr_ts, v_ts, v_hs;
-  int32_t batch, heads, d, rope, chunk, max_len, out_bf16, tiles;
+  int32_t batch, heads, chunk, max_len, out_bf16, nqb;
   float scale_log2;
+  uint64_t wait_ns;  // a test's limit of the waits, or 0
 };
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-
-struct ExpandedSrc {
-  const ExpandedParams& p;
-  int b, h, r0;
-  int64_t first;
-  __device__ int64_t row(int r) const { return ((int64_t)b * p.chunk + r0 + r) * p.heads + h; }
-  __device__ float query(int r, int c) const { return bf16_at(p.q + row(r) * (p.d + p.rope) + c); }
-  __device__ int64_t last(int r) const { return first + r0 + r; }
-  __device__ bool attends(int64_t pos) const { return pos < p.max_len; }
-  __device__ void load(int64_t pos, float* k, float* v, int lane) const {
-    const int64_t tok = (int64_t)b * p.max_len + pos;
-    for (int c = lane; c < p.d; c += 32) {
-      k[c] = pos < 0 ? 0.0f : bf16_at(p.k + tok * p.k_ts + h * p.k_hs + c);
-      v[c] = pos < 0 ? 0.0f : bf16_at(p.v + tok * p.v_ts + h * p.v_hs + c);
-    }
-    for (int c = lane; c < p.rope; c += 32) k[p.d + c] = pos < 0 ? 0.0f : bf16_at(p.kr + tok * p.kr_ts + c);
-  }
-  __device__ void store(int r, int c, float x) const {
-    const int64_t at = row(r) * p.d + c;
-    if (p.out_bf16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-    else
-      static_cast<float*>(p.out)[at] = x;
-  }
+template <int D>
+struct EGeo {
+  static constexpr int kKSlabs = (D + kERope) / 64, kVSlabs = D / 64;
+  static constexpr int kRing = D == 128 ? 2 : 4;
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kKSlabs * kQSlab;
+  static constexpr int kV = kK + kRing * kKSlabs * kTSlab;
+  static constexpr int kBar = kV + kRing * kVSlabs * kTSlab;
+  static constexpr int kMisc = kBar + 8 * kEBars;
+  static constexpr int kBytes = kMisc + 16 + 1024;  // 1024: the swizzle's alignment
+  static constexpr int kOCol = 2 * kET;
+  static_assert(kBytes <= 227 * 1024 && kBytes > 116 * 1024 && kOCol + 2 * D <= 512, "layout");
 };
 
-__global__ void __launch_bounds__(kThreadsR) expanded_attn_kernel(const ExpandedParams p) {
-  extern __shared__ float sm[];
-  const int r0 = blockIdx.x % p.tiles * kRowsR, bh = blockIdx.x / p.tiles;
+// Descriptors of operands with the 128-byte swizzle (8 rows of 128 bytes an atom).
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return smem_desc(saddr, lbo, sbo) | (uint64_t)2 << 61;
+}
+// kind::f16, bf16 operands, fp32 accumulator, M = 128.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// 16 columns of this warp's TMEM lanes and their maximum, without the wait.
+__device__ __forceinline__ void tmem_ld_max16(uint32_t taddr, uint32_t* v, uint32_t& m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, "
+      "[%17];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(m)
+      : "r"(taddr)
+      : "memory");
+}
+// keeps the uses of v and m behind the wait
+__device__ __forceinline__ void behind(uint32_t* v, uint32_t& m) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(m)
+               :
+               : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kEThreads, 1)
+    expanded_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mv,
+                         const ExpandedParams p) {
+  using G = EGeo<D>;
+  extern __shared__ uint8_t exp_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(exp_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_addr(base), bars = sb + G::kBar;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
+  const BoundedWaits wait{abort, p.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // 16 heads at a time, within them the last tokens (the longest) first
+  const int bhs = p.batch * p.heads, part = blockIdx.x / (kHeadsAtOnce * p.nqb);
+  const int in_part = min(kHeadsAtOnce, bhs - part * kHeadsAtOnce), at = blockIdx.x - part * kHeadsAtOnce * p.nqb;
+  const int bh = part * kHeadsAtOnce + at % in_part, qb = p.nqb - 1 - at / in_part;
   const int h = bh % p.heads, b = bh / p.heads;
   const int32_t T = __ldg(p.lens + b), n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
   if (n < 0 || n > p.chunk || T > p.max_len || T < n) {
-    if (threadIdx.x == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
+    if (tid == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
     if (n < 0 || n > p.chunk || T > p.max_len) return;
   }
-  const int rows = min(kRowsR, n - r0);
-  if (rows <= 0) return;
-  ExpandedSrc src{p, b, h, r0, (int64_t)T - n};
-  attend_rows(src, RowsShape{p.d + p.rope, p.d}, rows, T < n ? 0 : src.last(rows - 1) + 1, p.scale_log2, sm);
+  const int i0 = qb * 2 * kERows;
+  if (i0 >= n) return;  // padding only
+  const int rows = min(2 * kERows, n - i0);
+  const int64_t row0 = ((int64_t)b * p.chunk + i0) * p.heads + h;
+  if (T < n) {  // the chunk's own tokens must be among the keys
+    for (int i = tid; i < rows * (D / 4); i += kEThreads) {
+      const int64_t o = (row0 + (int64_t)(i / (D / 4)) * p.heads) * D + i % (D / 4) * 4;
+      if (p.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = make_uint2(0u, 0u);
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  const int first = T - n + i0;                  // position of the unit's token 0
+  const int nx = rows > kERows ? 2 : 1;          // query tiles with rows
+  // tiles that query tile X attends
+  const auto tiles_of = [&](int x) { return (first + min(rows, kERows * (x + 1)) + kET - 1) / kET; };
+  const int nt = tiles_of(nx - 1);
+
+  if (tid == 0) {
+    mbar_init(bars + 8 * kEQ, 1);
+    for (int i = 0; i < G::kRing; ++i) {
+      mbar_init(bars + 8 * (kEKFull + i), 1);
+      mbar_init(bars + 8 * (kEKEmpty + i), nx);
+      mbar_init(bars + 8 * (kEVFull + i), 1);
+      mbar_init(bars + 8 * (kEVEmpty + i), nx);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (kESFull + i), 1);
+      mbar_init(bars + 8 * (kEPFull + i), 4);
+      mbar_init(bars + 8 * (kEPvDone + i), 1);
+      mbar_init(bars + 8 * (kEDrain + i), 1);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(smem_addr(misc), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+
+  if (warp < kESoftmax) {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, r = tid & 127, i = kERows * x + r;
+    const uint32_t tw = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_col = tw + x * kET, o_col = tw + G::kOCol + x * D;
+    const int ntx = x < nx ? tiles_of(x) : 0;
+    const int last = first + i, all = first + kERows * x;  // last position of the row, of every row
+    float ref = -INFINITY;
+    uint64_t l2 = 0ull;
+    bool ok = true;
+    for (int j = 0; j < ntx && ok; ++j) {
+      if (!(ok = wait(bars + 8 * (kESFull + x), j & 1u))) break;
+      tc_fence_after();
+      uint32_t v[kET], mx[kET / 16];
+#pragma unroll
+      for (int k = 0; k < kET / 16; ++k) tmem_ld_max16(s_col + 16 * k, v + 16 * k, mx[k]);
+      asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < kET / 16; ++k) behind(v + 16 * k, mx[k]);
+      float top = -INFINITY;
+      if ((j + 1) * kET > all + 1) {  // some row sees the tile in part
+        const int lim = last - j * kET;
+#pragma unroll
+        for (int c = 0; c < kET; ++c) {
+          if (c > lim) v[c] = 0xFF800000u;
+          top = fmaxf(top, __uint_as_float(v[c]));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kET / 16; ++k) top = fmaxf(top, __uint_as_float(mx[k]));
+      }
+      top *= p.scale_log2;
+      const bool up = top > ref + kSlackE;
+      if (__any_sync(0xFFFFFFFFu, up)) {
+        const float to = up ? top : ref, a = up ? fast_exp2(ref - to) : 1.0f;
+        l2 = mul2(l2, pack2(a, a));
+        ref = to;
+        if (j > 0) {  // (S(j) was issued behind the sums of j - 1)
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tmem_st32_async(o_col + c, o);
+          }
+        }
+      }
+      const float zero = ref == -INFINITY ? 0.0f : -ref;
+      const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), r2 = pack2(zero, zero);
+#pragma unroll
+      for (int k = 0; k < kET / 32; ++k) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = 32 * k + 2 * e;
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, r2));
+          const float a = fast_exp2(y.x), bb = fast_exp2(y.y);
+          l2 = add2(l2, pack2(a, bb));
+          w[e] = bf16x2(a, bb);
+        }
+        tmem_st16_async(s_col + 16 * k, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kEPFull + x));
+    }
+    if (ok && ntx > 0 && (ok = wait(bars + 8 * (kEPvDone + x), (ntx - 1) & 1u))) {
+      tc_fence_after();
+      const float2 ll = unpack2(l2);
+      const float l = ll.x + ll.y, f = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t o = (row0 + (int64_t)i * p.heads) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t w[32];
+        tmem_ld32(o_col + c, w);
+        if (i < rows) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(w[k]) * f);
+          if (p.out_bf16) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o + c + k) =
+                  make_uint4(bf16x2(__uint_as_float(w[k]), __uint_as_float(w[k + 1])),
+                             bf16x2(__uint_as_float(w[k + 2]), __uint_as_float(w[k + 3])),
+                             bf16x2(__uint_as_float(w[k + 4]), __uint_as_float(w[k + 5])),
+                             bf16x2(__uint_as_float(w[k + 6]), __uint_as_float(w[k + 7])));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o + c + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+          }
+        }
+      }
+    }
+  } else if (warp == kELoad) {
+    // ------------------------------------------------------------ loader
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bars + 8 * kEQ, nx * G::kKSlabs * kQSlab);
+      for (int x = 0; x < nx; ++x)
+        for (int s = 0; s < G::kKSlabs; ++s)
+          tma_4d(sb + G::kQ + (x * G::kKSlabs + s) * kQSlab, &mq, 64 * s, h, i0 + kERows * x, b, bars + 8 * kEQ);
+    }
+    __syncwarp();
+    int kj = 0, vj = 0;  // tiles so far
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % G::kRing;
+      if (j >= G::kRing && !wait(bars + 8 * (kEKEmpty + s), (uint32_t)(j / G::kRing - 1) & 1u)) break;
+      if (lane == 0) {
+        const uint32_t bar = bars + 8 * (kEKFull + s), dst = sb + G::kK + s * G::kKSlabs * kTSlab;
+        mbar_arrive_expect_tx(bar, G::kKSlabs * kTSlab);
+        for (int c = 0; c < D / 64; ++c) tma_4d(dst + c * kTSlab, &mk, 64 * c, h, j * kET, b, bar);
+        tma_load_3d(dst + D / 64 * kTSlab, &mr, 0, j * kET, b, bar);
+      }
+      __syncwarp();
+      kj = j + 1;
+      if (j >= G::kRing && !wait(bars + 8 * (kEVEmpty + s), (uint32_t)(j / G::kRing - 1) & 1u)) break;
+      if (lane == 0) {
+        const uint32_t bar = bars + 8 * (kEVFull + s), dst = sb + G::kV + s * G::kVSlabs * kTSlab;
+        mbar_arrive_expect_tx(bar, G::kVSlabs * kTSlab);
+        for (int c = 0; c < G::kVSlabs; ++c) tma_4d(dst + c * kTSlab, &mv, 64 * c, h, j * kET, b, bar);
+      }
+      __syncwarp();
+      vj = j + 1;
+    }
+    // no copy outlives the CTA
+    const auto landed = [&](uint32_t bar, uint32_t parity) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait_hint(bar, parity, 20000u) && global_ns() - t0 < 20000000ull) {
+      }
+    };
+    landed(bars + 8 * kEQ, 0u);
+    for (int j = max(0, kj - G::kRing); j < kj; ++j) landed(bars + 8 * (kEKFull + j % G::kRing), (uint32_t)(j / G::kRing) & 1u);
+    for (int j = max(0, vj - G::kRing); j < vj; ++j) landed(bars + 8 * (kEVFull + j % G::kRing), (uint32_t)(j / G::kRing) & 1u);
+  } else if (warp - kEMma < nx) {
+    // ------------------------------------------------------------ MMA issue
+    const int x = warp - kEMma, ntx = tiles_of(x);
+    const uint64_t dq = swizzled_desc(sb + G::kQ + x * G::kKSlabs * kQSlab, 16, 1024);
+    const uint64_t dk = swizzled_desc(sb + G::kK, 16, 1024);        // positions as rows: K-major
+    const uint64_t dv = swizzled_desc(sb + G::kV, kTSlab, 1024);    // channels as rows: MN-major
+    const uint32_t s_col = tmem + x * kET, o_col = tmem + G::kOCol + x * D;
+    const auto scores = [&](int j) {
+      const int s = j % G::kRing;
+      if (elect_one_of_warp()) {
+        const uint64_t k0 = dk + (uint64_t)(s * (G::kKSlabs * kTSlab >> 4));
+#pragma unroll
+        for (int c = 0; c < (D + kERope) / 16; ++c)
+          tc_mma_f16(s_col, dq + (uint64_t)(((c >> 2) * kQSlab + (c & 3) * 32) >> 4),
+                     k0 + (uint64_t)(((c >> 2) * kTSlab + (c & 3) * 32) >> 4), idesc_bf16(kET, false), c > 0);
+        tc_commit(bars + 8 * (kESFull + x));
+        tc_commit(bars + 8 * (kEKEmpty + s));
+      }
+      __syncwarp();
+    };
+    bool ok = wait(bars + 8 * kEQ, 0u) && wait(bars + 8 * kEKFull, 0u);
+    tc_fence_after();
+    if (ok) scores(0);
+    for (int j = 0; j < nt && ok; ++j) {
+      const int s = j % G::kRing, sn = (j + 1) % G::kRing;
+      const uint32_t ph = (uint32_t)(j / G::kRing) & 1u, phn = (uint32_t)((j + 1) / G::kRing) & 1u;
+      if (!(ok = wait(bars + 8 * (kEVFull + s), ph))) break;
+      if (j < ntx) {
+        // values behind the sequence's end: no NaN there may meet a weight of 0
+        const int rest = T - j * kET;
+        if (rest < kET) {
+          const uint32_t v0 = sb + G::kV + s * G::kVSlabs * kTSlab;
+          for (int k = lane; k < G::kVSlabs * (kET - rest) * 8; k += 32) {
+            const int slab = k / ((kET - rest) * 8), u = k % ((kET - rest) * 8);
+            sts128(v0 + slab * kTSlab + rest * 128 + 16 * u, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = wait(bars + 8 * (kEPFull + x), j & 1u))) break;
+        tc_fence_after();
+        if (elect_one_of_warp()) {
+          const uint64_t v0 = dv + (uint64_t)(s * (G::kVSlabs * kTSlab >> 4));
+#pragma unroll
+          for (int c = 0; c < kET / 16; ++c)
+            tc_mma_f16_ta(o_col, s_col + 8 * c, v0 + (uint64_t)(c * 2048 >> 4), idesc_bf16(D, true), j > 0 || c > 0);
+          tc_commit(bars + 8 * (kEPvDone + x));
+          tc_commit(bars + 8 * (kEVEmpty + s));
+        }
+        __syncwarp();
+      } else if (lane == 0) {  // a tile that only the other query tile attends
+        mbar_arrive(bars + 8 * (kEVEmpty + s));
+      }
+      if (j + 1 < nt) {
+        if (!(ok = wait(bars + 8 * (kEKFull + sn), phn))) break;
+        if (j + 1 < ntx) {  // P lives in S's columns: the next scores follow the product that reads it
+          if (!(ok = wait(bars + 8 * (kEPvDone + x), j & 1u))) break;
+          tc_fence_after();
+          scores(j + 1);
+        } else if (lane == 0) {
+          mbar_arrive(bars + 8 * (kEKEmpty + sn));
+        }
+      }
+    }
+    // no product outlives the CTA
+    if (lane == 0) tc_commit(bars + 8 * (kEDrain + x));
+    __syncwarp();
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait_hint(bars + 8 * (kEDrain + x), 0u, 20000u) && global_ns() - t0 < 20000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) set_flag(p.flag, KVQ_FLAG_TIMEOUT);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 bool rows_ok(int64_t token, int64_t head, int64_t heads, int64_t width) {
   if (token % 8 != 0 || head % 8 != 0 || head < 0 || token < 0) return false;
   return (heads <= 1 || head >= width) && token >= (heads - 1) * head + width;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// bf16 rows of `width` values, [batch][tokens][heads] (heads 0: no such dimension),
+// copied by boxes of 64 values x `box` tokens of one head.
+bool encode(CUtensorMap* map, const void* ptr, int64_t width, int64_t heads, int64_t tokens, int64_t batch, int64_t head_stride,
+            int64_t token_stride, int box) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int rank = heads ? 4 : 3;
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t boxes[4], steps[4] = {1, 1, 1, 1};
+  int d = 0;
+  dims[d] = (cuuint64_t)width, boxes[d++] = 64;
+  if (heads) strides[d - 1] = (cuuint64_t)head_stride * 2, dims[d] = (cuuint64_t)heads, boxes[d++] = 1;
+  strides[d - 1] = (cuuint64_t)token_stride * 2, dims[d] = (cuuint64_t)tokens, boxes[d++] = (cuuint32_t)box;
+  strides[d - 1] = (cuuint64_t)token_stride * 2 * (cuuint64_t)tokens, dims[d] = (cuuint64_t)batch, boxes[d++] = 1;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, boxes, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+kvq_status launch_expanded(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mr, const CUtensorMap& mv,
+                           const ExpandedParams& p, cudaStream_t s) {
+  static DeviceOnce attr_set;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (attr_set.pending(dev)) {
+    if (cudaFuncSetAttribute(expanded_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, EGeo<D>::kBytes) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    attr_set.mark(dev);
+  }
+  expanded_attn_kernel<D><<<(unsigned)((int64_t)p.batch * p.heads * p.nqb), kEThreads, EGeo<D>::kBytes, s>>>(mq, mk, mr, mv, p);
+  return launch_status();
 }
 
 }  // namespace
@@ -85,7 +470,7 @@ extern "C" kvq_status kvq_expanded_attn(int32_t batch, int32_t num_heads, int32_
                                         int64_t v_head_stride, float softmax_scale, void* out, int32_t out_dtype,
                                         int32_t* d_err_flag, kvq_stream stream) {
   if (batch < 0 || num_heads < 1 || chunk < 0 || max_len < 0 || (head_dim != 64 && head_dim != 128) ||
-      rope_dim != 64 || !(softmax_scale > 0.0f) || !(softmax_scale < INFINITY) ||
+      rope_dim != kERope || !(softmax_scale > 0.0f) || !(softmax_scale < INFINITY) ||
       (out_dtype != KVQ_DTYPE_F32 && out_dtype != KVQ_DTYPE_BF16))
     return KVQ_ERR_INVALID_ARGUMENT;
   if (batch == 0 || chunk == 0) return KVQ_OK;
@@ -96,20 +481,26 @@ extern "C" kvq_status kvq_expanded_attn(int32_t batch, int32_t num_heads, int32_
   if (!rows_ok(k_token_stride, k_head_stride, num_heads, head_dim) || !rows_ok(k_rope_stride, 0, 1, rope_dim) ||
       !rows_ok(v_token_stride, v_head_stride, num_heads, head_dim))
     return KVQ_ERR_INVALID_ARGUMENT;
-  if ((double)batch * chunk * num_heads > (double)(1 << 30)) return KVQ_ERR_UNSUPPORTED;
   ExpandedParams p = {};
+  p.nqb = (int32_t)(((int64_t)chunk + 2 * kERows - 1) / (2 * kERows));
+  if ((double)batch * chunk * num_heads > (double)(1 << 30) || (double)batch * num_heads * p.nqb > (double)(1 << 30) ||
+      max_len > (1 << 30))
+    return KVQ_ERR_UNSUPPORTED;
   p.lens = d_seq_lens, p.chunk_lens = d_chunk_lens;
-  p.q = static_cast<const uint16_t*>(q), p.k = static_cast<const uint16_t*>(k);
-  p.kr = static_cast<const uint16_t*>(k_rope), p.v = static_cast<const uint16_t*>(v);
   p.out = out, p.flag = d_err_flag;
-  p.k_ts = k_token_stride, p.k_hs = k_head_stride, p.kr_ts = k_rope_stride, p.v_ts = v_token_stride, p.v_hs = v_head_stride;
-  p.batch = batch, p.heads = num_heads, p.d = head_dim, p.rope = rope_dim, p.chunk = chunk, p.max_len = max_len;
-  p.out_bf16 = out_dtype == KVQ_DTYPE_BF16, p.tiles = (chunk + kRowsR - 1) / kRowsR;
+  p.batch = batch, p.heads = num_heads, p.chunk = chunk, p.max_len = max_len;
+  p.out_bf16 = out_dtype == KVQ_DTYPE_BF16;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  const size_t bytes = RowsShape{head_dim + rope_dim, head_dim}.bytes();
-  if (cudaFuncSetAttribute(expanded_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+  p.wait_ns = test_wait_limit_ns();
+  const int64_t w = head_dim + rope_dim;
+  const int64_t tokens = max_len > 0 ? max_len : 1;  // (without keys nothing is copied: any map will do)
+  const int64_t kh = num_heads > 1 ? k_head_stride : head_dim, vh = num_heads > 1 ? v_head_stride : head_dim;
+  CUtensorMap mq, mk, mr, mv;
+  if (!encode(&mq, q, w, num_heads, chunk, batch, w, w * num_heads, kERows) ||
+      !encode(&mk, max_len > 0 ? k : q, head_dim, num_heads, tokens, batch, kh, k_token_stride, kET) ||
+      !encode(&mr, max_len > 0 ? k_rope : q, rope_dim, 0, tokens, batch, 0, k_rope_stride, kET) ||
+      !encode(&mv, max_len > 0 ? v : q, head_dim, num_heads, tokens, batch, vh, v_token_stride, kET))
     return KVQ_ERR_CUDA;
-  expanded_attn_kernel<<<(unsigned)((int64_t)batch * num_heads * p.tiles), kThreadsR, bytes,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return launch_status();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? launch_expanded<128>(mq, mk, mr, mv, p, s) : launch_expanded<64>(mq, mk, mr, mv, p, s);
 }

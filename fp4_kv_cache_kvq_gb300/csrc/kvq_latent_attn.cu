@@ -38,6 +38,7 @@
 //             one's waits do not hold up the other's products
 //   scales    2^e, e and 2^-e of a tile's tokens, once for all rows
 #include "kvq_latent.cuh"
+#include "kvq_roles.cuh"
 #include "kvq_tc.cuh"
 
 #include <cuda_bf16.h>
@@ -149,32 +150,6 @@ __device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[16], uint32_t (&b)[1
                :
                : "memory");
 }
-// Two fp32 values side by side.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ void tmem_st_16x256b_x1(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
@@ -216,13 +191,6 @@ __device__ __forceinline__ __half2 u32_half2(uint32_t v) {
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
-// One lane of a converged warp.  (A lane picked by its number makes the compiler treat
-// the descriptors as different from lane to lane: 70 cycles an MMA.)
-__device__ __forceinline__ bool elect_one_of_warp() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
-}
 // Named barrier 1 of the softmax warps; true when any thread's v is.
 __device__ __forceinline__ bool softmax_or(bool v) {
   uint32_t r;
@@ -233,32 +201,6 @@ __device__ __forceinline__ bool softmax_or(bool v) {
       : "memory");
   return r != 0;
 }
-
-// A wait of the whole warp with one outcome; it gives up after the library's limit
-// (or a test's, which polls: a suspending wait could outlast it), or with any other
-// wait of the CTA.
-struct LWaits {
-  volatile int* abort;
-  uint64_t limit;  // a test's, ns, or 0
-  __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) const {
-    return limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-  }
-  __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) const {
-    if (look(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (true) {
-      if (look(bar, parity)) return true;
-      if (*abort) return false;
-      if (global_ns() - t0 > (limit ? limit : kWaitLimitNs)) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity));
-  }
-};
 
 __device__ __forceinline__ int64_t capacity(const kvq_latent_cache& c) { return (int64_t)c.max_pages_per_seq * c.page_size; }
 
@@ -354,7 +296,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [warps]
   volatile int* near_s = reinterpret_cast<volatile int*>(base + G::kNear);
   volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
-  const LWaits wait{abort, p.wait_ns};
+  const BoundedWaits wait{abort, p.wait_ns};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
