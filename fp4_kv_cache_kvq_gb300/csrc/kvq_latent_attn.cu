@@ -30,7 +30,7 @@
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
 // the longest first.
-// Twelve warps: softmax (8; thread = two rows x 8 positions of a tile), loader, two
+// Twenty warps: softmax (16; thread = two rows x 4 positions of a tile), loader, two
 // that issue the products, scales, joined by mbarriers (every wait bounded):
 //   loader    bulk copies of 64-token tiles into a ring
 //   products  S(j) = q K(j)^T         kind::f8f6f4, q from TMEM
@@ -48,10 +48,12 @@ namespace {
 
 constexpr int kLT = 64;     // positions per tile
 constexpr int kLRows = 64;  // query rows per unit
-constexpr int kLSmWarps = 8, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 128;
+constexpr int kParts = 4, kPCols = kLT / kParts;  // softmax warps that share a row, a tile's positions of each
+constexpr int kLSmWarps = 4 * kParts, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 128;
 constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 1;  // and the scales' warp
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
-constexpr int kMinTiles = 4;           // least tiles of a split range
+constexpr int kMinTiles = 2;           // least tiles of a split range
+constexpr int kPairs = kPCols / 8;     // pairs of positions of a thread's
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): over 2^11.8 the rest
 // behind E5M2 would leave E4M3.  The references are raised only past the slack, since
 // that rescales O (a slack of 3: among 64 rows some raised its own in every second
@@ -97,12 +99,12 @@ struct LGeo {
   static constexpr int kExp = kP + 4 * kPBytes;           // [stages][64]
   static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
   static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns, [64] second ones
-  static constexpr int kTwo = kAlpha + 2 * 4 * kLRows;    // [3][2][64] what the two halves of a row exchange
-  static constexpr int kSc = kTwo + 3 * 2 * 4 * kLRows;   // [stages][3][64] 2^e, e (-inf: no token), 2^-e
+  static constexpr int kShare = kAlpha + 2 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
+  static constexpr int kSc = kShare + 2 * kParts * 4 * kLRows;  // [stages][3][64] 2^e, e (-inf: no token), 2^-e
   static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40
   static constexpr int kBar = kNear + 4 * 8;
   static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, plan
-  static constexpr int kUsed = kMisc + 192 + 128;
+  static constexpr int kUsed = kMisc + 320 + 128;
   static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;  // one CTA per SM: it holds all of TMEM
   static constexpr int kOCol = 0, kQCol = L / 2, kSCol = kQCol + (L + R) / 4;
   static_assert(kSCol + kLT <= 512 && kUsed <= 227 * 1024 && kBar % 8 == 0 && kStages <= 8, "layout");
@@ -127,26 +129,19 @@ constexpr uint32_t kIdS = (1u << 4) | (kLT / 8 << 17) | (128u / 16 << 24);
 constexpr uint32_t kIdOHi = (1u << 4) | (1u << 15) | (kLRows / 8 << 17) | (128u / 16 << 24);  // A MN-major
 constexpr uint32_t kIdOLo = kIdOHi | (1u << 10);
 
-// 16 lanes x 32 columns of TMEM, without the wait: register 4j + 2i + e holds row
+// 16 lanes x 16 columns of TMEM, without the wait: register 4j + 2i + e holds row
 // lane/4 + 8i, column 8j + 2(lane%4) + e.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
 }
 // Wait for the thread's TMEM loads; a and b pass through, so their uses stay behind it.
-__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[16], uint32_t (&b)[16]) {
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[8], uint32_t (&b)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
                  "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
                :
                : "memory");
 }
@@ -195,7 +190,7 @@ __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ bool softmax_or(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(v ? 1u : 0u)
       : "memory");
@@ -273,8 +268,11 @@ struct Walk {
         u.t1 = (int)min(s1, (int64_t)nt);
         u.whole = s0 == 0 && s1 == cost;
         u.slot = s0 > 0 ? 0 : 1;
-        if (flag == p.flag && s0 == 0 && threadIdx.x == 0)
-          p.rec[(int64_t)b * p.tpb + u.r] = make_int2((int)blockIdx.x, (int)((base + cost - 1) / per - base / per + 1));
+        if (flag == p.flag && s0 == 0 && threadIdx.x == 0) {
+          const int64_t span = base - lo + cost - 1;  // ranges that it reaches beyond this one: span / per
+          const int more = span < per ? 0 : span >> 32 ? (int)(span / per) : (int)((uint32_t)span / (uint32_t)per);
+          p.rec[(int64_t)b * p.tpb + u.r] = make_int2((int)blockIdx.x, more + 1);
+        }
         base += cost;
         ++b;
       }
@@ -294,6 +292,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
   Plan* plan = reinterpret_cast<Plan*>(misc + 2);
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [warps]
+  static_assert(8 + sizeof(Plan) + 8 * (kLThreads / 32) <= 256, "behind it, the softmax warps' words");
   volatile int* near_s = reinterpret_cast<volatile int*>(base + G::kNear);
   volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
   const BoundedWaits wait{abort, p.wait_ns};
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     }
     mbar_init(bars + 8 * kLDrain, 2);
     *abort = 0;
-    misc[32] = misc[33] = 0u;
+    misc[64] = misc[65] = 0u;
     plan->lo = plan->hi = plan->base = 0;
     plan->b = 0;
     fence_barrier_init();
@@ -363,17 +362,17 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   if (warp < kLSmWarps) {
     // ------------------------------------------------------------ softmax
     // warp w: rows 16 (w & 3) .. + 15, whose scores lie in its 32 TMEM lanes, and the
-    // positions 32 (w >> 2) .. + 31 of a tile
-    const int g = lane >> 2, t = lane & 3, quad = warp & 3, half = warp >> 2;
+    // positions 16 (w >> 2) .. + 15 of a tile
+    const int g = lane >> 2, t = lane & 3, quad = warp & 3, part = warp >> 2;
     const uint32_t tw = tmem + ((uint32_t)(32 * quad) << 16);
     const int lr[2] = {16 * quad + g, 16 * quad + g + 8};
     float* alpha = reinterpret_cast<float*>(base + G::kAlpha);
-    float* two = reinterpret_cast<float*>(base + G::kTwo) + half * kLRows;  // [3][2][64], this half's
-    const auto both = [&](int k, int r) {  // what the two halves put down for row r
-      const float* x = reinterpret_cast<const float*>(base + G::kTwo) + k * 2 * kLRows + r;
-      return make_float2(x[0], x[kLRows]);
+    float* own = reinterpret_cast<float*>(base + G::kShare) + part * kLRows;  // [2][kParts][64], this part's
+    const auto most = [&](int k, int r) {  // the largest that the parts put down for row r
+      const float* x = reinterpret_cast<const float*>(base + G::kShare) + k * kParts * kLRows + r;
+      return fmaxf(fmaxf(x[0], x[kLRows]), fmaxf(x[2 * kLRows], x[3 * kLRows]));
     };
-    volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 32;  // [2] a softmax wait did, by the tile's parity
+    volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 64;  // [2] a softmax wait did, by the tile's parity
     uint32_t it = 0;  // tiles so far
     while (walk.next(u, tid == 0 ? p.flag : nullptr)) {
       const int64_t row0 = (int64_t)u.b * p.chunk * p.hq + (int64_t)u.r * kLRows;
@@ -391,15 +390,14 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
         continue;
       }
-      // q: four lanes share a row's 64-byte pieces, the two halves take every second
-      // one; hi to lanes 0..15, lo to lanes 16..31 of the quarter's TMEM lanes
-      constexpr int kOwn = (kSteps + 1) / 2;
+      // q: four lanes share a row's 64-byte pieces, a part takes every fourth one; hi to lanes 0..15, lo to lanes 16..31 of the quarter's TMEM lanes
+      constexpr int kOwn = (kSteps + kParts - 1) / kParts;
       uint4 qv[2][kOwn];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
-          const int s = 2 * k + half;
+          const int s = kParts * k + part;
           qv[i][k] = make_uint4(0u, 0u, 0u, 0u);
           if (lr[i] < u.rows && s < kSteps)
             qv[i][k] = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + lr[i]) * (L + R) + 32 * s + 8 * t));
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-        if (t == 0) two[lr[i]] = __uint_as_float(am);
+        if (t == 0) own[lr[i]] = __uint_as_float(am);
       }
       named_barrier_sync(1, kLSoftmax);
       float xs[2];      // S to log2 units, before the token's scale
@@ -423,8 +421,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       bool plain = true;  // the short form of scores and sums has the range it needs
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 ab = both(0, lr[i]);
-        const uint32_t am = max(__float_as_uint(ab.x), __float_as_uint(ab.y));
+        const uint32_t* ams = reinterpret_cast<const uint32_t*>(base + G::kShare) + lr[i];
+        const uint32_t am = max(max(ams[0], ams[kLRows]), max(ams[2 * kLRows], ams[3 * kLRows]));
         const int ex = min(max((int)(am >> 23), 8), 254);  // times 2^(134 - ex): to [2^7, 2^8)
         const bool bad = am >= 0x7F800000u;  // an Inf or NaN: the row's scores are NaN, its codes 0
         const float mul = __uint_as_float((uint32_t)(261 - ex) << 23);
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       }
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) {
-        const int s = 2 * k + half;
+        const int s = kParts * k + part;
         if (s < kSteps) {
           tmem_st_16x256b_x1(tw + G::kQCol + 8 * s, qv[0][k].x, qv[0][k].y, qv[1][k].x, qv[1][k].y);
           tmem_st_16x256b_x1(tw + (16u << 16) + G::kQCol + 8 * s, qv[0][k].z, qv[0][k].w, qv[1][k].z, qv[1][k].w);
@@ -470,51 +468,51 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         const int st = (int)(it % G::kStages);
         if (!ready && !failed) failed = !wait(bars + 8 * (kLSFull + st), (it / G::kStages) & 1u);
         tc_fence_after();
-        uint32_t v[16], lo[16];
-        tmem_ld_16x256b_x4(tw + G::kSCol + 32 * half, v);
-        tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + 32 * half, lo);
+        uint32_t v[8], lo[8];
+        tmem_ld_16x256b_x2(tw + G::kSCol + kPCols * part, v);
+        tmem_ld_16x256b_x2(tw + (16u << 16) + G::kSCol + kPCols * part, lo);
         const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
-        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (32 * half + 2 * t));
-        uint64_t s2[4], x2[4];
+        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
+        uint64_t s2[kPairs], x2[kPairs];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kPairs; ++k) {
           s2[k] = lds_f32x2(sc + 32 * k);
           x2[k] = lds_f32x2(sc + 4 * kLT + 32 * k);
         }
         const int64_t p0 = (int64_t)j * kLT;
-        const bool part = p0 + kLT > full_upto;  // some row sees the tile in part
+        const bool partly = p0 + kLT > full_upto;  // some row sees the tile in part
         tmem_wait_ld2(v, lo);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
-        uint64_t z2[2][4];
+        uint64_t z2[2][kPairs];
         float top[2], my[2] = {m[0], m[1]};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kPairs; ++k) {
             const uint64_t S = add2(pack2(__uint_as_float(v[4 * k + 2 * i]), __uint_as_float(v[4 * k + 2 * i + 1])),
                                     pack2(__uint_as_float(lo[4 * k + 2 * i]), __uint_as_float(lo[4 * k + 2 * i + 1])));
             z2[i][k] = near ? fma2(mul2(S, pack2(xs[i], xs[i])), s2[k], x2[k])
                             : add2(mul2(S, mul2(pack2(xs[i], xs[i]), s2[k])), x2[k]);  // S xs could leave the range
           }
-          if (part) {
-            const int lim = (int)max((int64_t)-1, min((int64_t)kLT, last[i] - p0)) - 32 * half - 2 * t;
+          if (partly) {
+            const int lim = (int)max((int64_t)-1, min((int64_t)kLT, last[i] - p0)) - kPCols * part - 2 * t;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kPairs; ++k) {
               const float2 f = unpack2(z2[i][k]);
               z2[i][k] = pack2(8 * k > lim ? -INFINITY : f.x, 8 * k + 1 > lim ? -INFINITY : f.y);
             }
           }
           if (!near) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kPairs; ++k) {
               const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
               my[i] = fmaxf(my[i], fmaxf(x.x == -INFINITY ? x.x : f.x - x.x, x.y == -INFINITY ? x.y : f.y - x.y));
             }
           }
-          const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
-          top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
+          const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]);
+          top[i] = fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
         }
         // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
         const bool x_free = it < 2 || wait.look(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
@@ -535,14 +533,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           // others); O's columns follow (none at the unit's first tile)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (t == 0) two[2 * kLRows + lr[i]] = top[i];
+            if (t == 0) own[kParts * kLRows + lr[i]] = top[i];
           named_barrier_sync(1, kLSoftmax);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 ab = both(1, lr[i]);
-            const float most = fmaxf(ab.x, ab.y), to = most > ref[i] + kSlackL ? floorf(most) : ref[i];
+            const float all = most(1, lr[i]), to = all > ref[i] + kSlackL ? floorf(all) : ref[i];
             const float a = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
-            if (t == 0 && half == 0) alpha[lr[i]] = a;
+            if (t == 0 && part == 0) alpha[lr[i]] = a;
             if (near) {
               m[i] = to;
               l2[i] = mul2(l2[i], pack2(a, a));
@@ -555,18 +552,18 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             tc_fence_after();
 #pragma unroll 1
             for (int mm = 0; mm < kM; ++mm) {
-              uint32_t o[32];
-              const uint32_t at = tw + G::kOCol + kLRows * mm + 32 * half;
-              tmem_ld32(at, o);
+              uint32_t o[16];
+              const uint32_t at = tw + G::kOCol + kLRows * mm + 16 * part;
+              tmem_ld16(at, o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(alpha + 32 * half + 4 * k);
+              for (int k = 0; k < 4; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(alpha + 16 * part + 4 * k);
                 o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
                 o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
                 o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
                 o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * a.w);
               }
-              tmem_st32_async(at, o);
+              tmem_st16_async(at, o);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -578,7 +575,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           failed = !wait(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
         const uint32_t nx = it + 1;
         ready = j + 1 < u.t1 && wait.look(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
-        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(half * 2048 + 2 * t);
+        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 1024 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
@@ -590,7 +587,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             l2[i] = mul2(l2[i], pack2(a, a));
             m[i] = to;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kPairs; ++k) {
               const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
               l2[i] = add2(l2[i], pack2(x.x == -INFINITY ? 0.0f : fast_exp2((f.x - x.x) - zero),
                                         x.y == -INFINITY ? 0.0f : fast_exp2((f.y - x.y) - zero)));
@@ -598,7 +595,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           }
           uint64_t sum = 0ull;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kPairs; ++k) {
             const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
             if (near) sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
@@ -611,7 +608,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               hi = (hi & ~over) | (q & over);
               rest = (rest & ~over) | (r & over);
             }
-            const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
+            const uint32_t a = at + (uint32_t)(8 * k);
             sts_u16(a, hi);
             sts_u16(a + kPBytes, rest);
           }
@@ -622,62 +619,66 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         __syncwarp();
         if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + (it & 1)));
       }
-      // the unit's result: O / l, l over both halves and a reference of both
+      // the unit's result: O / l, l over the row's parts and for a reference of all
       if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
       if (softmax_or(failed)) {
         failed = true;
         break;
       }
-      float l[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mm = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
-        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 2));
-        const float2 x = unpack2(l2[i]);
-        l[i] = (x.x + x.y) * (m[i] == -INFINITY ? 1.0f : fast_exp2(m[i] - mm));
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-        if (t == 0) {
-          two[2 * kLRows + lr[i]] = mm;
-          two[4 * kLRows + lr[i]] = l[i];
-        }
-      }
-      named_barrier_sync(1, kLSoftmax);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 ma = both(1, lr[i]), la = both(2, lr[i]);
-        const float top = fmaxf(ma.x, ma.y), mm = top == -INFINITY ? 0.0f : top;
-        const float lx = (ma.x == -INFINITY ? la.x : la.x * fast_exp2(ma.x - mm)) +
-                         (ma.y == -INFINITY ? la.y : la.y * fast_exp2(ma.y - mm));
-        const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm, h = rintf(0.5f * d);
-        if (t == 0 && half == 0) {  // two factors: 2^d alone can leave fp32's range
-          alpha[lr[i]] = fast_exp2(h);
-          alpha[kLRows + lr[i]] = lx == 0.0f ? 0.0f : fast_exp2(d - h) / lx;
-          if (!u.whole)
-            p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + lr[i]] = lx == 0.0f ? -INFINITY : mm + log2f(lx);
-        }
-      }
-      named_barrier_sync(1, kLSoftmax);
       tc_fence_after();
-      float* po = p.part_o + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows * L;
-#pragma unroll 1
-      for (int mm = 0; mm < kM; ++mm) {
-        const int c0 = 32 * half, ch = 128 * mm + 32 * quad + lane;
-        if (c0 >= u.rows) break;
-        uint32_t o[32];
-        tmem_ld32(tw + G::kOCol + kLRows * mm + c0, o);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int r = c0 + c;
-          if (r < u.rows) {
-            const float f = alpha[kLRows + r];
-            const float x = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * alpha[r] * f;
-            if (!u.whole)
-              po[r * L + ch] = x;
-            else if (p.out_bf16)
-              static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * L + ch] = __float2bfloat16_rn(x);
-            else
-              static_cast<float*>(p.out)[(row0 + r) * L + ch] = x;
+      for (int i = 0; i < 2; ++i) {
+        float mq = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
+        mq = fmaxf(mq, __shfl_xor_sync(0xFFFFFFFFu, mq, 2));
+        if (t == 0) own[kParts * kLRows + lr[i]] = mq;
+      }
+      named_barrier_sync(1, kLSoftmax);
+      float mm[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float all = most(1, lr[i]);
+        mm[i] = all == -INFINITY ? 0.0f : all;
+        const float2 x = unpack2(l2[i]);
+        float l = (x.x + x.y) * fast_exp2(m[i] - mm[i]);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+        if (t == 0) own[lr[i]] = l;
+      }
+      named_barrier_sync(1, kLSoftmax);
+      if (t == 0 && part == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float* x = own + lr[i];  // part 0's
+          const float l = (x[0] + x[kLRows]) + (x[2 * kLRows] + x[3 * kLRows]);
+          const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm[i], h = rintf(0.5f * d);
+          alpha[lr[i]] = fast_exp2(h);  // two factors: 2^d alone can leave fp32's range
+          alpha[kLRows + lr[i]] = l == 0.0f ? 0.0f : fast_exp2(d - h) / l;
+          if (!u.whole)
+            p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + lr[i]] = l == 0.0f ? -INFINITY : mm[i] + log2f(l);
+        }
+      }
+      named_barrier_sync(1, kLSoftmax);
+      float* po = p.part_o + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows * L;
+      const int c0 = 16 * part, there = min(16, u.rows - c0);  // the part's columns of O, those with rows
+      if (there > 0) {
+#pragma unroll 1
+        for (int mm = 0; mm < kM; ++mm) {
+          const int ch = 128 * mm + 32 * quad + lane;
+          uint32_t o[16];
+          tmem_ld16(tw + G::kOCol + kLRows * mm + c0, o);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int r = c0 + c;
+            if (c < there) {
+              const float f = alpha[kLRows + r];
+              const float x = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * alpha[r] * f;
+              if (!u.whole)
+                po[r * L + ch] = x;
+              else if (p.out_bf16)
+                static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * L + ch] = __float2bfloat16_rn(x);
+              else
+                static_cast<float*>(p.out)[(row0 + r) * L + ch] = x;
+            }
           }
         }
       }
@@ -851,57 +852,64 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   }
 }
 
-// Joins the parts of units that several CTAs worked on: a warp per row,
-// out = sum w_i o_i, w_i = 2^(lse_i - m) / sum 2^(lse_j - m).
+// Joins the parts of units that several CTAs worked on, out = sum w_i o_i, w_i =
+// 2^(lse_i - m) / sum 2^(lse_j - m): a CTA per row, its warps take every fourth part, two
+// at a time, and add up in a fixed order.
 template <int L>
-__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParams p, int row_blocks) {
-  grid_dependency_wait();
-  const int unit = blockIdx.x / row_blocks, r = blockIdx.x % row_blocks * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int b = unit / p.tpb, rt = unit % p.tpb;
+__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParams p, int rows_per_unit) {
+  __shared__ float acc_s[4][L];
+  __shared__ float l_s[4];
+  const int unit = blockIdx.x / rows_per_unit, r = blockIdx.x % rows_per_unit, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, b = unit / p.tpb, rt = unit % p.tpb;
   const int n = p.chunk_lens ? __ldg(p.chunk_lens + b) : p.chunk;
-  if (n < 0 || n > p.chunk || r >= kLRows || (int64_t)rt * kLRows + r >= (int64_t)n * p.hq) return;
+  grid_dependency_wait();
+  if (n < 0 || n > p.chunk || (int64_t)rt * kLRows + r >= (int64_t)n * p.hq) return;
   const int2 rec = p.rec[unit];
   if (rec.y <= 1 || !KVQ_IN(rec.x >= 0 && (int64_t)rec.x + (int64_t)(rec.y - 1) * p.tpb < (int64_t)p.groups * p.tpb, p.flag)) return;
   const auto at = [&](int i) { return ((int64_t)(rec.x + i * p.tpb) * 2 + (i == 0 ? 1 : 0)) * kLRows + r; };
   float m = -INFINITY;
-  bool nan = false;
-  for (int i = lane; i < rec.y; i += 32) {
-    const float x = p.part_lse[at(i)];
-    m = fmaxf(m, x);
-    nan |= x != x;
-  }
+  for (int i = lane; i < rec.y; i += 32) m = fmaxf(m, p.part_lse[at(i)]);
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  nan = __any_sync(0xFFFFFFFFu, nan);
   const float mm = m == -INFINITY ? 0.0f : m;
   float acc[L / 32], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < L / 32; ++c) acc[c] = 0.0f;
-  for (int i = 0; i < rec.y; ++i) {
-    const int64_t a = at(i);
-    const float x = p.part_lse[a];
-    if (x == -INFINITY) continue;
-    const float w = fast_exp2(x - mm);
-    l += w;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + a * L) + lane;
+  for (int i = warp; i < rec.y; i += 8) {
+    const int64_t a[2] = {at(i), at(i + 4 < rec.y ? i + 4 : i)};
+    float4 v[2][L / 128];
+    float w[2];
 #pragma unroll
-    for (int c = 0; c < L / 128; ++c) {
-      const float4 v = src[32 * c];
-      acc[4 * c] += w * v.x, acc[4 * c + 1] += w * v.y, acc[4 * c + 2] += w * v.z, acc[4 * c + 3] += w * v.w;
+    for (int k = 0; k < 2; ++k) {
+      w[k] = p.part_lse[a[k]];
+#pragma unroll
+      for (int c = 0; c < L / 128; ++c) v[k][c] = (reinterpret_cast<const float4*>(p.part_o + a[k] * L) + lane)[32 * c];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (w[k] == -INFINITY || (k == 1 && i + 4 >= rec.y)) continue;  // (a part without weight left no result)
+      const float x = fast_exp2(w[k] - mm);
+      l += x;
+#pragma unroll
+      for (int c = 0; c < L / 128; ++c) {
+        acc[4 * c] += x * v[k][c].x, acc[4 * c + 1] += x * v[k][c].y;
+        acc[4 * c + 2] += x * v[k][c].z, acc[4 * c + 3] += x * v[k][c].w;
+      }
     }
   }
-  const float f = nan ? __uint_as_float(0x7FFFFFFFu) : l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t row = (int64_t)b * p.chunk * p.hq + (int64_t)rt * kLRows + r;
 #pragma unroll
-  for (int c = 0; c < L / 128; ++c) {
-    const float4 v = make_float4(acc[4 * c] * f, acc[4 * c + 1] * f, acc[4 * c + 2] * f, acc[4 * c + 3] * f);
-    if (p.out_bf16) {
-      uint2 w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w.x) : "f"(v.y), "f"(v.x));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w.y) : "f"(v.w), "f"(v.z));
-      *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * L) + 32 * c + lane) = w;
-    } else {
-      *(reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * L) + 32 * c + lane) = v;
-    }
+  for (int c = 0; c < L / 128; ++c)
+    reinterpret_cast<float4*>(acc_s[warp])[32 * c + lane] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  const int64_t row = (int64_t)b * p.chunk * p.hq + (int64_t)rt * kLRows + r;
+  l = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  for (int c = threadIdx.x; c < L; c += 128) {
+    const float x = ((acc_s[0][c] + acc_s[1][c]) + (acc_s[2][c] + acc_s[3][c])) * f;
+    if (p.out_bf16)
+      static_cast<__nv_bfloat16*>(p.out)[row * L + c] = __float2bfloat16_rn(x);
+    else
+      static_cast<float*>(p.out)[row * L + c] = x;
   }
 }
 
@@ -957,9 +965,8 @@ kvq_status launch_latent(const LatentAttnParams& p, const LatentCut& cut, cudaSt
   if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
   if (cut.groups == 0) return KVQ_OK;
   const int rows = (int)((int64_t)p.chunk * p.hq < kLRows ? (int64_t)p.chunk * p.hq : kLRows);
-  const int row_blocks = (rows + 3) / 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.batch * p.tpb * row_blocks));
+  cfg.gridDim = dim3((unsigned)(p.batch * p.tpb * rows));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -967,7 +974,7 @@ kvq_status launch_latent(const LatentAttnParams& p, const LatentCut& cut, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L>, p, row_blocks) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L>, p, rows) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 bool latent_sizes_ok(int32_t batch, int32_t hq, int32_t chunk) {
