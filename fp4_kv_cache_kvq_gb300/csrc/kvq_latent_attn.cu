@@ -30,10 +30,12 @@
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
 // the longest first.
-// Twenty warps: softmax (16; thread = two rows x 4 positions of a tile), loader, two
-// that issue the products, scales, joined by mbarriers (every wait bounded):
+// Twenty warps: softmax (two groups of 8 that take every second tile; thread = two rows x
+// 8 positions), loader, two that issue the products, scales, joined by mbarriers (every
+// wait bounded); of a tile's steps only the choice of the references waits for the tile
+// before:
 //   loader    bulk copies of 64-token tiles into a ring
-//   products  S(j) = q K(j)^T         kind::f8f6f4, q from TMEM
+//   products  S(j) = q K(j)^T         kind::f8f6f4, q's latent part from TMEM; two buffers
 //             O^T += K(j)^T x(j)      kind::f8f6f4, twice (hi, lo), from another warp:
 //             one's waits do not hold up the other's products
 //   scales    2^e, e and 2^-e of a tile's tokens, once for all rows
@@ -48,12 +50,12 @@ namespace {
 
 constexpr int kLT = 64;     // positions per tile
 constexpr int kLRows = 64;  // query rows per unit
-constexpr int kParts = 4, kPCols = kLT / kParts;  // softmax warps that share a row, a tile's positions of each
+// softmax warps: two groups that take every second tile, two parts of a tile's positions each
+constexpr int kParts = 4, kPCols = 32, kPairs = kPCols / 8, kGroupThreads = 256;
 constexpr int kLSmWarps = 4 * kParts, kLSoftmax = 32 * kLSmWarps, kLThreads = kLSoftmax + 128;
 constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 1;  // and the scales' warp
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 2;           // least tiles of a split range
-constexpr int kPairs = kPCols / 8;     // pairs of positions of a thread's
 // x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): over 2^11.8 the rest
 // behind E5M2 would leave E4M3.  The references are raised only past the slack, since
 // that rescales O (a slack of 3: among 64 rows some raised its own in every second
@@ -65,8 +67,9 @@ enum : int {
   kLFull = 0,               // [stages] codes and exponents landed
   kLEmpty = kLFull + 8,     // [stages] the tile's sums done (commit)
   kLSFull = kLEmpty + 8,    // [stages] S in TMEM (commit), and the tile's scales ready
-  kLSFree = kLSFull + 8,    // S taken by the softmax warps
-  kLQFull = kLSFree + 1,    // q in TMEM
+  kLSFree = kLSFull + 8,    // [2] S taken by the group's warps
+  kLRef = kLSFree + 2,      // [2] the references that hold from a tile on
+  kLQFull = kLRef + 2,      // q in TMEM and shared memory
   kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
   kLPvDone = kLPFull + 2,   // [2] O += done
   kLDrain = kLPvDone + 2,   // the last commits of the two issuing warps
@@ -94,20 +97,23 @@ template <int L, int R>
 struct LGeo {
   static constexpr int kRow = L + 2 * R;
   static constexpr int kTile = kLT * kRow;
-  static constexpr int kStages = kTile * 5 + 4 * kPBytes > 220 * 1024 ? 4 : 5;
-  static constexpr int kP = kStages * kTile;              // [2][hi, lo]
-  static constexpr int kExp = kP + 4 * kPBytes;           // [stages][64]
+  static constexpr int kMost = (220 * 1024 - 4 * kPBytes - 128 * R) / (kTile + kLT * 13);
+  static constexpr int kStages = kMost < 6 ? kMost : 6;
+  static constexpr int kP = kStages * kTile;              // [2][first, second part]
+  static constexpr int kQr = kP + 4 * kPBytes;            // q's position part [R / 16][16 row groups][8][16]
+  static constexpr int kExp = kQr + 128 * R;              // [stages][64]
   static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
-  static constexpr int kAlpha = kMask + 8 * 8;            // [64] factors of O's columns, [64] second ones
+  static constexpr int kRefS = kMask + 8 * 8;             // [64] the rows' references
+  static constexpr int kAlpha = kRefS + 4 * kLRows;       // [2][64] factors of O's columns: a group's, or the result's two
   static constexpr int kShare = kAlpha + 2 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
   static constexpr int kSc = kShare + 2 * kParts * 4 * kLRows;  // [stages][3][64] 2^e, e (-inf: no token), 2^-e
   static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40
   static constexpr int kBar = kNear + 4 * 8;
-  static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, plan
-  static constexpr int kUsed = kMisc + 320 + 128;
+  static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, the groups' [2][2]
+  static constexpr int kUsed = kMisc + 32 + 128;
   static constexpr int kBytes = kUsed > 116 * 1024 ? kUsed : 116 * 1024;  // one CTA per SM: it holds all of TMEM
-  static constexpr int kOCol = 0, kQCol = L / 2, kSCol = kQCol + (L + R) / 4;
-  static_assert(kSCol + kLT <= 512 && kUsed <= 227 * 1024 && kBar % 8 == 0 && kStages <= 8, "layout");
+  static constexpr int kOCol = 0, kQCol = L / 2, kSCol = kQCol + L / 4;
+  static_assert(kSCol + 2 * kLT <= 512 && kStages >= 4 && kUsed <= 227 * 1024 && kBar % 8 == 0 && kStages <= 8, "layout");
 };
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -129,19 +135,26 @@ constexpr uint32_t kIdS = (1u << 4) | (kLT / 8 << 17) | (128u / 16 << 24);
 constexpr uint32_t kIdOHi = (1u << 4) | (1u << 15) | (kLRows / 8 << 17) | (128u / 16 << 24);  // A MN-major
 constexpr uint32_t kIdOLo = kIdOHi | (1u << 10);
 
-// 16 lanes x 16 columns of TMEM, without the wait: register 4j + 2i + e holds row
+// 16 lanes x 32 columns of TMEM, without the wait: register 4j + 2i + e holds row
 // lane/4 + 8i, column 8j + 2(lane%4) + e.
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(taddr)
-               : "memory");
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
 }
 // Wait for the thread's TMEM loads; a and b pass through, so their uses stay behind it.
-__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[8], uint32_t (&b)[8]) {
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[16], uint32_t (&b)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
                  "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
                :
                : "memory");
 }
@@ -175,6 +188,9 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
   asm volatile("ld.shared.b64 %0, [%1];\n" : "=l"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void sts_u32x2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
@@ -186,13 +202,13 @@ __device__ __forceinline__ __half2 u32_half2(uint32_t v) {
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
-// Named barrier 1 of the softmax warps; true when any thread's v is.
-__device__ __forceinline__ bool softmax_or(bool v) {
+// Named barrier `id` of `threads` softmax threads; true when any thread's v is.
+__device__ __forceinline__ bool softmax_or(uint32_t id, uint32_t threads, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(v ? 1u : 0u)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -213,11 +229,42 @@ struct Unit {
   int slot;
 };
 
+// The CTA's range of the line of all sequences' tiles: sequence b starts at `base` of it.
 struct Plan {
-  int64_t lo, hi, base;  // range on the line, and where sequence b starts on it
-  int64_t per;
+  int64_t lo, hi, base, per;
   int b;
 };
+
+// Every warp finds it for itself, so that none waits for another's.
+__device__ __forceinline__ Plan find_plan(const LatentAttnParams& p, int lane) {
+  Plan r = {0, 0, 0, 1, 0};
+  if (p.groups == 0) return r;
+  int64_t total = 0;
+  for (int b = lane; b - lane < p.batch; b += 32)
+    total += __reduce_add_sync(0xFFFFFFFFu, b < p.batch ? (uint32_t)line_tiles(p, b) : 0u);  // 2^25 each at most
+  const int64_t up = total + p.groups - 1;
+  r.per = max((int64_t)kMinTiles, up >> 32 ? up / p.groups : (int64_t)((uint32_t)up / (uint32_t)p.groups));
+  r.lo = (int64_t)(blockIdx.x / (unsigned)p.tpb) * r.per;
+  if (r.lo >= total) return r;
+  r.hi = min(r.lo + r.per, total);
+  for (int b = lane; b - lane < p.batch; b += 32) {
+    const uint32_t c = b < p.batch ? (uint32_t)line_tiles(p, b) : 0u;
+    uint32_t pre = c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    const uint32_t sum = __shfl_sync(0xFFFFFFFFu, pre, 31);
+    if (r.lo < r.base + sum) {
+      const int at = __ffs(__ballot_sync(0xFFFFFFFFu, r.lo < r.base + pre)) - 1;
+      r.base += __shfl_sync(0xFFFFFFFFu, pre - c, at);
+      r.b = b - lane + at;
+      break;
+    }
+    r.base += sum;
+  }
+  return r;
+}
 
 // The CTA's units in order; every role walks them alike.
 struct Walk {
@@ -290,9 +337,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   const uint32_t sb = smem_addr(base), bars = sb + G::kBar;
   uint32_t* misc = reinterpret_cast<uint32_t*>(base + G::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
-  Plan* plan = reinterpret_cast<Plan*>(misc + 2);
-  int64_t* sums = reinterpret_cast<int64_t*>(misc + 2 + sizeof(Plan) / 4);  // [warps]
-  static_assert(8 + sizeof(Plan) + 8 * (kLThreads / 32) <= 256, "behind it, the softmax warps' words");
   volatile int* near_s = reinterpret_cast<volatile int*>(base + G::kNear);
   volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(base + G::kMask);
   const BoundedWaits wait{abort, p.wait_ns};
@@ -304,76 +348,41 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       mbar_init(bars + 8 * (kLEmpty + s), 1);
       mbar_init(bars + 8 * (kLSFull + s), 2);
     }
-    mbar_init(bars + 8 * kLSFree, kLSmWarps);
     mbar_init(bars + 8 * kLQFull, kLSmWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (kLPFull + i), kLSmWarps);
+      mbar_init(bars + 8 * (kLSFree + i), kLSmWarps / 2);
+      mbar_init(bars + 8 * (kLRef + i), kLSmWarps / 2);
+      mbar_init(bars + 8 * (kLPFull + i), kLSmWarps / 2);
       mbar_init(bars + 8 * (kLPvDone + i), 1);
     }
     mbar_init(bars + 8 * kLDrain, 2);
     *abort = 0;
-    misc[64] = misc[65] = 0u;
-    plan->lo = plan->hi = plan->base = 0;
-    plan->b = 0;
+    misc[2] = misc[3] = misc[4] = misc[5] = 0u;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_addr(misc), 512);
-  if (p.groups > 0) {  // where the CTA's range of the line lies
-    const int each = (p.batch + kLThreads - 1) / kLThreads, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
-    int64_t own = 0;
-    for (int b = b0; b < b1; ++b) own += line_tiles(p, b);
-    int64_t pre = own;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, pre, o);
-      if (lane >= o) pre += x;
-    }
-    if (lane == 31) sums[warp] = pre;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kLThreads / 32; ++w) {
-      if (w < warp) pre += sums[w];
-      total += sums[w];
-    }
-    const int64_t per = max((int64_t)kMinTiles, (total + p.groups - 1) / p.groups);
-    const int64_t lo = (int64_t)(blockIdx.x / (unsigned)p.tpb) * per;
-    int64_t at = pre - own;
-    if (lo >= at && lo < pre) {
-      int b = b0;
-      for (; b < b1; ++b) {
-        const int64_t c = line_tiles(p, b);
-        if (lo < at + c) break;
-        at += c;
-      }
-      plan->lo = lo;
-      plan->hi = min(lo + per, total);
-      plan->base = at;
-      plan->per = per;
-      plan->b = b;
-    }
-  }
+  Walk walk(p, find_plan(p, lane));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
-  Walk walk(p, *plan);
   Unit u;
   bool failed = false;
 
   if (warp < kLSmWarps) {
     // ------------------------------------------------------------ softmax
-    // warp w: rows 16 (w & 3) .. + 15, whose scores lie in its 32 TMEM lanes, and the
-    // positions 16 (w >> 2) .. + 15 of a tile
-    const int g = lane >> 2, t = lane & 3, quad = warp & 3, part = warp >> 2;
+    // warp w: rows 16 (w & 3) .. + 15, whose scores lie in its 32 TMEM lanes; of every
+    // second tile (w >> 3) the positions 32 (w >> 2 & 1) .. + 31
+    const int g = lane >> 2, t = lane & 3, quad = warp & 3, share = warp >> 2, part = share & 1;
+    const uint32_t grp = (uint32_t)share >> 1, bar_g = 2 + grp;
     const uint32_t tw = tmem + ((uint32_t)(32 * quad) << 16);
     const int lr[2] = {16 * quad + g, 16 * quad + g + 8};
+    float* ref_s = reinterpret_cast<float*>(base + G::kRefS);
     float* alpha = reinterpret_cast<float*>(base + G::kAlpha);
-    float* own = reinterpret_cast<float*>(base + G::kShare) + part * kLRows;  // [2][kParts][64], this part's
-    const auto most = [&](int k, int r) {  // the largest that the parts put down for row r
-      const float* x = reinterpret_cast<const float*>(base + G::kShare) + k * kParts * kLRows + r;
-      return fmaxf(fmaxf(x[0], x[kLRows]), fmaxf(x[2 * kLRows], x[3 * kLRows]));
-    };
-    volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 64;  // [2] a softmax wait did, by the tile's parity
-    uint32_t it = 0;  // tiles so far
+    float* shared = reinterpret_cast<float*>(base + G::kShare);  // [2][kParts][64]
+    float* own = shared + share * kLRows;
+    volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 2 + 2 * grp;  // [2] a wait of the group did, by its tile's parity
+    uint32_t it0 = 0;  // tiles before the unit
     while (walk.next(u, tid == 0 ? p.flag : nullptr)) {
       const int64_t row0 = (int64_t)u.b * p.chunk * p.hq + (int64_t)u.r * kLRows;
       if (u.t0 >= u.t1) {  // nothing attended: zero rows, or a part without weight
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
-          const int s = kParts * k + part;
+          const int s = kParts * k + share;
           qv[i][k] = make_uint4(0u, 0u, 0u, 0u);
           if (lr[i] < u.rows && s < kSteps)
             qv[i][k] = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + lr[i]) * (L + R) + 32 * s + 8 * t));
@@ -415,14 +424,16 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
         if (t == 0) own[lr[i]] = __uint_as_float(am);
       }
+      if (tid < kLRows) ref_s[tid] = -INFINITY;
       named_barrier_sync(1, kLSoftmax);
       float xs[2];      // S to log2 units, before the token's scale
       int64_t last[2];  // last position that the row attends
       bool plain = true;  // the short form of scores and sums has the range it needs
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t* ams = reinterpret_cast<const uint32_t*>(base + G::kShare) + lr[i];
-        const uint32_t am = max(max(ams[0], ams[kLRows]), max(ams[2 * kLRows], ams[3 * kLRows]));
+        const float* ams = shared + lr[i];
+        const uint32_t am = max(max(__float_as_uint(ams[0]), __float_as_uint(ams[kLRows])),
+                                max(__float_as_uint(ams[2 * kLRows]), __float_as_uint(ams[3 * kLRows])));
         const int ex = min(max((int)(am >> 23), 8), 254);  // times 2^(134 - ex): to [2^7, 2^8)
         const bool bad = am >= 0x7F800000u;  // an Inf or NaN: the row's scores are NaN, its codes 0
         const float mul = __uint_as_float((uint32_t)(261 - ex) << 23);
@@ -446,12 +457,21 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       }
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) {
-        const int s = kParts * k + part;
-        if (s < kSteps) {
+        const int s = kParts * k + share;
+        if (s < L / 32) {
           tmem_st_16x256b_x1(tw + G::kQCol + 8 * s, qv[0][k].x, qv[0][k].y, qv[1][k].x, qv[1][k].y);
           tmem_st_16x256b_x1(tw + (16u << 16) + G::kQCol + 8 * s, qv[0][k].z, qv[0][k].w, qv[1][k].z, qv[1][k].w);
+        } else if (s < kSteps) {  // the position part: row 32 quad + 16 (lo) + its number, as the TMEM lanes
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = sb + G::kQr + (uint32_t)((2 * (s - L / 32) + (t >> 1)) * 2048 + (4 * quad + i) * 128 +
+                                                         g * 16 + (t & 1) * 8);
+            sts_u32x2(at, qv[i][k].x, qv[i][k].y);
+            sts_u32x2(at + 256, qv[i][k].z, qv[i][k].w);
+          }
         }
       }
+      fence_async_smem();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -460,17 +480,18 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       // l counts 2^(y - m).  Short form: m is ref, and 2^(y - ref) is x 2^-e.  That would lose
       // what scales far apart leave under fp32's range: from a tile with a scale outside
       // 2^-40 .. 2^40 on, m is the thread's own largest y, with exponentials of its own.
-      float ref[2] = {-INFINITY, -INFINITY}, m[2] = {-INFINITY, -INFINITY};
+      float m[2] = {-INFINITY, -INFINITY};
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
-      bool ready = false;  // the next tile's scores are there
-      for (int j = u.t0; j < u.t1; ++j, ++it) {
+      bool ready = false;  // the group's next tile's scores are there
+      for (int j = u.t0 + (int)((grp ^ it0) & 1u); j < u.t1; j += 2) {
+        const uint32_t it = it0 + (uint32_t)(j - u.t0);
         const int st = (int)(it % G::kStages);
         if (!ready && !failed) failed = !wait(bars + 8 * (kLSFull + st), (it / G::kStages) & 1u);
         tc_fence_after();
-        uint32_t v[8], lo[8];
-        tmem_ld_16x256b_x2(tw + G::kSCol + kPCols * part, v);
-        tmem_ld_16x256b_x2(tw + (16u << 16) + G::kSCol + kPCols * part, lo);
+        uint32_t v[16], lo[16];
+        tmem_ld_16x256b_x4(tw + G::kSCol + kLT * grp + kPCols * part, v);
+        tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + kLT * grp + kPCols * part, lo);
         const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
         const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
         uint64_t s2[kPairs], x2[kPairs];
@@ -484,7 +505,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         tmem_wait_ld2(v, lo);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * kLSFree);
+        if (lane == 0) mbar_arrive(bars + 8 * (kLSFree + grp));
         uint64_t z2[2][kPairs];
         float top[2], my[2] = {m[0], m[1]};
 #pragma unroll
@@ -511,21 +532,24 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               my[i] = fmaxf(my[i], fmaxf(x.x == -INFINITY ? x.x : f.x - x.x, x.y == -INFINITY ? x.y : f.y - x.y));
             }
           }
-          const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]);
-          top[i] = fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+          const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
+          top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
         // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
-        const bool x_free = it < 2 || wait.look(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
+        const bool x_free = it < 2 || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
+        if (j > u.t0 && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
+        float ref[2];
         bool up = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          ref[i] = ref_s[lr[i]];
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
           up |= top[i] > ref[i] + kSlackL;
         }
-        if (failed) gave_up[it & 1] = 1;
-        if (softmax_or(up || failed)) {
-          if (gave_up[it & 1]) {
+        if (failed) gave_up[it >> 1 & 1] = 1;
+        if (softmax_or(bar_g, kGroupThreads, up || failed)) {
+          if (gave_up[it >> 1 & 1]) {
             failed = true;
             break;
           }
@@ -534,30 +558,31 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (t == 0) own[kParts * kLRows + lr[i]] = top[i];
-          named_barrier_sync(1, kLSoftmax);
+          named_barrier_sync(bar_g, kGroupThreads);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float all = most(1, lr[i]), to = all > ref[i] + kSlackL ? floorf(all) : ref[i];
-            const float a = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
-            if (t == 0 && part == 0) alpha[lr[i]] = a;
-            if (near) {
-              m[i] = to;
-              l2[i] = mul2(l2[i], pack2(a, a));
+            const float* x = shared + (kParts + 2 * grp) * kLRows + lr[i];
+            const float all = fmaxf(x[0], x[kLRows]), to = all > ref[i] + kSlackL ? floorf(all) : ref[i];
+            if (t == 0 && part == 0) {
+              alpha[grp * kLRows + lr[i]] = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
+              ref_s[lr[i]] = to;
             }
             ref[i] = to;
           }
-          named_barrier_sync(1, kLSoftmax);
+          named_barrier_sync(bar_g, kGroupThreads);
+          if (lane == 0) mbar_arrive(bars + 8 * (kLRef + grp));
           if (j > u.t0) {
-            failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
+            failed = !wait(bars + 8 * (kLPvDone + (grp ^ 1)), ((it - 1) >> 1) & 1u);
             tc_fence_after();
 #pragma unroll 1
-            for (int mm = 0; mm < kM; ++mm) {
+            for (int c = 0; c < 2 * kM; ++c) {
               uint32_t o[16];
-              const uint32_t at = tw + G::kOCol + kLRows * mm + 16 * part;
+              const int col = 32 * part + 16 * (c & 1);
+              const uint32_t at = tw + G::kOCol + kLRows * (c >> 1) + col;
               tmem_ld16(at, o);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(alpha + 16 * part + 4 * k);
+                const float4 a = *reinterpret_cast<const float4*>(alpha + grp * kLRows + col + 4 * k);
                 o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
                 o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
                 o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
@@ -568,20 +593,26 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             tmem_wait_st();
             tc_fence_before();
           }
+        } else if (lane == 0) {
+          mbar_arrive(bars + 8 * (kLRef + grp));
         }
         // x in two parts to shared memory, [16 tokens][8 rows] core matrices, once the sums
         // of the tile before last have read theirs
         if (!__all_sync(0xFFFFFFFFu, x_free) && !failed)
-          failed = !wait(bars + 8 * (kLPvDone + (it & 1)), ((it >> 1) - 1) & 1u);
-        const uint32_t nx = it + 1;
-        ready = j + 1 < u.t1 && wait.look(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
-        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 1024 + 2 * t);
+          failed = !wait(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
+        const uint32_t nx = it + 2;  // a look at the next wait, ahead of its time: it takes 150 cycles
+        ready = j + 2 < u.t1 && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
+        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
           const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448
           const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16);
-          if (!near) {
+          if (near) {
+            const float a = m[i] == ref[i] ? 1.0f : fast_exp2(m[i] - ref[i]);  // raised since the group's last tile
+            l2[i] = mul2(l2[i], pack2(a, a));
+            m[i] = ref[i];
+          } else {
             const float to = my[i], zero = to == -INFINITY ? 0.0f : to;
             const float a = m[i] == -INFINITY ? 1.0f : fast_exp2(m[i] - to);
             l2[i] = mul2(l2[i], pack2(a, a));
@@ -608,7 +639,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               hi = (hi & ~over) | (q & over);
               rest = (rest & ~over) | (r & over);
             }
-            const uint32_t a = at + (uint32_t)(8 * k);
+            const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
             sts_u16(a, hi);
             sts_u16(a + kPBytes, rest);
           }
@@ -617,11 +648,12 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + (it & 1)));
+        if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + grp));
       }
       // the unit's result: O / l, l over the row's parts and for a reference of all
-      if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1u);
-      if (softmax_or(failed)) {
+      it0 += (uint32_t)(u.t1 - u.t0);
+      if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it0 - 1) & 1)), ((it0 - 1) >> 1) & 1u);
+      if (softmax_or(1, kLSoftmax, failed)) {
         failed = true;
         break;
       }
@@ -636,7 +668,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       float mm[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float all = most(1, lr[i]);
+        const float* ms = shared + kParts * kLRows + lr[i];
+        const float all = fmaxf(fmaxf(ms[0], ms[kLRows]), fmaxf(ms[2 * kLRows], ms[3 * kLRows]));
         mm[i] = all == -INFINITY ? 0.0f : all;
         const float2 x = unpack2(l2[i]);
         float l = (x.x + x.y) * fast_exp2(m[i] - mm[i]);
@@ -645,12 +678,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         if (t == 0) own[lr[i]] = l;
       }
       named_barrier_sync(1, kLSoftmax);
-      if (t == 0 && part == 0) {
+      if (t == 0 && share == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float* x = own + lr[i];  // part 0's
+          const float* x = shared + lr[i];
+          const float r = ref_s[lr[i]];
           const float l = (x[0] + x[kLRows]) + (x[2 * kLRows] + x[3 * kLRows]);
-          const float d = (ref[i] == -INFINITY ? 0.0f : ref[i]) - kTop - mm[i], h = rintf(0.5f * d);
+          const float d = (r == -INFINITY ? 0.0f : r) - kTop - mm[i], h = rintf(0.5f * d);
           alpha[lr[i]] = fast_exp2(h);  // two factors: 2^d alone can leave fp32's range
           alpha[kLRows + lr[i]] = l == 0.0f ? 0.0f : fast_exp2(d - h) / l;
           if (!u.whole)
@@ -659,27 +693,40 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       }
       named_barrier_sync(1, kLSoftmax);
       float* po = p.part_o + ((int64_t)blockIdx.x * 2 + u.slot) * kLRows * L;
-      const int c0 = 16 * part, there = min(16, u.rows - c0);  // the part's columns of O, those with rows
-      if (there > 0) {
+      // (128 channels of 16 rows at a time, the warps of a quarter in turn)
 #pragma unroll 1
-        for (int mm = 0; mm < kM; ++mm) {
-          const int ch = 128 * mm + 32 * quad + lane;
-          uint32_t o[16];
-          tmem_ld16(tw + G::kOCol + kLRows * mm + c0, o);
+      for (int c = share; c < 4 * kM; c += kParts) {
+        const int mm = c % kM, c0 = 16 * (c / kM), there = u.rows - c0, ch = 128 * mm + 32 * quad + lane;
+        if (there <= 0) break;
+        uint32_t o[16];
+        float4 fa[4], fb[4];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int r = c0 + c;
-            if (c < there) {
-              const float f = alpha[kLRows + r];
-              const float x = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * alpha[r] * f;
-              if (!u.whole)
-                po[r * L + ch] = x;
-              else if (p.out_bf16)
-                static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * L + ch] = __float2bfloat16_rn(x);
-              else
-                static_cast<float*>(p.out)[(row0 + r) * L + ch] = x;
-            }
-          }
+        for (int k = 0; k < 4; ++k) {
+          fa[k] = *reinterpret_cast<const float4*>(alpha + c0 + 4 * k);
+          fb[k] = *reinterpret_cast<const float4*>(alpha + kLRows + c0 + 4 * k);
+        }
+        tmem_ld16(tw + G::kOCol + kLRows * mm + c0, o);
+        const auto scaled = [&](int k, float a, float b) { return b == 0.0f ? 0.0f : __uint_as_float(o[k]) * a * b; };
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[4 * k] = scaled(4 * k, fa[k].x, fb[k].x), x[4 * k + 1] = scaled(4 * k + 1, fa[k].y, fb[k].y);
+          x[4 * k + 2] = scaled(4 * k + 2, fa[k].z, fb[k].z), x[4 * k + 3] = scaled(4 * k + 3, fa[k].w, fb[k].w);
+        }
+        if (!u.whole) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (k < there) po[(c0 + k) * L + ch] = x[k];
+        } else if (p.out_bf16) {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (row0 + c0) * L + ch;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (k < there) out[k * L] = __float2bfloat16_rn(x[k]);
+        } else {
+          float* out = static_cast<float*>(p.out) + (row0 + c0) * L + ch;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (k < there) out[k * L] = x[k];
         }
       }
       tc_fence_before();
@@ -736,6 +783,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     if (warp == kSWarpL) {
       // ---------------------------------------------------------- scores
       const uint64_t dk = smem_desc(sb, 128, 8 * G::kRow);  // tokens as rows: K-major
+      const uint64_t dq = smem_desc(sb + G::kQr, 2048, 128);
       uint32_t un = 0;
       while (!failed && walk.next(u, nullptr)) {
         if (u.t0 >= u.t1) continue;
@@ -744,7 +792,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         for (int j = u.t0; j < u.t1; ++j, ++it) {
           const int st = (int)(it % G::kStages);
           if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u) ||
-              (it > 0 && !wait(bars + 8 * kLSFree, (it - 1) & 1u))) {
+              (it > 1 && !wait(bars + 8 * (kLSFree + (it & 1)), ((it >> 1) - 1) & 1u))) {
             failed = true;
             break;
           }
@@ -762,11 +810,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           tc_fence_after();
           if (elect_one_of_warp()) {
             const uint64_t kd = dk + (uint64_t)(st * (G::kTile >> 4));
+            const uint32_t d = tmem + G::kSCol + kLT * (it & 1);
 #pragma unroll
-            for (int s = 0; s < kSteps + R / 32; ++s) {
-              const int a = s < kSteps ? s : s - R / 32;  // the key part's lo codes meet the same q
-              mma_f8_ta(tmem + G::kSCol, tmem + G::kQCol + 8 * a, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
-            }
+            for (int s = 0; s < L / 32; ++s)
+              mma_f8_ta(d, tmem + G::kQCol + 8 * s, kd + (uint64_t)(s * 256 >> 4), kIdS, s > 0);
+#pragma unroll
+            for (int s = 0; s < 2 * R / 32; ++s)  // the key part's hi and lo codes meet the same q
+              mma_f8(d, dq + (uint64_t)(s % (R / 32) * 4096 >> 4), kd + (uint64_t)((L / 32 + s) * 256 >> 4), kIdS, true);
             tc_commit(bars + 8 * (kLSFull + st));
           }
           __syncwarp();

@@ -12,8 +12,11 @@ namespace kvq {
 struct BoundedWaits {
   volatile int* abort;
   uint64_t limit;  // a test's, ns, or 0
+  // whether the phase is over; does not wait
+  __device__ __forceinline__ bool over(uint32_t bar, uint32_t parity) const { return mbar_test_wait(bar, parity); }
+  // (suspended in the barrier: a warp that polls takes issue slots from those that work)
   __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) const {
-    return limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+    return limit ? mbar_test_wait(bar, parity) : mbar_try_wait_hint(bar, parity, 1000000u);
   }
   __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) const {
     if (look(bar, parity)) return true;
