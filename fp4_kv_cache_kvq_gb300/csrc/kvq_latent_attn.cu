@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       named_barrier_sync(1, kLSoftmax);
       float xs[2];      // S to log2 units, before the token's scale
       int64_t last[2];  // last position that the row attends
-      bool plain = true;  // the short form of scores and sums has the range it needs
+      bool plain = true;  // the short form of the sums has the range it needs
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float* ams = shared + lr[i];
@@ -438,7 +438,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         const bool bad = am >= 0x7F800000u;  // an Inf or NaN: the row's scores are NaN, its codes 0
         const float mul = __uint_as_float((uint32_t)(261 - ex) << 23);
         xs[i] = bad ? __uint_as_float(0x7FFFFFFFu) : p.scale_log2 * __uint_as_float((uint32_t)(ex - 7) << 23);
-        plain = plain && !(xs[i] > 1.15e18f);  // (a NaN stays one in either form)
         last[i] = lr[i] < u.rows ? u.first + (u.r * kLRows + lr[i]) / p.hq : -1;
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {  // in place: x, y the hi codes, z, w the lo codes
@@ -514,8 +513,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           for (int k = 0; k < kPairs; ++k) {
             const uint64_t S = add2(pack2(__uint_as_float(v[4 * k + 2 * i]), __uint_as_float(v[4 * k + 2 * i + 1])),
                                     pack2(__uint_as_float(lo[4 * k + 2 * i]), __uint_as_float(lo[4 * k + 2 * i + 1])));
-            z2[i][k] = near ? fma2(mul2(S, pack2(xs[i], xs[i])), s2[k], x2[k])
-                            : add2(mul2(S, mul2(pack2(xs[i], xs[i]), s2[k])), x2[k]);  // S xs could leave the range
+            z2[i][k] = fma2(S, mul2(pack2(xs[i], xs[i]), s2[k]), x2[k]);
           }
           if (partly) {
             const int lim = (int)max((int64_t)-1, min((int64_t)kLT, last[i] - p0)) - kPCols * part - 2 * t;
@@ -606,8 +604,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
-          const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448
           const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16);
+          const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448: E5M2 first
           if (near) {
             const float a = m[i] == ref[i] ? 1.0f : fast_exp2(m[i] - ref[i]);  // raised since the group's last tile
             l2[i] = mul2(l2[i], pack2(a, a));
@@ -629,7 +627,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           for (int k = 0; k < kPairs; ++k) {
             const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
-            if (near) sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
+            sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
             const uint32_t h = pack_f16x2(xa, xb);
             uint32_t hi = e4m3x2_of_f16x2(h);
             uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
