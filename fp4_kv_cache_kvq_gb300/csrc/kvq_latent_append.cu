@@ -16,6 +16,8 @@ namespace kvq {
 namespace {
 
 constexpr int kThreadsA = 256;
+constexpr int kThreadsD = 8 * (512 + 64) / 16;  // of the read-back, at most
+constexpr int kQHeads = 2;  // query heads of a thread: they share the angles
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 struct LatentAppendParams {
@@ -32,7 +34,8 @@ struct LatentAppendParams {
   int64_t q_ts, q_hs, qo_ts, qo_hs, c_ts, k_ts, table_rows;
   int32_t batch, n_new, hq, interleaved;
   uint32_t blocks;   // 8-token blocks per sequence
-  uint32_t tok_ctas; // CTAs of latents and key parts; the rest rotate queries
+  uint32_t head_groups;  // of kQHeads query heads
+  uint32_t tok_ctas;     // CTAs of latents and key parts; the rest rotate queries
 };
 
 // New tokens of sequence b and its start; 0 tokens (flagged) where either is bad.
@@ -48,22 +51,23 @@ __device__ __forceinline__ int new_tokens(const LatentAppendParams& p, int b, in
 
 __device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// Eight pairs: x0 and x1 hold the first and the second halves' 8 values (or, of
-// adjacent pairs, 16 consecutive values); rotated in place.  cs: 8 cosines, sn: 8
-// sines.  Every product and sum is rounded to fp32, the result to bf16.
-__device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float* __restrict__ cs, const float* __restrict__ sn,
-                                        int interleaved) {
-  uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-  float c[8], s[8];
+// Eight cosines, then eight sines, `half` behind them in the table's row.
+__device__ __forceinline__ void load_angles(const float* row, int half, float (&cs)[16]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs) + i), s4 = __ldg(reinterpret_cast<const float4*>(sn) + i);
-    c[4 * i] = c4.x, c[4 * i + 1] = c4.y, c[4 * i + 2] = c4.z, c[4 * i + 3] = c4.w;
-    s[4 * i] = s4.x, s[4 * i + 1] = s4.y, s[4 * i + 2] = s4.z, s[4 * i + 3] = s4.w;
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(row + (i >> 1) * half) + (i & 1));
+    cs[4 * i] = v.x, cs[4 * i + 1] = v.y, cs[4 * i + 2] = v.z, cs[4 * i + 3] = v.w;
   }
+}
+
+// Eight pairs: a and b hold the first and the second halves' 8 values (or, of
+// adjacent pairs, 16 consecutive values); rotated in place.  Every product and sum
+// is rounded to fp32, the result to bf16.
+__device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[16], int interleaved) {
+  uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
   const auto turn = [&](float x0, float x1, int i, float& y0, float& y1) {
-    y0 = __fsub_rn(__fmul_rn(x0, c[i]), __fmul_rn(x1, s[i]));
-    y1 = __fadd_rn(__fmul_rn(x1, c[i]), __fmul_rn(x0, s[i]));
+    y0 = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(x1, cs[8 + i]));
+    y1 = __fadd_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x0, cs[8 + i]));
   };
   if (interleaved) {
 #pragma unroll
@@ -137,36 +141,46 @@ __device__ __forceinline__ int piece_b(int i, int half, int interleaved) { retur
 // (token t = lane & 7, unit u) 16 channels of the latent, so that 8 lanes store one
 // core matrix; the block's first warp also takes the key parts, lane (t, item).
 template <int L>
-__global__ void __launch_bounds__(kThreadsA) latent_append_kernel(const LatentAppendParams p) {
+__global__ void __launch_bounds__(kThreadsA, 5) latent_append_kernel(const LatentAppendParams p) {
   constexpr int kPer = L / 2, kBlocks = kThreadsA / kPer;
   __shared__ uint32_t amax_s[kBlocks * 8];
   const int tid = threadIdx.x, R = p.c.rope_dim, half = R / 2;
-  if (blockIdx.x >= p.tok_ctas) {  // query parts: one thread per eight pairs
-    const uint64_t i = (uint64_t)(blockIdx.x - p.tok_ctas) * kThreadsA + tid;
-    const uint32_t per = (uint32_t)R / 16u;
-    const uint32_t it = (uint32_t)i % per;
-    const uint64_t rest = i / per;
-    const uint32_t h = (uint32_t)(rest % (uint32_t)p.hq);
-    const uint64_t tok = rest / (uint32_t)p.hq;
-    if (tok >= (uint64_t)p.batch * p.n_new) return;
-    const int b = (int)(tok / (uint32_t)p.n_new), t = (int)(tok % (uint32_t)p.n_new);
-    const uint16_t* src = p.q + tok * p.q_ts + h * p.q_hs;
+  if (blockIdx.x >= p.tok_ctas) {  // query parts: eight pairs of kQHeads heads a thread
+    const uint32_t i = (blockIdx.x - p.tok_ctas) * kThreadsA + tid;  // under 2^30 + 256
+    const uint32_t it = i & ((uint32_t)R / 16u - 1u), rest = i >> (R == 64 ? 2 : 1);
+    const uint32_t tok32 = rest / p.head_groups;
+    const int h0 = (int)(rest - tok32 * p.head_groups) * kQHeads, heads = min(kQHeads, p.hq - h0);
+    const int b = (int)(tok32 / (uint32_t)p.n_new), t = (int)(tok32 - (uint32_t)b * (uint32_t)p.n_new);
+    if (b >= p.batch) return;
+    const int64_t tok = tok32;
+    const uint16_t* src = p.q + tok * p.q_ts + h0 * p.q_hs;
+    uint16_t* dst = p.q_out + tok * p.qo_ts + h0 * p.qo_hs;
     const int ca = piece_a(it, p.interleaved), cb = piece_b(it, half, p.interleaved);
-    uint16_t* dst = p.q_out + tok * p.qo_ts + h * p.qo_hs;
     int32_t sp;
     if (t >= new_tokens(p, b, sp)) return;
-    uint4 va = *reinterpret_cast<const uint4*>(src + ca), vb = *reinterpret_cast<const uint4*>(src + cb);
+    uint4 va[kQHeads], vb[kQHeads];
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k)
+      if (k < heads) {
+        va[k] = *reinterpret_cast<const uint4*>(src + k * p.q_hs + ca);
+        vb[k] = *reinterpret_cast<const uint4*>(src + k * p.q_hs + cb);
+      }
+    float cs[16];
+    const int64_t pos = (int64_t)sp + t;
     if (p.table != nullptr) {
-      const int64_t pos = (int64_t)sp + t;
       if (pos >= p.table_rows) {
         set_flag(p.flag, KVQ_FLAG_POSITION);
         return;
       }
-      const float* row = p.table + pos * R;
-      rotate8(va, vb, row + 8 * it, row + half + 8 * it, p.interleaved);
+      load_angles(p.table + pos * R + 8 * it, half, cs);
     }
-    *reinterpret_cast<uint4*>(dst + ca) = va;
-    *reinterpret_cast<uint4*>(dst + cb) = vb;
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k)
+      if (k < heads) {
+        if (p.table != nullptr) rotate8(va[k], vb[k], cs, p.interleaved);
+        *reinterpret_cast<uint4*>(dst + k * p.qo_hs + ca) = va[k];
+        *reinterpret_cast<uint4*>(dst + k * p.qo_hs + cb) = vb[k];
+      }
     return;
   }
   if (tid < kBlocks * 8) amax_s[tid] = 0u;
@@ -199,8 +213,9 @@ __global__ void __launch_bounds__(kThreadsA) latent_append_kernel(const LatentAp
     }
     grp = latent_group(p.c, lay, b, pos, p.flag);
     if (rope && p.table != nullptr) {
-      const float* row = p.table + pos * R;
-      rotate8(ka, kb, row + 8 * it, row + half + 8 * it, p.interleaved);
+      float cs[16];
+      load_angles(p.table + pos * R + 8 * it, half, cs);
+      rotate8(ka, kb, cs, p.interleaved);
     }
   }
   uint32_t m = max(max(amax8(v0), amax8(v1)), max(amax8(ka), amax8(kb)));
@@ -249,7 +264,7 @@ struct LatentDequantParams {
   void* k_out;
   int32_t* flag;
   int32_t batch, max_len;
-  uint32_t blocks;  // 8-token blocks per sequence
+  uint32_t pairs;  // pairs of 8-token blocks per sequence
 };
 
 // 16 E4M3 codes (bytes of v) as fp32.
@@ -275,46 +290,54 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&x)[16]) {
     reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// A thread per token and 16 channels (of the latent, then of the key part), 8
-// tokens side by side in a warp: they read one core matrix.
+// A CTA takes two blocks of 8 tokens, a thread one token's 16 channels (of the latent,
+// then of the key part) in each, 8 tokens side by side in a warp: they read one core
+// matrix.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsA) latent_dequant_kernel(const LatentDequantParams p) {
+__global__ void __launch_bounds__(kThreadsD) latent_dequant_kernel(const LatentDequantParams p) {
   const LatentLayout lay(p.c);
-  const uint32_t units = (uint32_t)(lay.L + lay.R) / 16u;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreadsA + threadIdx.x;
-  const int t8 = (int)(i & 7);
-  const uint32_t u = (uint32_t)((i >> 3) % units);
-  const uint64_t blk = (i >> 3) / units;
-  const int b = (int)(blk / p.blocks);
-  const int64_t pos = (int64_t)(blk % p.blocks) * 8 + t8;
-  if (b >= p.batch || pos >= p.max_len) return;
+  const uint32_t pair = blockIdx.x % p.pairs;
+  const int b = (int)(blockIdx.x / p.pairs), t8 = threadIdx.x & 7, u = threadIdx.x >> 3;
   const int len = __ldg(p.lens + b);
-  if (len < 0 && pos == 0 && u == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
-  float x[16];
+  if (len < 0 && pair == 0 && threadIdx.x == 0) set_flag(p.flag, KVQ_FLAG_BAD_LENGTH);
+  const bool key = 16 * u >= lay.L;
+  const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
+  uint4 v[2], w[2];
+  uint32_t e[2];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) x[c] = 0.0f;
-  if (pos < len) {
+  for (int i = 0; i < 2; ++i) {
+    const int64_t pos = (int64_t)pair * 16 + 8 * i + t8;
+    v[i] = w[i] = make_uint4(0u, 0u, 0u, 0u);
+    e[i] = 1u;
+    if (pos >= len || pos >= p.max_len) continue;
     const int64_t grp = latent_group(p.c, lay, b, pos, p.flag);
-    if (grp >= 0 && KVQ_IN(grp + lay.group_bytes() <= p.c.num_pages * lay.page_bytes(), p.flag)) {
-      const uint8_t* base = static_cast<const uint8_t*>(p.c.data) + grp;
-      const int slot = (int)(pos & (lay.G - 1));
-      const float s = latent_scale(__ldg(base + lay.exponent(slot)));
-      decode16(__ldg(reinterpret_cast<const uint4*>(base + lay.unit(slot, u))), x);
-      if (16 * u >= (uint32_t)lay.L) {
-        float lo[16];
-        decode16(__ldg(reinterpret_cast<const uint4*>(base + lay.unit(slot, u + lay.R / 16))), lo);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] += lo[c];
-      }
-#pragma unroll
-      for (int c = 0; c < 16; ++c) x[c] *= s;
-    }
+    if (grp < 0 || !KVQ_IN(grp + lay.group_bytes() <= p.c.num_pages * lay.page_bytes(), p.flag)) continue;
+    const int slot = (int)(pos & (lay.G - 1));
+    e[i] = __ldg(pool + grp + lay.exponent(slot));
+    v[i] = __ldg(reinterpret_cast<const uint4*>(pool + grp + lay.unit(slot, u)));
+    if (key) w[i] = __ldg(reinterpret_cast<const uint4*>(pool + grp + lay.unit(slot, u + lay.R / 16)));
   }
-  const int64_t row = (int64_t)b * p.max_len + pos;
-  if (16 * u < (uint32_t)lay.L)
-    store16(static_cast<T*>(p.c_out) + row * lay.L + 16 * u, x);
-  else
-    store16(static_cast<T*>(p.k_out) + row * lay.R + 16 * u - lay.L, x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t pos = (int64_t)pair * 16 + 8 * i + t8;
+    if (pos >= p.max_len) continue;
+    float x[16];
+    decode16(v[i], x);
+    if (key) {
+      float lo[16];
+      decode16(w[i], lo);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] += lo[c];
+    }
+    const float s = latent_scale(e[i]);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) x[c] *= s;
+    const int64_t row = (int64_t)b * p.max_len + pos;
+    if (!key)
+      store16(static_cast<T*>(p.c_out) + row * lay.L + 16 * u, x);
+    else
+      store16(static_cast<T*>(p.k_out) + row * lay.R + 16 * u - lay.L, x);
+  }
 }
 
 // Strides of rows of `width` values: multiples of 8 that leave no overlap.
@@ -374,8 +397,9 @@ extern "C" kvq_status kvq_latent_append(const kvq_latent_cache* cache, int32_t b
   p.c_ts = c_stride, p.k_ts = k_stride, p.table_rows = table_rows;
   p.batch = batch, p.n_new = n_new, p.hq = num_q_heads, p.interleaved = interleaved;
   p.blocks = ((uint32_t)n_new + 14u) / 8u;  // aligned blocks can be cut at both ends
-  const double tok = (double)batch * p.blocks * (L / 2), qi = (double)batch * n_new * num_q_heads * (R / 16);
+  const double tok = (double)batch * p.blocks * (L / 2), qi = (double)batch * n_new * ((num_q_heads + kQHeads - 1) / kQHeads) * (R / 16);
   if (tok > (double)(1 << 30) || qi > (double)(1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  p.head_groups = (uint32_t)((num_q_heads + kQHeads - 1) / kQHeads);
   p.tok_ctas = grid_for((int64_t)tok, kThreadsA);
   const unsigned grid = p.tok_ctas + (num_q_heads > 0 ? grid_for((int64_t)qi, kThreadsA) : 0u);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -403,14 +427,13 @@ extern "C" kvq_status kvq_latent_dequant(const kvq_latent_cache* cache, int32_t 
   p.lens = d_seq_lens;
   p.c_out = c_out, p.k_out = k_out, p.flag = d_err_flag;
   p.batch = batch, p.max_len = max_len;
-  p.blocks = ((uint32_t)max_len + 7u) / 8u;
-  const double items = (double)batch * p.blocks * 8.0 * ((cache->latent_dim + cache->rope_dim) / 16);
-  if (items > 256.0 * 2147483647.0) return KVQ_ERR_UNSUPPORTED;
-  const unsigned grid = grid_for((int64_t)items, kThreadsA);
+  p.pairs = ((uint32_t)max_len + 15u) / 16u;
+  if ((double)batch * p.pairs > 2147483647.0) return KVQ_ERR_UNSUPPORTED;
+  const unsigned grid = (unsigned)batch * p.pairs, threads = 8u * (unsigned)(cache->latent_dim + cache->rope_dim) / 16u;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (out_dtype == KVQ_DTYPE_BF16)
-    latent_dequant_kernel<uint16_t><<<grid, kThreadsA, 0, s>>>(p);
+    latent_dequant_kernel<uint16_t><<<grid, threads, 0, s>>>(p);
   else
-    latent_dequant_kernel<float><<<grid, kThreadsA, 0, s>>>(p);
+    latent_dequant_kernel<float><<<grid, threads, 0, s>>>(p);
   return launch_status();
 }

@@ -92,7 +92,7 @@ def test_invalid_appends_are_refused(lib, bad):
 def test_appends_too_large_for_one_call(lib):
     big = dict(c=_cache(num_pages=1 << 30, max_pages_per_seq=1 << 22))
     assert _append(lib, n=1 << 26, qt=64 * 192, ot=64 * 576, **big) == 2
-    assert _append(lib, n=1 << 21, hq=128, qt=128 * 192, ot=128 * 576, **big) == 2
+    assert _append(lib, n=1 << 23, hq=128, qt=128 * 192, ot=128 * 576, **big) == 2
 
 
 @pytest.mark.parametrize("bad", [
