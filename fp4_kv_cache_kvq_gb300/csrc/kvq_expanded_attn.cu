@@ -10,17 +10,20 @@
 // 2^kSlackE; sums, maxima and accumulators are fp32.
 //
 // What bounds it: the tensor pipe, 2 (2 d + 64) flop per attended pair and head; a
-// unit's tiles come from L2, 61 KB per 96 positions at d = 128.
+// unit's tiles come from L2, 51 KB per 80 positions at d = 128.
 // Work: a CTA takes 256 query tokens of a head as two 128-row tiles that share each
-// tile of 96 positions (two of them in flight, with both query tiles, is what shared
-// memory holds at d = 128); the longest first, 16 heads at a time so that their keys
-// and values stay in L2.
+// tile of 80 positions: with 80, tensor memory holds both tiles' scores, weights and
+// sums side by side, so that the next scores are computed beside the softmax of these
+// (with 96 and the weights over the scores: S, softmax and P V one after the other, 3200
+// cycles a tile; 302 us where this takes 277, 2 x 4096 tokens, 32 heads of 128).  The longest first, 16 heads at a time so that their keys and
+// values stay in L2.
 // Eleven warps: softmax (2 x 4, thread = row), loader (TMA, 128-byte swizzle), MMA
 // issue (one per query tile, so that one's softmax runs beside the other's products),
 // joined by mbarriers (every wait bounded):
 //   S_X(j) = q_X K(j)^T    both from shared memory; the key's position part is one
 //                          more 64-channel slab behind the head's own
-//   O_X += P_X(j) V(j)     P from TMEM over S's columns, V as MN-major operand
+//   O_X += P_X(j) V(j)     P from TMEM, V as MN-major operand
+//                          in the order S(j + 1), O(j)
 #include "../../include/kvq_latent.h"
 #include "kvq_common.cuh"
 #include "kvq_host.cuh"
@@ -32,7 +35,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kET = 96;       // positions per tile
+constexpr int kET = 80;       // positions per tile
 constexpr int kERows = 128;   // rows of a query tile
 constexpr int kERope = 64;
 constexpr int kESoftmax = 8, kELoad = kESoftmax, kEMma = kELoad + 1, kEThreads = 32 * (kEMma + 2);
@@ -47,7 +50,8 @@ enum : int {
   kEVFull = kEKEmpty + 4,
   kEVEmpty = kEVFull + 4,
   kESFull = kEVEmpty + 4,   // [2] S_X in TMEM
-  kEPFull = kESFull + 2,    // [2] P_X in TMEM, O_X rescaled
+  kESFree = kESFull + 2,    // [2] S_X taken by the softmax
+  kEPFull = kESFree + 2,    // [2] P_X in TMEM, O_X rescaled
   kEPvDone = kEPFull + 2,   // [2] O_X += done
   kEDrain = kEPvDone + 2,   // [2] an MMA warp's last commit
   kEBars = kEDrain + 2
@@ -73,8 +77,8 @@ struct EGeo {
   static constexpr int kBar = kV + kRing * kVSlabs * kTSlab;
   static constexpr int kMisc = kBar + 8 * kEBars;
   static constexpr int kBytes = kMisc + 16 + 1024;  // 1024: the swizzle's alignment
-  static constexpr int kOCol = 2 * kET;
-  static_assert(kBytes <= 227 * 1024 && kBytes > 116 * 1024 && kOCol + 2 * D <= 512, "layout");
+  static constexpr int kSCol = 2 * D, kPCol = kSCol + 2 * kET;  // O_X at [X D, +D)
+  static_assert(kBytes <= 227 * 1024 && kBytes > 116 * 1024 && kPCol + kET <= 512, "layout");
 };
 
 // Descriptors of operands with the 128-byte swizzle (8 rows of 128 bytes an atom).
@@ -103,6 +107,12 @@ __device__ __forceinline__ void tmem_ld_max16(uint32_t taddr, uint32_t* v, uint3
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(m)
       : "r"(taddr)
       : "memory");
+}
+// 8 columns of this warp's TMEM lanes, without the wait.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // keeps the uses of v and m behind the wait
 __device__ __forceinline__ void behind(uint32_t* v, uint32_t& m) {
@@ -173,6 +183,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (kESFull + i), 1);
+      mbar_init(bars + 8 * (kESFree + i), 4);
       mbar_init(bars + 8 * (kEPFull + i), 4);
       mbar_init(bars + 8 * (kEPvDone + i), 1);
       mbar_init(bars + 8 * (kEDrain + i), 1);
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2, r = tid & 127, i = kERows * x + r;
     const uint32_t tw = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t s_col = tw + x * kET, o_col = tw + G::kOCol + x * D;
+    const uint32_t s_col = tw + G::kSCol + x * kET, p_col = tw + G::kPCol + x * (kET / 2), o_col = tw + x * D;
     const int ntx = x < nx ? tiles_of(x) : 0;
     const int last = first + i, all = first + kERows * x;  // last position of the row, of every row
     float ref = -INFINITY;
@@ -205,6 +216,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
       asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
       for (int k = 0; k < kET / 16; ++k) behind(v + 16 * k, mx[k]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kESFree + x));
       float top = -INFINITY;
       if ((j + 1) * kET > all + 1) {  // some row sees the tile in part
         const int lim = last - j * kET;
@@ -218,12 +232,15 @@ __global__ void __launch_bounds__(kEThreads, 1)
         for (int k = 0; k < kET / 16; ++k) top = fmaxf(top, __uint_as_float(mx[k]));
       }
       top *= p.scale_log2;
+      // the sums of the tile before: done with O and P
+      if (j > 0 && !(ok = wait(bars + 8 * (kEPvDone + x), (j - 1) & 1u))) break;
+      tc_fence_after();
       const bool up = top > ref + kSlackE;
       if (__any_sync(0xFFFFFFFFu, up)) {
         const float to = up ? top : ref, a = up ? fast_exp2(ref - to) : 1.0f;
         l2 = mul2(l2, pack2(a, a));
         ref = to;
-        if (j > 0) {  // (S(j) was issued behind the sums of j - 1)
+        if (j > 0) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -237,17 +254,17 @@ __global__ void __launch_bounds__(kEThreads, 1)
       const float zero = ref == -INFINITY ? 0.0f : -ref;
       const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), r2 = pack2(zero, zero);
 #pragma unroll
-      for (int k = 0; k < kET / 32; ++k) {
-        uint32_t w[16];
+      for (int k = 0; k < kET / 16; ++k) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = 32 * k + 2 * e;
+        for (int e = 0; e < 8; ++e) {
+          const int c = 16 * k + 2 * e;
           const float2 y = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, r2));
           const float a = fast_exp2(y.x), bb = fast_exp2(y.y);
           l2 = add2(l2, pack2(a, bb));
           w[e] = bf16x2(a, bb);
         }
-        tmem_st16_async(s_col + 16 * k, w);
+        tmem_st8(p_col + 8 * k, w);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     const uint64_t dq = swizzled_desc(sb + G::kQ + x * G::kKSlabs * kQSlab, 16, 1024);
     const uint64_t dk = swizzled_desc(sb + G::kK, 16, 1024);        // positions as rows: K-major
     const uint64_t dv = swizzled_desc(sb + G::kV, kTSlab, 1024);    // channels as rows: MN-major
-    const uint32_t s_col = tmem + x * kET, o_col = tmem + G::kOCol + x * D;
+    const uint32_t s_col = tmem + G::kSCol + x * kET, p_col = tmem + G::kPCol + x * (kET / 2), o_col = tmem + x * D;
     const auto scores = [&](int j) {
       const int s = j % G::kRing;
       if (elect_one_of_warp()) {
@@ -347,6 +364,16 @@ __global__ void __launch_bounds__(kEThreads, 1)
     for (int j = 0; j < nt && ok; ++j) {
       const int s = j % G::kRing, sn = (j + 1) % G::kRing;
       const uint32_t ph = (uint32_t)(j / G::kRing) & 1u, phn = (uint32_t)((j + 1) / G::kRing) & 1u;
+      if (j + 1 < nt) {
+        if (!(ok = wait(bars + 8 * (kEKFull + sn), phn))) break;
+        if (j + 1 < ntx) {
+          if (!(ok = wait(bars + 8 * (kESFree + x), j & 1u))) break;
+          tc_fence_after();
+          scores(j + 1);
+        } else if (lane == 0) {  // a tile that only the other query tile attends
+          mbar_arrive(bars + 8 * (kEKEmpty + sn));
+        }
+      }
       if (!(ok = wait(bars + 8 * (kEVFull + s), ph))) break;
       if (j < ntx) {
         // values behind the sequence's end: no NaN there may meet a weight of 0
@@ -366,23 +393,13 @@ __global__ void __launch_bounds__(kEThreads, 1)
           const uint64_t v0 = dv + (uint64_t)(s * (G::kVSlabs * kTSlab >> 4));
 #pragma unroll
           for (int c = 0; c < kET / 16; ++c)
-            tc_mma_f16_ta(o_col, s_col + 8 * c, v0 + (uint64_t)(c * 2048 >> 4), idesc_bf16(D, true), j > 0 || c > 0);
+            tc_mma_f16_ta(o_col, p_col + 8 * c, v0 + (uint64_t)(c * 2048 >> 4), idesc_bf16(D, true), j > 0 || c > 0);
           tc_commit(bars + 8 * (kEPvDone + x));
           tc_commit(bars + 8 * (kEVEmpty + s));
         }
         __syncwarp();
-      } else if (lane == 0) {  // a tile that only the other query tile attends
+      } else if (lane == 0) {
         mbar_arrive(bars + 8 * (kEVEmpty + s));
-      }
-      if (j + 1 < nt) {
-        if (!(ok = wait(bars + 8 * (kEKFull + sn), phn))) break;
-        if (j + 1 < ntx) {  // P lives in S's columns: the next scores follow the product that reads it
-          if (!(ok = wait(bars + 8 * (kEPvDone + x), j & 1u))) break;
-          tc_fence_after();
-          scores(j + 1);
-        } else if (lane == 0) {
-          mbar_arrive(bars + 8 * (kEKEmpty + sn));
-        }
       }
     }
     // no product outlives the CTA
