@@ -17,13 +17,17 @@
 // (with 96 and the weights over the scores: S, softmax and P V one after the other, 3200
 // cycles a tile; 302 us where this takes 277, 2 x 4096 tokens, 32 heads of 128).  The longest first, 16 heads at a time so that their keys and
 // values stay in L2.
-// Eleven warps: softmax (2 x 4, thread = row), loader (TMA, 128-byte swizzle), MMA
+// Twelve warps: softmax (2 x 4, thread = row), loader (TMA, 128-byte swizzle), MMA
 // issue (one per query tile, so that one's softmax runs beside the other's products),
-// joined by mbarriers (every wait bounded):
+// values, joined by mbarriers (every wait bounded):
 //   S_X(j) = q_X K(j)^T    both from shared memory; the key's position part is one
 //                          more 64-channel slab behind the head's own
 //   O_X += P_X(j) V(j)     P from TMEM, V as MN-major operand
 //                          in the order S(j + 1), O(j)
+//   values                 in tiles that some row attends in part (five of a unit at most)
+//                          Inf and NaN leave V, since a weight of 0 would carry them to
+//                          rows that do not see them, and are noted by channel: the rows
+//                          from the first one's position on are NaN there
 #include "../../include/kvq_latent.h"
 #include "kvq_common.cuh"
 #include "kvq_host.cuh"
@@ -38,7 +42,7 @@ namespace {
 constexpr int kET = 80;       // positions per tile
 constexpr int kERows = 128;   // rows of a query tile
 constexpr int kERope = 64;
-constexpr int kESoftmax = 8, kELoad = kESoftmax, kEMma = kELoad + 1, kEThreads = 32 * (kEMma + 2);
+constexpr int kESoftmax = 8, kELoad = kESoftmax, kEMma = kELoad + 1, kEValues = kEMma + 2, kEThreads = 32 * (kEValues + 1);
 constexpr int kQSlab = kERows * 128, kTSlab = kET * 128;  // 64 channels of a query tile, of a tile
 constexpr int kHeadsAtOnce = 16;
 constexpr float kSlackE = 20.0f;
@@ -49,7 +53,8 @@ enum : int {
   kEKEmpty = kEKFull + 4,
   kEVFull = kEKEmpty + 4,
   kEVEmpty = kEVFull + 4,
-  kESFull = kEVEmpty + 4,   // [2] S_X in TMEM
+  kEVIn = kEVEmpty + 4,     // [ring] a partly attended tile's values landed (kEVFull: looked at, too)
+  kESFull = kEVIn + 4,      // [2] S_X in TMEM
   kESFree = kESFull + 2,    // [2] S_X taken by the softmax
   kEPFull = kESFree + 2,    // [2] P_X in TMEM, O_X rescaled
   kEPvDone = kEPFull + 2,   // [2] O_X += done
@@ -75,7 +80,8 @@ struct EGeo {
   static constexpr int kK = 2 * kKSlabs * kQSlab;
   static constexpr int kV = kK + kRing * kKSlabs * kTSlab;
   static constexpr int kBar = kV + kRing * kVSlabs * kTSlab;
-  static constexpr int kMisc = kBar + 8 * kEBars;
+  static constexpr int kNan = kBar + 8 * kEBars;  // [D] the first position whose value is Inf or NaN
+  static constexpr int kMisc = kNan + 4 * D;
   static constexpr int kBytes = kMisc + 16 + 1024;  // 1024: the swizzle's alignment
   static constexpr int kSCol = 2 * D, kPCol = kSCol + 2 * kET;  // O_X at [X D, +D)
   static_assert(kBytes <= 227 * 1024 && kBytes > 116 * 1024 && kPCol + kET <= 512, "layout");
@@ -122,6 +128,11 @@ __device__ __forceinline__ void behind(uint32_t* v, uint32_t& m) {
                  "+r"(m)
                :
                : "memory");
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
@@ -172,6 +183,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
   // tiles that query tile X attends
   const auto tiles_of = [&](int x) { return (first + min(rows, kERows * (x + 1)) + kET - 1) / kET; };
   const int nt = tiles_of(nx - 1);
+  const int part0 = (first + 1) / kET;           // the first tile that not all rows attend
 
   if (tid == 0) {
     mbar_init(bars + 8 * kEQ, 1);
@@ -180,6 +192,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
       mbar_init(bars + 8 * (kEKEmpty + i), nx);
       mbar_init(bars + 8 * (kEVFull + i), 1);
       mbar_init(bars + 8 * (kEVEmpty + i), nx);
+      mbar_init(bars + 8 * (kEVIn + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (kESFull + i), 1);
@@ -189,13 +202,20 @@ __global__ void __launch_bounds__(kEThreads, 1)
       mbar_init(bars + 8 * (kEDrain + i), 1);
     }
     *abort = 0;
+    misc[2] = 0u;
     fence_barrier_init();
   }
+  int* nan_first = reinterpret_cast<int*>(base + G::kNan);
+  if (tid < D) nan_first[tid] = INT32_MAX;
   if (warp == 0) tmem_alloc(smem_addr(misc), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+
+  // where tile j's values land, and the phase of that
+  const auto values_in = [&](int j) { return bars + 8 * ((j < part0 ? kEVFull : kEVIn) + j % G::kRing); };
+  const auto values_phase = [&](int j) { return (uint32_t)((j < part0 ? j : j - part0) / G::kRing) & 1u; };
 
   if (warp < kESoftmax) {
     // ------------------------------------------------------------ softmax
@@ -283,6 +303,11 @@ __global__ void __launch_bounds__(kEThreads, 1)
         if (i < rows) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(w[k]) * f);
+          if (*reinterpret_cast<volatile uint32_t*>(misc + 2)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (nan_first[c + k] <= last) w[k] = 0x7FFFFFFFu;
+          }
           if (p.out_bf16) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
@@ -322,7 +347,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
       kj = j + 1;
       if (j >= G::kRing && !wait(bars + 8 * (kEVEmpty + s), (uint32_t)(j / G::kRing - 1) & 1u)) break;
       if (lane == 0) {
-        const uint32_t bar = bars + 8 * (kEVFull + s), dst = sb + G::kV + s * G::kVSlabs * kTSlab;
+        const uint32_t bar = values_in(j), dst = sb + G::kV + s * G::kVSlabs * kTSlab;
         mbar_arrive_expect_tx(bar, G::kVSlabs * kTSlab);
         for (int c = 0; c < G::kVSlabs; ++c) tma_4d(dst + c * kTSlab, &mv, 64 * c, h, j * kET, b, bar);
       }
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     };
     landed(bars + 8 * kEQ, 0u);
     for (int j = max(0, kj - G::kRing); j < kj; ++j) landed(bars + 8 * (kEKFull + j % G::kRing), (uint32_t)(j / G::kRing) & 1u);
-    for (int j = max(0, vj - G::kRing); j < vj; ++j) landed(bars + 8 * (kEVFull + j % G::kRing), (uint32_t)(j / G::kRing) & 1u);
+    for (int j = max(0, vj - G::kRing); j < vj; ++j) landed(values_in(j), values_phase(j));
   } else if (warp - kEMma < nx) {
     // ------------------------------------------------------------ MMA issue
     const int x = warp - kEMma, ntx = tiles_of(x);
@@ -376,17 +401,6 @@ __global__ void __launch_bounds__(kEThreads, 1)
       }
       if (!(ok = wait(bars + 8 * (kEVFull + s), ph))) break;
       if (j < ntx) {
-        // values behind the sequence's end: no NaN there may meet a weight of 0
-        const int rest = T - j * kET;
-        if (rest < kET) {
-          const uint32_t v0 = sb + G::kV + s * G::kVSlabs * kTSlab;
-          for (int k = lane; k < G::kVSlabs * (kET - rest) * 8; k += 32) {
-            const int slab = k / ((kET - rest) * 8), u = k % ((kET - rest) * 8);
-            sts128(v0 + slab * kTSlab + rest * 128 + 16 * u, make_uint4(0u, 0u, 0u, 0u));
-          }
-          fence_async_smem();
-          __syncwarp();
-        }
         if (!(ok = wait(bars + 8 * (kEPFull + x), j & 1u))) break;
         tc_fence_after();
         if (elect_one_of_warp()) {
@@ -407,6 +421,52 @@ __global__ void __launch_bounds__(kEThreads, 1)
     __syncwarp();
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait_hint(bars + 8 * (kEDrain + x), 0u, 20000u) && global_ns() - t0 < 20000000ull) {
+    }
+  } else if (warp == kEValues) {
+    // ------------------------------------------------------------ values
+    for (int j = part0; j < nt; ++j) {
+      const int s = j % G::kRing;
+      if (!wait(values_in(j), values_phase(j))) break;
+      const uint32_t v0 = sb + G::kV + s * G::kVSlabs * kTSlab;
+      const int there = T - j * kET;  // positions of the tile that the sequence has
+      uint32_t top = 0u;              // the largest magnitudes' bits, Inf and NaN above the rest
+#pragma unroll 8
+      for (int k = 0; k < G::kVSlabs * kET / 4; ++k) {
+        const uint4 v = lds128(v0 + 512 * k + 16 * lane);
+        top = max_u16x2(max_u16x2(top, v.x & 0x7FFF7FFFu), max_u16x2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu));
+        top = max_u16x2(top, v.w & 0x7FFF7FFFu);
+      }
+      const bool look = (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u || there < kET;
+      bool found = false;
+      if (__any_sync(0xFFFFFFFFu, look))
+#pragma unroll 1
+      for (int k = lane; k < G::kVSlabs * kET * 8; k += 32) {  // 16-byte units: slab, position, eight channels
+        const int pos = k / 8 % kET, slab = k / (8 * kET);
+        const uint32_t at = v0 + slab * kTSlab + k % (8 * kET) * 16;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t bad = pos < there ? 0u : 1u;
+        if (pos < there) {
+          v = lds128(at);
+          uint32_t* w = &v.x;
+          uint32_t hit = 0u;  // bit c: channel c of the eight
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if ((w[c] & 0x7F80u) == 0x7F80u) hit |= 1u << 2 * c, w[c] &= 0xFFFF0000u;
+            if ((w[c] & 0x7F800000u) == 0x7F800000u) hit |= 2u << 2 * c, w[c] &= 0xFFFFu;
+          }
+          bad = hit;
+          const int ch = 64 * slab + (k % 8 ^ (pos & 7)) * 8;  // (the swizzle's place of the unit)
+          for (; hit; hit &= hit - 1u) {
+            atomicMin(nan_first + ch + __ffs(hit) - 1, j * kET + pos);
+            found = true;
+          }
+        }
+        if (bad) sts128(at, v);
+      }
+      if (found) *reinterpret_cast<volatile uint32_t*>(misc + 2) = 1u;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kEVFull + s));
     }
   }
   tc_fence_before();

@@ -31,6 +31,7 @@ struct BoundedWaits {
     }
   }
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
     return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity));
   }
 };

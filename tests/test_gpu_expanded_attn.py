@@ -112,6 +112,27 @@ def test_each_position_counts():
     check(out, q, k, kr, v, [T], [T], 1.0)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_later_values_do_not_reach_earlier_rows(bad):
+    """Inf and NaN among keys and values: rows before their position stay as they were, bit for
+    bit; the rows from a value's position on are not finite in its channel."""
+    T, d = 300, 128
+    q, k, kr, v = draw(1, T, T, 2, d, 10, True)
+    want = kvq.expanded_attn(q, k, kr, v, _ints([T]))
+    for pos, ch in ((0, 0), (77, 5), (150, 64), (299, 127)):
+        w = v.clone()
+        w[0, pos, 1, ch] = bad
+        got = kvq.expanded_attn(q, k, kr, w, _ints([T]))
+        hit = torch.zeros_like(want, dtype=torch.bool)
+        hit[0, pos:, 1, ch] = True
+        assert torch.equal(got[~hit], want[~hit]) and not torch.isfinite(got[hit]).any()
+        kk = k.clone()
+        kk[0, pos, 0, ch] = float("nan")
+        got = kvq.expanded_attn(q, kk, kr, v, _ints([T]))
+        assert torch.equal(got[:, :pos], want[:, :pos]) and torch.isnan(got[:, pos:, 0]).all()
+        assert torch.equal(got[:, :, 1], want[:, :, 1])
+
+
 def test_flags_and_skipped_sequences():
     q, k, kr, v = draw(5, 6, 50, 2, 64, 7, True)
     err = _ints([0])
