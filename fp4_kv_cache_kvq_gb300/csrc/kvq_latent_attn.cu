@@ -130,10 +130,10 @@ __device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
-// Instruction descriptors: fp32 accumulators, M = 128, N = 64, A E4M3, B E4M3 or E5M2.
+// Instruction descriptors: fp32 accumulators, M = 128, A E4M3, B E4M3 or E5M2.
 constexpr uint32_t kIdS = (1u << 4) | (kLT / 8 << 17) | (128u / 16 << 24);
-constexpr uint32_t kIdOHi = (1u << 4) | (1u << 15) | (kLRows / 8 << 17) | (128u / 16 << 24);  // A MN-major
-constexpr uint32_t kIdOLo = kIdOHi | (1u << 10);
+constexpr uint32_t kIdO = (1u << 4) | (1u << 15) | (128u / 16 << 24);  // A MN-major; the columns: those with rows
+constexpr uint32_t kIdE5m2 = 1u << 10;                                 // B E5M2
 
 // 16 lanes x 32 columns of TMEM, without the wait: register 4j + 2i + e holds row
 // lane/4 + 8i, column 8j + 2(lane%4) + e.
@@ -482,18 +482,25 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       float m[2] = {-INFINITY, -INFINITY};
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
+      // (a warp without rows keeps step only: the weights that it leaves in x meet columns of O
+      // that nothing reads)
+      const bool rows_here = 16 * quad < u.rows;
       bool ready = false;  // the group's next tile's scores are there
       for (int j = u.t0 + (int)((grp ^ it0) & 1u); j < u.t1; j += 2) {
         const uint32_t it = it0 + (uint32_t)(j - u.t0);
         const int st = (int)(it % G::kStages);
+        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
+        uint64_t z2[2][kPairs], x2[kPairs];
+        float top[2] = {-INFINITY, -INFINITY}, my[2];
+        bool near = true;
+        if (rows_here) {
         if (!ready && !failed) failed = !wait(bars + 8 * (kLSFull + st), (it / G::kStages) & 1u);
         tc_fence_after();
         uint32_t v[16], lo[16];
         tmem_ld_16x256b_x4(tw + G::kSCol + kLT * grp + kPCols * part, v);
         tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + kLT * grp + kPCols * part, lo);
-        const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
-        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
-        uint64_t s2[kPairs], x2[kPairs];
+        near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
+        uint64_t s2[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           s2[k] = lds_f32x2(sc + 32 * k);
@@ -505,8 +512,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kLSFree + grp));
-        uint64_t z2[2][kPairs];
-        float top[2], my[2] = {m[0], m[1]};
+        my[0] = m[0], my[1] = m[1];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -533,9 +539,12 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
           top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
+        } else if (lane == 0) {
+          mbar_arrive(bars + 8 * (kLSFree + grp));
+        }
         // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
-        const bool x_free = it < 2 || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
-        if (j > u.t0 && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
+        const bool x_free = it < 2 || !rows_here || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
+        if (j > u.t0 && rows_here && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
         float ref[2];
         bool up = false;
 #pragma unroll
@@ -599,7 +608,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         if (!__all_sync(0xFFFFFFFFu, x_free) && !failed)
           failed = !wait(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
         const uint32_t nx = it + 2;  // a look at the next wait, ahead of its time: it takes 150 cycles
-        ready = j + 2 < u.t1 && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
+        ready = j + 2 < u.t1 && rows_here && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
+        if (rows_here) {
         const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -642,6 +652,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             sts_u16(a + kPBytes, rest);
           }
           if (near) l2[i] = fma2(sum, pack2(kTopInv, kTopInv), l2[i]);
+        }
         }
         ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
@@ -733,16 +744,16 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
   } else if (warp == kLdWarpL) {
     // ------------------------------------------------------------ loader
     const LatentLayout lay(p.c);
-    const int gs = lay.G, ng = kLT / gs, tb = 32 / ng;  // groups per tile, tiles per lookup
+    const int gs = lay.G, ngs = __ffs(kLT / gs) - 1, ng = 1 << ngs, tb = 32 >> ngs;  // groups per tile, tiles per lookup
     const uint8_t* pool = static_cast<const uint8_t*>(p.c.data);
     uint32_t it = 0;
     while (!failed && walk.next(u, nullptr)) {
       int64_t off = -1;
       for (int j = u.t0; j < u.t1; ++j, ++it) {
-        const int st = (int)(it % G::kStages), k = (j - u.t0) % tb;
+        const int st = (int)(it % G::kStages), k = (j - u.t0) & (tb - 1);
         if (k == 0) {
-          const int64_t pos = (int64_t)(j + lane / ng) * kLT + lane % ng * gs;
-          off = pos < u.limit && j + lane / ng < u.t1 ? latent_group(p.c, lay, u.b, pos, p.flag) : -1;
+          const int64_t pos = (int64_t)(j + (lane >> ngs)) * kLT + (lane & (ng - 1)) * gs;
+          off = pos < u.limit && j + (lane >> ngs) < u.t1 ? latent_group(p.c, lay, u.b, pos, p.flag) : -1;
           if (off >= 0 && !KVQ_IN(off + lay.group_bytes() <= p.c.num_pages * lay.page_bytes(), p.flag)) off = -1;
         }
         const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (k * ng + lane) & 31);
@@ -825,6 +836,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       const uint64_t dv = smem_desc(sb, 8 * G::kRow, 128);  // channels as rows: MN-major
       const uint64_t dp = smem_desc(sb + G::kP, 1024, 128);
       while (!failed && walk.next(u, nullptr)) {
+        const uint32_t id = kIdO | (uint32_t)((u.rows + 15) / 16 * 2) << 17;
         for (int j = u.t0; j < u.t1; ++j, ++it) {
           if (!wait(bars + 8 * (kLPFull + (it & 1)), (it >> 1) & 1u)) {
             failed = true;
@@ -841,8 +853,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
               for (int s = 0; s < 2; ++s) {  // 32 tokens: four core matrices of the tile, two of x
                 const uint64_t am = a + (uint64_t)((mm * 1024 + s * 32 * G::kRow) >> 4);
-                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)(s * 2048 >> 4), kIdOHi, more || s > 0);
-                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)((s * 2048 + kPBytes) >> 4), kIdOLo, true);
+                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)(s * 2048 >> 4), id, more || s > 0);
+                mma_f8(tmem + G::kOCol + mm * kLRows, am, b + (uint64_t)((s * 2048 + kPBytes) >> 4), id | kIdE5m2, true);
               }
             tc_commit(bars + 8 * (kLEmpty + st));
             tc_commit(bars + 8 * (kLPvDone + (it & 1)));

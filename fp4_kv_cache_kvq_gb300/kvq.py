@@ -439,6 +439,8 @@ def append(cache, start_pos: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """kvq_append: k, v bf16 [batch][n_new][Hkv][head_dim]; start_pos int32 [batch].
     An Fp8BlockCache (kvq_fp8_block_append) also takes new_lens, int32 [batch]:
     sequence b has new_lens[b] <= n_new new tokens."""
+    if isinstance(cache, LatentCache):
+        raise ValueError("a LatentCache is filled by latent_append")
     _need(k, torch.bfloat16, "k")
     _need(v, torch.bfloat16, "v")
     _need(start_pos, torch.int32, "start_pos")

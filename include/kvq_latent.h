@@ -122,11 +122,18 @@ kvq_status kvq_latent_dequant(const kvq_latent_cache *cache, int32_t batch, cons
  *                Both 16-byte aligned.
  *   workspace    kvq_latent_attn_workspace_bytes(...) bytes, 16-byte aligned,
  *                not shared by calls that may overlap.
+ * q enters the products exactly down to 2^-9 of its row's largest element, and
+ * off by at most 2^-17 of that below (2^-110 in rows whose largest is under
+ * 2^-93).  A weight enters the second product times its token's scale, off by at
+ * most 2^-8 of that, or 2^-19 of the largest such product that the row attends.
+ * Sums, softmax statistics and their joins are fp32.
  * A row that attends a token marked as non-finite, or whose query holds an Inf
  * or NaN, is NaN; no other row is touched by either.
  * Device flags: BAD_LENGTH (n_b outside 0..chunk: the sequence is skipped;
  * T_b < n_b, or T_b < 0: its n_b rows are written as 0), PAGE_OOB (the page's
- * tokens are left out), TIMEOUT.
+ * tokens are left out), TIMEOUT (kvq_test_set_wait_limit_ns reaches this call's
+ * waits and kvq_expanded_attn's, too).
+ * Host errors: INVALID_ARGUMENT, WORKSPACE, UNSUPPORTED (2^30 rows and more).
  */
 size_t kvq_latent_attn_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t latent_dim, int32_t chunk);
 kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t num_q_heads, int32_t chunk,
@@ -151,6 +158,12 @@ kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t
  *   max_len      tokens per sequence in k, k_rope and v; positions from T_b on
  *                are not used.
  *   out          device [batch][chunk][num_heads][d] of out_dtype, 16-byte aligned.
+ * q, k and v enter the products as they are; a weight is rounded to bf16, sums and
+ * softmax statistics are fp32.  A row that attends a value that is Inf or NaN is
+ * not finite in its channel; no Inf or NaN among the keys and values behind a
+ * row's position reaches the row.
+ * Host errors: INVALID_ARGUMENT, UNSUPPORTED (2^30 rows and more, max_len above
+ * 2^30).
  * Device flags: BAD_LENGTH (n_b outside 0..chunk, T_b > max_len: the sequence is
  * skipped; T_b < n_b, or T_b < 0: its n_b rows are written as 0), TIMEOUT.
  */
