@@ -25,7 +25,8 @@
 //
 // Work.  A row is a query head of a token; a unit is 64 rows of one sequence and
 // all its positions.  A CTA holds 64 rows: sum^T is 4 accumulators of 128
-// channels x 64 rows (256 TMEM columns at latent_dim 512), q 144 columns, S 64.
+// channels x 64 rows (256 TMEM columns at latent_dim 512), q's latent part 128 columns,
+// S two times 64; q's position part lies in shared memory.
 // Few units: the positions of all sequences, laid end to end, are split evenly over
 // the CTAs, the row tiles of a sequence side by side so that they read the same
 // tile at the same time, and a second launch joins the parts.  Many: a unit per CTA,
@@ -39,6 +40,26 @@
 //             O^T += K(j)^T x(j)      kind::f8f6f4, twice (hi, lo), from another warp:
 //             one's waits do not hold up the other's products
 //   scales    2^e, e and 2^-e of a tile's tokens, once for all rows
+//
+// What bounds it: for 64 rows a tile's products take 1152 cycles of the tensor pipe at its
+// rate, and 1660 as they come: 39 an MMA of the scores (64 columns: the queries' rows are
+// read for half the work), 53 one of the sums (A from shared memory, 4 KB each); its
+// codes, 41 KB, take 1750 from HBM when every SM reads its own.  A tile takes 2000 to
+// 2100: the softmax's chain of loads, exponentials, conversions and waits, in two groups
+// that overlap by half, and the references that some row of 64 raises in every tenth tile
+// (2000 cycles, 11% of a chunk).
+// Measured (TFLOP/s of the absorbed form, 2 (2 L + R) per pair; L 512, R 64, page 64, L2
+// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 2.03 ms, 1079; 64 x 8192
+// positions, 16 heads 95 us, 3.5 TB/s; 16 x 32768, 128 heads 164 us, 892.
+// From 3.71 ms for the chunk: softmax on eight warps instead of four 3.45; a tile's
+// scales prepared by a warp of their own 3.31; MMAs issued by an elected lane 2.53;
+// scores and sums issued by a warp each 2.46; the references' slack 3 -> 6 (E5M2 first
+// over 448) 2.36; two groups of eight, with waits suspended in the barrier instead of
+// polling, 2.07; a wait that is over looked at once 2.03.
+// Slower: A kept in the collector for the second MMA of a pair (the second one's B is then
+// read in the first one's type); waits by one lane of a warp (2.79) or by one warp of a group
+// (2.26); polling 64 times before suspending (3.94); four warps a group 2.35; warps
+// without rows skipped (2.08: the spills cost more).
 #include "kvq_latent.cuh"
 #include "kvq_roles.cuh"
 #include "kvq_tc.cuh"
@@ -482,25 +503,18 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       float m[2] = {-INFINITY, -INFINITY};
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
-      // (a warp without rows keeps step only: the weights that it leaves in x meet columns of O
-      // that nothing reads)
-      const bool rows_here = 16 * quad < u.rows;
       bool ready = false;  // the group's next tile's scores are there
       for (int j = u.t0 + (int)((grp ^ it0) & 1u); j < u.t1; j += 2) {
         const uint32_t it = it0 + (uint32_t)(j - u.t0);
         const int st = (int)(it % G::kStages);
-        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
-        uint64_t z2[2][kPairs], x2[kPairs];
-        float top[2] = {-INFINITY, -INFINITY}, my[2];
-        bool near = true;
-        if (rows_here) {
         if (!ready && !failed) failed = !wait(bars + 8 * (kLSFull + st), (it / G::kStages) & 1u);
         tc_fence_after();
         uint32_t v[16], lo[16];
         tmem_ld_16x256b_x4(tw + G::kSCol + kLT * grp + kPCols * part, v);
         tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + kLT * grp + kPCols * part, lo);
-        near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
-        uint64_t s2[kPairs];
+        const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
+        const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
+        uint64_t s2[kPairs], x2[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           s2[k] = lds_f32x2(sc + 32 * k);
@@ -512,7 +526,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kLSFree + grp));
-        my[0] = m[0], my[1] = m[1];
+        uint64_t z2[2][kPairs];
+        float top[2], my[2] = {m[0], m[1]};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -539,12 +554,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
           top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
-        } else if (lane == 0) {
-          mbar_arrive(bars + 8 * (kLSFree + grp));
-        }
         // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
-        const bool x_free = it < 2 || !rows_here || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
-        if (j > u.t0 && rows_here && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
+        const bool x_free = it < 2 || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
+        if (j > u.t0 && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
         float ref[2];
         bool up = false;
 #pragma unroll
@@ -608,8 +620,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         if (!__all_sync(0xFFFFFFFFu, x_free) && !failed)
           failed = !wait(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
         const uint32_t nx = it + 2;  // a look at the next wait, ahead of its time: it takes 150 cycles
-        ready = j + 2 < u.t1 && rows_here && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
-        if (rows_here) {
+        ready = j + 2 < u.t1 && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
         const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -652,7 +663,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             sts_u16(a + kPBytes, rest);
           }
           if (near) l2[i] = fma2(sum, pack2(kTopInv, kTopInv), l2[i]);
-        }
         }
         ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
