@@ -15,7 +15,7 @@
 //       values hi = RNE(q), lo = RNE(q - hi): exact down to 2^-9 of the row's
 //       largest element, off by at most 2^-17 of it below.  hi and lo are rows of
 //       one operand (128 rows for 64 queries); their scores are added in fp32.
-//   x   reaches 2^5 .. 2^11 in every row and is rounded to f16, then held as a sum of
+//   x   reaches 2^3 .. 2^11 in every row and is rounded to f16, then held as a sum of
 //       an E4M3 and an E5M2 value: first the rounding to E4M3 (to E5M2 over 448, E4M3's
 //       end), then of the rest to the other: off by 2^-8 of x either way, or 2^-14
 //       under 2^-6, where E4M3's steps end and E5M2's range (down to 2^-17) takes
@@ -44,18 +44,17 @@
 // What bounds it: for 64 rows a tile's products take 1152 cycles of the tensor pipe at its
 // rate, and 1660 as they come: 39 an MMA of the scores (64 columns: the queries' rows are
 // read for half the work), 53 one of the sums (A from shared memory, 4 KB each); its
-// codes, 41 KB, take 1750 from HBM when every SM reads its own.  A tile takes 2000 to
-// 2100: the softmax's chain of loads, exponentials, conversions and waits, in two groups
-// that overlap by half, and the references that some row of 64 raises in every tenth tile
-// (2000 cycles, 11% of a chunk).
+// codes, 41 KB, take 1750 from HBM when every SM reads its own.  A tile takes 1900: the
+// softmax's chain of loads, exponentials, conversions and waits, in two groups that
+// overlap by half.
 // Measured (TFLOP/s of the absorbed form, 2 (2 L + R) per pair; L 512, R 64, page 64, L2
-// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 2.03 ms, 1079; 64 x 8192
-// positions, 16 heads 95 us, 3.5 TB/s; 16 x 32768, 128 heads 164 us, 892.
+// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.85 ms, 1184; 64 x 8192
+// positions, 16 heads 92 us, 3.7 TB/s; 16 x 32768, 128 heads 155 us, 943.
 // From 3.71 ms for the chunk: softmax on eight warps instead of four 3.45; a tile's
 // scales prepared by a warp of their own 3.31; MMAs issued by an elected lane 2.53;
 // scores and sums issued by a warp each 2.46; the references' slack 3 -> 6 (E5M2 first
 // over 448) 2.36; two groups of eight, with waits suspended in the barrier instead of
-// polling, 2.07; a wait that is over looked at once 2.03.
+// polling, 2.07; a wait that is over looked at once 2.03; references set ahead 1.85.
 // Slower: A kept in the collector for the second MMA of a pair (the second one's B is then
 // read in the first one's type); waits by one lane of a warp (2.79) or by one warp of a group
 // (2.26); polling 64 times before suspending (3.94); four warps a group 2.35; warps
@@ -82,6 +81,11 @@ constexpr int kMinTiles = 2;           // least tiles of a split range
 // that rescales O (a slack of 3: among 64 rows some raised its own in every second
 // tile, 1100 cycles each).
 constexpr float kTop = 5.0f, kSlackL = 6.0f, kTopInv = 1.0f / 32.0f;
+// Where both halves of the tile that raises a reference hold products within 2^kNearL of
+// each other, it is set 2^kAhead higher: larger ones will follow (chunk 2.03 -> 1.85 ms).  A
+// single large one in one half is more likely the largest of all, and leaves the small
+// ones beside it their distance to the end of E5M2.
+constexpr float kNearL = 4.0f, kAhead = 2.0f;
 constexpr float kE4m3End = 8.80f;  // a little under log2 448
 
 enum : int {
@@ -581,7 +585,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float* x = shared + (kParts + 2 * grp) * kLRows + lr[i];
-            const float all = fmaxf(x[0], x[kLRows]), to = all > ref[i] + kSlackL ? floorf(all) : ref[i];
+            const float all = fmaxf(x[0], x[kLRows]), other = fminf(x[0], x[kLRows]);
+            const float ahead = other > all - kNearL ? kAhead : 0.0f;
+            const float to = all > ref[i] + kSlackL ? floorf(all) + ahead : ref[i];
             if (t == 0 && part == 0) {
               alpha[grp * kLRows + lr[i]] = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
               ref_s[lr[i]] = to;

@@ -125,7 +125,7 @@ kvq_status kvq_latent_dequant(const kvq_latent_cache *cache, int32_t batch, cons
  * q enters the products exactly down to 2^-9 of its row's largest element, and
  * off by at most 2^-17 of that below (2^-110 in rows whose largest is under
  * 2^-93).  A weight enters the second product times its token's scale, off by at
- * most 2^-8 of that, or 2^-19 of the largest such product that the row attends.
+ * most 2^-8 of that, or 2^-17 of the largest such product that the row attends.
  * Sums, softmax statistics and their joins are fp32.
  * A row that attends a token marked as non-finite, or whose query holds an Inf
  * or NaN, is NaN; no other row is touched by either.

@@ -5,11 +5,11 @@ include/kvq_latent.h.  Nothing here uses the CUDA library.
 Bounds count the roundings of the attention kernels, row by row.
   latent (attn_bound)
     weights  x = weight * value scale over a power of two, the row's largest x between
-             2^5 and 2^11, rounded to f16 (2^-11 relative), then held as an E4M3 and an
+             2^3 and 2^11, rounded to f16 (2^-11 relative), then held as an E4M3 and an
              E5M2 value, one the rounding of x, the other of the rest: off by half a step of
              the rest's rounding, 2^-8 of x (of x in [1, 2) the rest behind E4M3 is at most
              2^-4 and E5M2's half step there 2^-8; behind E5M2, over 448, 2^-3 and 2^-8),
-             or 2^-14 where x is under 2^-6 (E4M3's steps end at 2^-9), which is 2^-19 of
+             or 2^-14 where x is under 2^-6 (E4M3's steps end at 2^-9), which is 2^-17 of
              the row's largest.  It reaches the result times the value's code.
     scores   q is scaled to 2^7 .. 2^8 and held in two E4M3 parts: off by at most
              2^-17 of the row's largest element; (w + 8) half steps of fp32 of the
@@ -133,8 +133,8 @@ def attn_bound(q, c, k, s, p, scale, out=torch.float32, ref=None):
     top = prod.amax(-1, keepdim=True)
     total = p @ c.abs()
     e = total * (2.0 ** -8 + 2.0 ** -11 + (2 * math.log(2) * score + T / 16 * 2.0 ** -24 + 2.0 ** -20)[..., None])
-    small = seen & (prod < 2.0 ** -11 * top)
-    e = e + 2.0 ** -19 * top * (small.double() @ (c.abs() / s[:, None]))
+    small = seen & (prod < 2.0 ** -9 * top)
+    e = e + 2.0 ** -17 * top * (small.double() @ (c.abs() / s[:, None]))
     return _finish(e, out, ref)
 
 
