@@ -10,8 +10,6 @@
 // query head.
 #include "kvq_latent.cuh"
 
-#include <cuda_bf16.h>
-
 namespace kvq {
 namespace {
 
@@ -49,7 +47,12 @@ __device__ __forceinline__ int new_tokens(const LatentAppendParams& p, int b, in
   return n;
 }
 
-__device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+// Two fp32 values rounded to bf16 (lo in the low half).
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 // Eight cosines, then eight sines, `half` behind them in the table's row.
 __device__ __forceinline__ void load_angles(const float* row, int half, float (&cs)[16]) {
@@ -74,9 +77,9 @@ __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[16
     for (int i = 0; i < 4; ++i) {
       float y0, y1;
       turn(bf16_lo(wa[i]), bf16_hi(wa[i]), i, y0, y1);
-      wa[i] = bf16_bits(y0) | bf16_bits(y1) << 16;
+      wa[i] = bf16x2_rn(y0, y1);
       turn(bf16_lo(wb[i]), bf16_hi(wb[i]), 4 + i, y0, y1);
-      wb[i] = bf16_bits(y0) | bf16_bits(y1) << 16;
+      wb[i] = bf16x2_rn(y0, y1);
     }
   } else {
 #pragma unroll
@@ -84,8 +87,8 @@ __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[16
       float u0, u1, v0, v1;
       turn(bf16_lo(wa[i]), bf16_lo(wb[i]), 2 * i, u0, u1);
       turn(bf16_hi(wa[i]), bf16_hi(wb[i]), 2 * i + 1, v0, v1);
-      wa[i] = bf16_bits(u0) | bf16_bits(v0) << 16;
-      wb[i] = bf16_bits(u1) | bf16_bits(v1) << 16;
+      wa[i] = bf16x2_rn(u0, v0);
+      wb[i] = bf16x2_rn(u1, v1);
     }
   }
   a = make_uint4(wa[0], wa[1], wa[2], wa[3]);
@@ -284,7 +287,7 @@ __device__ __forceinline__ void store16(float* dst, const float (&x)[16]) {
 __device__ __forceinline__ void store16(uint16_t* dst, const float (&x)[16]) {
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = bf16_bits(x[2 * i]) | bf16_bits(x[2 * i + 1]) << 16;
+  for (int i = 0; i < 8; ++i) w[i] = bf16x2_rn(x[2 * i], x[2 * i + 1]);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
