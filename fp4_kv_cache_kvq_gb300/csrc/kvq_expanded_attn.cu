@@ -547,7 +547,7 @@ extern "C" kvq_status kvq_expanded_attn(int32_t batch, int32_t num_heads, int32_
                                         int64_t v_head_stride, float softmax_scale, void* out, int32_t out_dtype,
                                         int32_t* d_err_flag, kvq_stream stream) {
   if (batch < 0 || num_heads < 1 || chunk < 0 || max_len < 0 || (head_dim != 64 && head_dim != 128) ||
-      rope_dim != kERope || !(softmax_scale > 0.0f) || !(softmax_scale < INFINITY) ||
+      rope_dim != kERope || !(softmax_scale > 0.0f) || !(softmax_scale < 2.0e38f) ||
       (out_dtype != KVQ_DTYPE_F32 && out_dtype != KVQ_DTYPE_BF16))
     return KVQ_ERR_INVALID_ARGUMENT;
   if (batch == 0 || chunk == 0) return KVQ_OK;

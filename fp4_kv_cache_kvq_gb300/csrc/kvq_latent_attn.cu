@@ -1075,7 +1075,7 @@ extern "C" kvq_status kvq_latent_attn(const kvq_latent_cache* cache, int32_t bat
                                       const int32_t* d_seq_lens, const int32_t* d_chunk_lens, const void* q,
                                       float softmax_scale, void* out, int32_t out_dtype, void* workspace,
                                       size_t workspace_bytes, int32_t* d_err_flag, kvq_stream stream) {
-  if (batch < 0 || num_q_heads < 1 || chunk < 0 || !(softmax_scale > 0.0f) || !(softmax_scale < INFINITY) ||
+  if (batch < 0 || num_q_heads < 1 || chunk < 0 || !(softmax_scale > 0.0f) || !(softmax_scale < 2.0e38f) ||
       (out_dtype != KVQ_DTYPE_F32 && out_dtype != KVQ_DTYPE_BF16))
     return KVQ_ERR_INVALID_ARGUMENT;
   const kvq_status st = check_latent_cache(cache, batch);

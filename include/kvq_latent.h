@@ -123,8 +123,8 @@ kvq_status kvq_latent_dequant(const kvq_latent_cache *cache, int32_t batch, cons
  *   workspace    kvq_latent_attn_workspace_bytes(...) bytes, 16-byte aligned,
  *                not shared by calls that may overlap.
  * q enters the products exactly down to 2^-9 of its row's largest element, and
- * off by at most 2^-17 of that below (2^-110 in rows whose largest is under
- * 2^-93).  A weight enters the second product times its token's scale, off by at
+ * off by at most 2^-17 of that below (2^-136 in rows whose largest is under
+ * 2^-119).  A weight enters the second product times its token's scale, off by at
  * most 2^-8 of that, or 2^-17 of the largest such product that the row attends.
  * Sums, softmax statistics and their joins are fp32.
  * A row that attends a token marked as non-finite, or whose query holds an Inf
