@@ -627,11 +627,15 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           failed = !wait(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
         const uint32_t nx = it + 2;  // a look at the next wait, ahead of its time: it takes 150 cycles
         ready = j + 2 < u.t1 && wait.over(bars + 8 * (kLSFull + nx % G::kStages), (nx / G::kStages) & 1u);
-        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
+        // (all of a thread's loads, then its arithmetic, then its stores: they keep their order, and
+        // one pair after the other would wait for each one's chain of conversions)
+        uint64_t inv2[kPairs];
+        uint32_t w[2][kPairs];  // first part | second part << 16
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) inv2[k] = lds_f32x2(sc + 8 * kLT + 32 * k);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
-          const uint32_t at = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16);
           const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448: E5M2 first
           if (near) {
             const float a = m[i] == ref[i] ? 1.0f : fast_exp2(m[i] - ref[i]);  // raised since the group's last tile
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           for (int k = 0; k < kPairs; ++k) {
             const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
-            sum = fma2(pack2(xa, xb), lds_f32x2(sc + 8 * kLT + 32 * k), sum);
+            sum = fma2(pack2(xa, xb), inv2[k], sum);
             const uint32_t h = pack_f16x2(xa, xb);
             uint32_t hi = e4m3x2_of_f16x2(h);
             uint32_t rest = e5m2x2_of_f16x2(hsub2(h, f16x2_from_e4m3x2(hi)));
@@ -664,12 +668,19 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               hi = (hi & ~over) | (q & over);
               rest = (rest & ~over) | (r & over);
             }
-            const uint32_t a = at + (uint32_t)((k >> 1) * 1024 + (k & 1) * 8);
-            sts_u16(a, hi);
-            sts_u16(a + kPBytes, rest);
+            w[i][k] = hi | rest << 16;
           }
           if (near) l2[i] = fma2(sum, pack2(kTopInv, kTopInv), l2[i]);
         }
+        const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < kPairs; ++k) {
+            const uint32_t a = pb + (uint32_t)((lr[i] >> 3) * 128 + (lr[i] & 7) * 16 + (k >> 1) * 1024 + (k & 1) * 8);
+            sts_u16(a, w[i][k]);
+            sts_u16(a + kPBytes, w[i][k] >> 16);
+          }
         ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
         __syncwarp();
