@@ -561,15 +561,14 @@ def _row_strides(dev: int, t: torch.Tensor, name: str, heads: bool):
     shape = t.shape
     if t.dtype is not torch.bfloat16 or t.get_device() != dev or len(shape) != (4 if heads else 3):
         raise ValueError(f"{name} must be a bfloat16 tensor [batch, n, {'heads, ' if heads else ''}width] on cuda:{dev}")
-    B, n, H, w = shape if heads else (shape[0], shape[1], 1, shape[2])
-    if t.is_contiguous():
-        return H * w, w, shape
-    st = t.stride()
-    sb, sn, sh, sw = st if heads else (st[0], st[1], w, st[2])
+    if heads:
+        (B, n, H, w), (sb, sn, sh, sw) = shape, t.stride()
+    else:
+        (B, n, w), (sb, sn, sw), H, sh = shape, t.stride(), 1, shape[2]
     if H == 1:
         sh = w
     step = sn if n > 1 else sb if B > 1 else H * max(sh, w)
-    if t.numel() and not (sw == 1 and sh >= w and step >= (H - 1) * sh + w and (n == 1 or B == 1 or sb == n * sn)):
+    if (sw != 1 or sh < w or step < (H - 1) * sh + w or (n > 1 and B > 1 and sb != n * sn)) and t.numel():
         raise ValueError(f"{name}: rows must be contiguous, heads and tokens evenly spaced and without overlap")
     return step, sh, shape
 
