@@ -45,11 +45,10 @@
 // rate, and 1660 as they come: 39 an MMA of the scores (64 columns: the queries' rows are
 // read for half the work), 53 one of the sums (A from shared memory, 4 KB each); its
 // codes, 41 KB, take 1750 from HBM when every SM reads its own.  A tile takes 1900.  In
-// copies with a part left out the chunk takes, of 1.85 ms: 1.74 without the group's vote
-// on raising, 1.70 without the hand-over of the references either; 1.81 without the
-// conversions to 8 bits, 1.83 without the exponentials or the stores: what is left is
-// the products.  The batch of 16 heads stays where it is in each of these: a third of
-// its time is start, change of unit, end and join.
+// copies with arithmetic left out the chunk takes, of 1.85 ms, 1.81 without the
+// conversions to 8 bits, 1.83 without the exponentials or the stores: the products, and
+// the hand-offs between the groups, are what is left.  The batch of 16 heads stays where
+// it is in each of these: a third of its time is start, change of unit, end and join.
 // Measured (TFLOP/s of the absorbed form, 2 (2 L + R) per pair; L 512, R 64, page 64, L2
 // flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.85 ms, 1184; 64 x 8192
 // positions, 16 heads 92 us, 3.7 TB/s; 16 x 32768, 128 heads 155 us, 943.
