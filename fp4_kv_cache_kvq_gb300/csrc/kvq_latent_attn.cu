@@ -45,18 +45,19 @@
 // rate, and 1660 as they come: 39 an MMA of the scores (64 columns: the queries' rows are
 // read for half the work), 53 one of the sums (A from shared memory, 4 KB each); its
 // codes, 41 KB, take 1750 from HBM when every SM reads its own.  A tile takes 1900.  In
-// copies with arithmetic left out the chunk takes, of 1.85 ms, 1.81 without the
+// copies with arithmetic left out the chunk took, of 1.85 ms, 1.81 without the
 // conversions to 8 bits, 1.83 without the exponentials or the stores: the products, and
 // the hand-offs between the groups, are what is left.  The batch of 16 heads stays where
 // it is in each of these: a third of its time is start, change of unit, end and join.
 // Measured (TFLOP/s of the absorbed form, 2 (2 L + R) per pair; L 512, R 64, page 64, L2
-// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.85 ms, 1184; 64 x 8192
-// positions, 16 heads 92 us, 3.7 TB/s; 16 x 32768, 128 heads 155 us, 943.
+// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.81 ms, 1210; 64 x 8192
+// positions, 16 heads 91 us, 3.7 TB/s; 16 x 32768, 128 heads 151 us, 968.
 // From 3.71 ms for the chunk: softmax on eight warps instead of four 3.45; a tile's
 // scales prepared by a warp of their own 3.31; MMAs issued by an elected lane 2.53;
 // scores and sums issued by a warp each 2.46; the references' slack 3 -> 6 (E5M2 first
 // over 448) 2.36; two groups of eight, with waits suspended in the barrier instead of
-// polling, 2.07; a wait that is over looked at once 2.03; references set ahead 1.85.
+// polling, 2.07; a wait that is over looked at once 2.03; references set ahead 1.85;
+// a row's references settled by its own two warps, O rescaled after the weights 1.81.
 // Slower: A kept in the collector for the second MMA of a pair (the second one's B is then
 // read in the first one's type); waits by one lane of a warp (2.79) or by one warp of a group
 // (2.26); polling 64 times before suspending (3.94); four warps a group 2.35; warps
@@ -95,8 +96,8 @@ enum : int {
   kLEmpty = kLFull + 8,     // [stages] the tile's sums done (commit)
   kLSFull = kLEmpty + 8,    // [stages] S in TMEM (commit), and the tile's scales ready
   kLSFree = kLSFull + 8,    // [2] S taken by the group's warps
-  kLRef = kLSFree + 2,      // [2] the references that hold from a tile on
-  kLQFull = kLRef + 2,      // q in TMEM and shared memory
+  kLRef = kLSFree + 2,      // [2][4] the references of a quarter's rows that hold from a tile on
+  kLQFull = kLRef + 8,      // q in TMEM and shared memory
   kLPFull = kLQFull + 1,    // [2] x in shared memory, O rescaled
   kLPvDone = kLPFull + 2,   // [2] O += done
   kLDrain = kLPvDone + 2,   // the last commits of the two issuing warps
@@ -131,8 +132,8 @@ struct LGeo {
   static constexpr int kExp = kQr + 128 * R;              // [stages][64]
   static constexpr int kMask = kExp + kStages * kLT;      // [stages] valid tokens, 64 bits
   static constexpr int kRefS = kMask + 8 * 8;             // [64] the rows' references
-  static constexpr int kAlpha = kRefS + 4 * kLRows;       // [2][64] factors of O's columns: a group's, or the result's two
-  static constexpr int kShare = kAlpha + 2 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
+  static constexpr int kAlpha = kRefS + 4 * kLRows;       // [2][2][64] factors of O's columns, by group and tile; the result's two
+  static constexpr int kShare = kAlpha + 4 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
   static constexpr int kSc = kShare + 2 * kParts * 4 * kLRows;  // [stages][3][64] 2^e, e (-inf: no token), 2^-e
   static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40
   static constexpr int kBar = kNear + 4 * 8;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     mbar_init(bars + 8 * kLQFull, kLSmWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (kLSFree + i), kLSmWarps / 2);
-      mbar_init(bars + 8 * (kLRef + i), kLSmWarps / 2);
+      for (int k = 0; k < 4; ++k) mbar_init(bars + 8 * (kLRef + 4 * i + k), 2);
       mbar_init(bars + 8 * (kLPFull + i), kLSmWarps / 2);
       mbar_init(bars + 8 * (kLPvDone + i), 1);
     }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     // warp w: rows 16 (w & 3) .. + 15, whose scores lie in its 32 TMEM lanes; of every
     // second tile (w >> 3) the positions 32 (w >> 2 & 1) .. + 31
     const int g = lane >> 2, t = lane & 3, quad = warp & 3, share = warp >> 2, part = share & 1;
-    const uint32_t grp = (uint32_t)share >> 1, bar_g = 2 + grp;
+    const uint32_t grp = (uint32_t)share >> 1, bar_g = 2 + grp, bar_r = 4 + 4 * grp + quad;  // named barriers: the group's, a row's two warps'
     const uint32_t tw = tmem + ((uint32_t)(32 * quad) << 16);
     const int lr[2] = {16 * quad + g, 16 * quad + g + 8};
     float* ref_s = reinterpret_cast<float*>(base + G::kRefS);
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
         // (waits that are over are known to be by the time they are due: a look takes 150 cycles)
         const bool x_free = it < 2 || wait.over(bars + 8 * (kLPvDone + grp), ((it >> 1) - 1) & 1u);
-        if (j > u.t0 && !failed) failed = !wait(bars + 8 * (kLRef + (grp ^ 1)), ((it - 1) >> 1) & 1u);
+        if (j > u.t0 && !failed) failed = !wait(bars + 8 * (kLRef + 4 * (grp ^ 1) + quad), ((it - 1) >> 1) & 1u);
         float ref[2];
         bool up = false;
 #pragma unroll
@@ -572,57 +573,30 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
           up |= top[i] > ref[i] + kSlackL;
         }
-        if (failed) gave_up[it >> 1 & 1] = 1;
-        if (softmax_or(bar_g, kGroupThreads, up || failed)) {
-          if (gave_up[it >> 1 & 1]) {
-            failed = true;
-            break;
-          }
-          // raise the references of the rows that need it (what a row gives does not depend on
-          // others); O's columns follow (none at the unit's first tile)
+        // raise the references of the rows that need it (what a row gives does not depend on
+        // others); a row's two warps agree, the other group's wait for them
+        float* fac = alpha + (2 * grp + (it >> 1 & 1)) * kLRows;
+        float a2[2] = {1.0f, 1.0f};
+        const bool raised = softmax_or(bar_r, 64, up);
+        if (raised) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (t == 0) own[kParts * kLRows + lr[i]] = top[i];
-          named_barrier_sync(bar_g, kGroupThreads);
+          named_barrier_sync(bar_r, 64);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float* x = shared + (kParts + 2 * grp) * kLRows + lr[i];
             const float all = fmaxf(x[0], x[kLRows]), other = fminf(x[0], x[kLRows]);
             const float ahead = other > all - kNearL ? kAhead : 0.0f;
             const float to = all > ref[i] + kSlackL ? floorf(all) + ahead : ref[i];
-            if (t == 0 && part == 0) {
-              alpha[grp * kLRows + lr[i]] = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
-              ref_s[lr[i]] = to;
-            }
+            a2[i] = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
+            if (t == 0 && part == 0) ref_s[lr[i]] = to;
             ref[i] = to;
           }
-          named_barrier_sync(bar_g, kGroupThreads);
-          if (lane == 0) mbar_arrive(bars + 8 * (kLRef + grp));
-          if (j > u.t0) {
-            failed = !wait(bars + 8 * (kLPvDone + (grp ^ 1)), ((it - 1) >> 1) & 1u);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 2 * kM; ++c) {
-              uint32_t o[16];
-              const int col = 32 * part + 16 * (c & 1);
-              const uint32_t at = tw + G::kOCol + kLRows * (c >> 1) + col;
-              tmem_ld16(at, o);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(alpha + grp * kLRows + col + 4 * k);
-                o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
-                o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
-                o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
-                o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * a.w);
-              }
-              tmem_st16_async(at, o);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        } else if (lane == 0) {
-          mbar_arrive(bars + 8 * (kLRef + grp));
         }
+        if (t == 0 && part == 0) fac[lr[0]] = a2[0], fac[lr[1]] = a2[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kLRef + 4 * grp + quad));
         // x in two parts to shared memory, [16 tokens][8 rows] core matrices, once the sums
         // of the tile before last have read theirs
         if (!__all_sync(0xFFFFFFFFu, x_free) && !failed)
@@ -685,6 +659,37 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           }
         ready = __all_sync(0xFFFFFFFFu, ready);
         fence_async_smem();
+        // O's columns follow (none at the unit's first tile): all warps, since each holds a
+        // quarter of the channels
+        if (failed) gave_up[it >> 1 & 1] = 1;
+        if (softmax_or(bar_g, kGroupThreads, raised || failed)) {
+          if (gave_up[it >> 1 & 1]) {
+            failed = true;
+            break;
+          }
+          if (j > u.t0) {
+            failed = !wait(bars + 8 * (kLPvDone + (grp ^ 1)), ((it - 1) >> 1) & 1u);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 2 * kM; ++c) {
+              uint32_t o[16];
+              const int col = 32 * part + 16 * (c & 1);
+              const uint32_t at = tw + G::kOCol + kLRows * (c >> 1) + col;
+              tmem_ld16(at, o);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(fac + col + 4 * k);
+                o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * a.x);
+                o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * a.y);
+                o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * a.z);
+                o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * a.w);
+              }
+              tmem_st16_async(at, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
         __syncwarp();
         if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + grp));
       }
