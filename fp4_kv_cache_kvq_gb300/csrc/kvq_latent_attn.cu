@@ -135,7 +135,7 @@ struct LGeo {
   static constexpr int kAlpha = kRefS + 4 * kLRows;       // [2][2][64] factors of O's columns, by group and tile; the result's two
   static constexpr int kShare = kAlpha + 4 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
   static constexpr int kSc = kShare + 2 * kParts * 4 * kLRows;  // [stages][3][64] 2^e, e (-inf: no token), 2^-e
-  static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40
+  static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40, up to this tile
   static constexpr int kBar = kNear + 4 * 8;
   static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, the groups' [2][2]
   static constexpr int kUsed = kMisc + 32 + 128;
@@ -456,7 +456,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       named_barrier_sync(1, kLSoftmax);
       float xs[2];      // S to log2 units, before the token's scale
       int64_t last[2];  // last position that the row attends
-      bool plain = true;  // the short form of the sums has the range it needs
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float* ams = shared + lr[i];
@@ -505,8 +504,10 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       if (lane == 0) mbar_arrive(bars + 8 * kLQFull);
 
       // l counts 2^(y - m).  Short form: m is ref, and 2^(y - ref) is x 2^-e.  That would lose
-      // what scales far apart leave under fp32's range: from a tile with a scale outside
-      // 2^-40 .. 2^40 on, m is the thread's own largest y, with exponentials of its own.
+      // what scales far apart leave under fp32's range: from the unit's first tile with a
+      // scale outside 2^-40 .. 2^40 on, m is the thread's own largest y, with exponentials of
+      // its own; in both groups, whichever has that tile, since it raises the references that
+      // they share, and over such a one a sum in the short form would become 0.
       float m[2] = {-INFINITY, -INFINITY};
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         uint32_t v[16], lo[16];
         tmem_ld_16x256b_x4(tw + G::kSCol + kLT * grp + kPCols * part, v);
         tmem_ld_16x256b_x4(tw + (16u << 16) + G::kSCol + kLT * grp + kPCols * part, lo);
-        const bool near = plain = plain && near_s[st] != 0;  // (the long form up to the unit's end)
+        const bool near = near_s[st] != 0;  // (the long form up to the unit's end)
         const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 4 * (kPCols * part + 2 * t));
         uint64_t s2[kPairs], x2[kPairs];
 #pragma unroll
@@ -907,6 +908,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     // ------------------------------------------------------------ scales
     uint32_t it = 0;
     while (!failed && walk.next(u, nullptr)) {
+      bool near = true;  // the unit's tiles so far
       for (int j = u.t0; j < u.t1; ++j, ++it) {
         const int st = (int)(it % G::kStages);
         if (!wait(bars + 8 * (kLFull + st), (it / G::kStages) & 1u)) {
@@ -917,7 +919,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         const uint32_t sc = sb + G::kSc + (uint32_t)(st * 3 * 4 * kLT + 8 * lane);
         const uint32_t e2 = lds16(sb + G::kExp + st * kLT + 2 * lane);
         float s[2], x[2], inv[2];
-        bool near = true;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t e = i ? e2 >> 8 : e2 & 0xFFu;
