@@ -6,8 +6,11 @@
 //   y = softmax_scale log2 e (q[:d] . k + q[d:] . k_rope),  P = 2^(y - m),
 //   out = sum P v / sum P.
 // q, k and v enter the products as they are (bf16); P is rounded to bf16, which has
-// fp32's range, so the reference m of a row is raised only when a score passes it by
-// 2^kSlackE; sums, maxima and accumulators are fp32.
+// fp32's range; sums, maxima and accumulators are fp32.  The reference m of a row is raised
+// only when a score passes the one it was set by by more than kSlackE, and lies so far over
+// that one that no sum of the unit's P reaches past 1: 8 for the slack and log2 of the
+// positions.  So sum P v stays within fp32's range for every finite v (the largest bf16 values
+// leave no factor at all), at the other end's cost: products under 2^-126 are lost.
 //
 // What bounds it: the tensor pipe, 2 (2 d + 64) flop per attended pair and head; a
 // unit's tiles come from L2, 51 KB per 80 positions at d = 128.
@@ -45,7 +48,7 @@ constexpr int kERope = 64;
 constexpr int kESoftmax = 8, kELoad = kESoftmax, kEMma = kELoad + 1, kEValues = kEMma + 2, kEThreads = 32 * (kEValues + 1);
 constexpr int kQSlab = kERows * 128, kTSlab = kET * 128;  // 64 channels of a query tile, of a tile
 constexpr int kHeadsAtOnce = 16;
-constexpr float kSlackE = 20.0f;
+constexpr float kSlackE = 8.0f;
 
 enum : int {
   kEQ = 0,              // queries landed
@@ -224,6 +227,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     const uint32_t s_col = tw + G::kSCol + x * kET, p_col = tw + G::kPCol + x * (kET / 2), o_col = tw + x * D;
     const int ntx = x < nx ? tiles_of(x) : 0;
     const int last = first + i, all = first + kERows * x;  // last position of the row, of every row
+    const float count = (float)(32 - __clz(first + rows - 1)), room = count + kSlackE;  // log2 of the positions, rounded up
     float ref = -INFINITY;
     uint64_t l2 = 0ull;
     bool ok = true;
@@ -255,9 +259,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
       // the sums of the tile before: done with O and P
       if (j > 0 && !(ok = wait(bars + 8 * (kEPvDone + x), (j - 1) & 1u))) break;
       tc_fence_after();
-      const bool up = top > ref + kSlackE;
+      const bool up = top > ref - count;
       if (__any_sync(0xFFFFFFFFu, up)) {
-        const float to = up ? top : ref, a = up ? fast_exp2(ref - to) : 1.0f;
+        const float to = up ? top + room : ref, a = up ? fast_exp2(ref - to) : 1.0f;
         l2 = mul2(l2, pack2(a, a));
         ref = to;
         if (j > 0) {

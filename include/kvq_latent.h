@@ -159,7 +159,9 @@ kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t
  *                are not used.
  *   out          device [batch][chunk][num_heads][d] of out_dtype, 16-byte aligned.
  * q, k and v enter the products as they are; a weight is rounded to bf16, sums and
- * softmax statistics are fp32.  A row that attends a value that is Inf or NaN is
+ * softmax statistics are fp32.  Finite values up to bf16's largest do not overflow a sum;
+ * products of a weight and a value that are under fp32's normal range are lost, which is
+ * less than T_b^2 2^-117 in a result.  A row that attends a value that is Inf or NaN is
  * not finite in its channel; no Inf or NaN among the keys and values behind a
  * row's position reaches the row.
  * Host errors: INVALID_ARGUMENT, UNSUPPORTED (2^30 rows and more, max_len above
