@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     if (ok && ntx > 0 && (ok = wait(bars + 8 * (kEPvDone + x), (ntx - 1) & 1u))) {
       tc_fence_after();
       const float2 ll = unpack2(l2);
-      const float l = ll.x + ll.y, f = l == 0.0f ? 0.0f : 1.0f / l;
+      const float l = ll.x + ll.y, f = 1.0f / l;  // (l is 0 where every score is -Inf: 0 * Inf, a row of NaN)
       const int64_t o = (row0 + (int64_t)i * p.heads) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
         tmem_ld32(o_col + c, w);
         if (i < rows) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(w[k]) * f);
+          for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
           if (*reinterpret_cast<volatile uint32_t*>(misc + 2)) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)

@@ -163,7 +163,7 @@ kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t
  * products of a weight and a value that are under fp32's normal range are lost, which is
  * less than T_b^2 2^-117 in a result.  A row that attends a value that is Inf or NaN is
  * not finite in its channel; no Inf or NaN among the keys and values behind a
- * row's position reaches the row.
+ * row's position reaches the row.  A row whose scores are all -Inf is NaN.
  * Host errors: INVALID_ARGUMENT, UNSUPPORTED (2^30 rows and more, max_len above
  * 2^30).
  * Device flags: BAD_LENGTH (n_b outside 0..chunk, T_b > max_len: the sequence is

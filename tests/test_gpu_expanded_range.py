@@ -1,5 +1,8 @@
 """kvq_expanded_attn at the ends of its values' range, against float64: values up to the largest
-bf16 under weights that are equal or rise along the positions, and small values."""
+bf16 under weights that are equal or rise along the positions, small values, and rows
+all of whose scores are -Inf."""
+import math
+
 import pytest
 import torch
 
@@ -79,3 +82,22 @@ def test_small_values_keep_their_precision():
     row's largest score (8 for the room above it, 9 for 300 positions): under T 2^(17 - 126)."""
     T = 300
     run(T, T, 2, 128, torch.linspace(0.0, 4.0, T, device="cuda"), _values(T, 2, 128, 1e-26, 4), extra=T * 2.0 ** -109)
+
+
+def test_rows_whose_scores_are_all_minus_inf():
+    """0 / 0 by the definition: NaN, not 0; rows that see one finite score take its weight."""
+    T, d, H = 200, 64, 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.zeros((1, T, H, d + R), dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    k = torch.zeros((1, T, H, d), dtype=BF, device="cuda")
+    k[0, :90, 1, 0] = -math.inf
+    kr = torch.zeros((1, T, R), dtype=BF, device="cuda")
+    v = torch.randn((1, T, H, d), generator=g, device="cuda").to(BF)
+    out = kvq.expanded_attn(q, k, kr, v, _ints([T]), 1.0)[0]
+    assert torch.isnan(out[:90, 1]).all()
+    assert torch.isfinite(out[:, 0]).all() and torch.isfinite(out[90:, 1]).all()
+    vv = v[0, :, 1].double()
+    for i in range(90, T):
+        want, size = vv[90:i + 1].mean(0), vv[90:i + 1].abs().mean(0)
+        assert ((out[i, 1].double() - want).abs() <= size * (2.0 ** -8 + 2.0 ** -18)).all(), i
