@@ -982,7 +982,7 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParam
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (w[k] == -INFINITY || (k == 1 && i + 4 >= rec.y)) continue;  // (a part without weight left no result)
-      const float x = fast_exp2(w[k] - mm);
+      const float x = fast_exp2(w[k] - mm) * (1.0f / 256.0f);  // (fewer parts than 256: sum x o stays in fp32 for any o)
       l += x;
 #pragma unroll
       for (int c = 0; c < L / 128; ++c) {
