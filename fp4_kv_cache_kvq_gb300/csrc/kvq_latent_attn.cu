@@ -898,8 +898,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         }
       }
     }
-    // no product outlives the CTA
-    if (lane == 0) tc_commit(bars + 8 * kLDrain);
+    // no product outlives the CTA (a commit covers its own thread's, so the lane that issued them makes it)
+    __syncwarp();
+    if (elect_one_of_warp()) tc_commit(bars + 8 * kLDrain);
     __syncwarp();
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait_hint(bars + 8 * kLDrain, 0u, 20000u) && global_ns() - t0 < 20000000ull) {
