@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       it0 += (uint32_t)(u.t1 - u.t0);
       if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it0 - 1) & 1)), ((it0 - 1) >> 1) & 1u);
       if (softmax_or(1, kLSoftmax, failed)) {
-        failed = true;
+        failed = true;  // (in every softmax warp)
         break;
       }
       tc_fence_after();
@@ -775,6 +775,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       }
       tc_fence_before();
       named_barrier_sync(1, kLSoftmax);  // alpha and what the halves exchanged are free again
+    }
+    // after a wait that gave up the walk ends without work: the join reads the record of each
+    // unit, which next() writes, and each part's sum of weights (of an empty one no result)
+    if (failed) {
+      do {
+        if (!u.whole && tid < kLRows) p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + tid] = -INFINITY;
+      } while (walk.next(u, tid == 0 ? p.flag : nullptr));
     }
   } else if (warp == kLdWarpL) {
     // ------------------------------------------------------------ loader
@@ -961,7 +968,10 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParam
   grid_dependency_wait();
   if (n < 0 || n > p.chunk || (int64_t)rt * kLRows + r >= (int64_t)n * p.hq) return;
   const int2 rec = p.rec[unit];
-  if (rec.y <= 1 || !KVQ_IN(rec.x >= 0 && (int64_t)rec.x + (int64_t)(rec.y - 1) * p.tpb < (int64_t)p.groups * p.tpb, p.flag)) return;
+  // (looked at in every build: the record is in the caller's memory, and all reads go by it)
+  const int ctas = p.groups * p.tpb;
+  const bool inside = rec.y <= p.groups && rec.x >= 0 && rec.x < ctas && rec.x + (rec.y - 1) * p.tpb < ctas;
+  if (rec.y <= 1 || !KVQ_IN(inside, p.flag) || !inside) return;
   const auto at = [&](int i) { return ((int64_t)(rec.x + i * p.tpb) * 2 + (i == 0 ? 1 : 0)) * kLRows + r; };
   float m = -INFINITY;
   for (int i = lane; i < rec.y; i += 32) m = fmaxf(m, p.part_lse[at(i)]);
