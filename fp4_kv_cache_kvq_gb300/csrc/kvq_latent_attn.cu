@@ -4,13 +4,14 @@
 //
 // Mathematics.  With a token's codes and its scale s = 2^e,
 //   S = q . codes,  y = S s (softmax_scale log2 e),  x = 2^(y + e - ref),
-//   out = 2^(ref - m) sum x code / l,  l = sum 2^(y - m).
+//   out = 2^-o sum x code / l,  l = sum x 2^(-e - o).
 // The values' scale is a power of two and stands in x's exponent beside the
 // softmax's own, so the codes enter both products as the cache holds them: a tile
 // is copied once and read twice, as K-major operand (tokens x channels) for S and
-// as MN-major operand (channels x tokens) for the sums.  ref and m are references
-// of a row's own (the largest y + e and y so far), so neither tiny nor huge values
-// beside others make x or l leave their range.
+// as MN-major operand (channels x tokens) for the sums.  ref, of a row's own, goes by the
+// largest y + e so far, and o, if scales lie far apart, by the largest y: the same y + e,
+// rounded once, and exact differences of it stand in x and in l, so that neither tiny nor
+// huge values beside others, nor scores of any size, make the two differ.
 //   q   scaled per row by a power of two to [2^7, 2^8), is the sum of two E4M3
 //       values hi = RNE(q), lo = RNE(q - hi): exact down to 2^-9 of the row's
 //       largest element, off by at most 2^-17 of it below.  hi and lo are rows of
@@ -79,11 +80,12 @@ constexpr int kLSmWarps = 4 * kParts, kLSoftmax = 32 * kLSmWarps, kLThreads = kL
 constexpr int kLdWarpL = kLSmWarps, kSWarpL = kLdWarpL + 1, kOWarpL = kSWarpL + 1;  // and the scales' warp
 constexpr int kPBytes = kLRows * kLT;  // one part (hi or lo) of x, one byte an element
 constexpr int kMinTiles = 2;           // least tiles of a split range
-// x of a row's largest product is 2^kTop .. 2^(kTop + kSlackL): over 2^11.8 the rest
-// behind E5M2 would leave E4M3.  The references are raised only past the slack, since
+// x of a row's largest product is 2^(kTop - kAhead) .. 2^(kTop + kSlackL): over 2^11.8 the rest
+// behind E5M2 would leave E4M3.  (The references lie kTop under the scores: added apart it would
+// be lost beside large ones.)  They are raised only past the slack, since
 // that rescales O (a slack of 3: among 64 rows some raised its own in every second
 // tile, 1100 cycles each).
-constexpr float kTop = 5.0f, kSlackL = 6.0f, kTopInv = 1.0f / 32.0f;
+constexpr float kTop = 5.0f, kSlackL = 6.0f;
 // Where both halves of the tile that raises a reference hold products within 2^kNearL of
 // each other, it is set 2^kAhead higher: larger ones will follow (chunk 2.03 -> 1.85 ms).  A
 // single large one in one half is more likely the largest of all, and leaves the small
@@ -135,7 +137,8 @@ struct LGeo {
   static constexpr int kAlpha = kRefS + 4 * kLRows;       // [2][2][64] factors of O's columns, by group and tile; the result's two
   static constexpr int kShare = kAlpha + 4 * 4 * kLRows;  // [2][kParts][64] what the parts of a row exchange
   static constexpr int kSc = kShare + 2 * kParts * 4 * kLRows;  // [stages][3][64] 2^e, e (-inf: no token), 2^-e
-  static constexpr int kNear = kSc + kStages * 3 * 4 * kLT;  // [stages] all scales within 2^-40 .. 2^40, up to this tile
+  static constexpr int kOff = kSc + kStages * 3 * 4 * kLT;  // [threads][2] l's own references
+  static constexpr int kNear = kOff + 8 * kLSoftmax;  // [stages] all scales within 2^-40 .. 2^40, up to this tile
   static constexpr int kBar = kNear + 4 * 8;
   static constexpr int kMisc = kBar + 8 * kLBars;         // TMEM slot, abort, the groups' [2][2]
   static constexpr int kUsed = kMisc + 32 + 128;
@@ -218,6 +221,14 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
 }
 __device__ __forceinline__ void sts_u32x2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(a), "f"(b) : "memory");
@@ -410,6 +421,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
     float* shared = reinterpret_cast<float*>(base + G::kShare);  // [2][kParts][64]
     float* own = shared + share * kLRows;
     volatile int* gave_up = reinterpret_cast<volatile int*>(misc) + 2 + 2 * grp;  // [2] a wait of the group did, by its tile's parity
+    const uint32_t off = sb + G::kOff + 8 * tid;
     uint32_t it0 = 0;  // tiles before the unit
     while (walk.next(u, tid == 0 ? p.flag : nullptr)) {
       const int64_t row0 = (int64_t)u.b * p.chunk * p.hq + (int64_t)u.r * kLRows;
@@ -503,12 +515,14 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * kLQFull);
 
-      // l counts 2^(y - m).  Short form: m is ref, and 2^(y - ref) is x 2^-e.  That would lose
-      // what scales far apart leave under fp32's range: from the unit's first tile with a
-      // scale outside 2^-40 .. 2^40 on, m is the thread's own largest y, with exponentials of
-      // its own; in both groups, whichever has that tile, since it raises the references that
-      // they share, and over such a one a sum in the short form would become 0.
+      // l counts x 2^(-e - o) over the reference m of the thread's last tile.  Short form: o
+      // is 0.  That would lose what scales far apart leave under fp32's range: from the unit's
+      // first tile with a scale outside 2^-40 .. 2^40 on, o goes by the thread's own largest
+      // (y + e - m) - e, with exponentials of its own; in both groups, whichever has that
+      // tile, since it raises the references that they share, and over such a one a sum in
+      // the short form would become 0.
       float m[2] = {-INFINITY, -INFINITY};
+      sts_f32x2(off, 0.0f, 0.0f);
       uint64_t l2[2] = {0ull, 0ull};
       const int64_t full_upto = min(u.limit, u.first + (u.r * kLRows) / p.hq + 1);  // attended by every row
       bool ready = false;  // the group's next tile's scores are there
@@ -535,7 +549,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kLSFree + grp));
         uint64_t z2[2][kPairs];
-        float top[2], my[2] = {m[0], m[1]};
+        float top[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -552,13 +566,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
               z2[i][k] = pack2(8 * k > lim ? -INFINITY : f.x, 8 * k + 1 > lim ? -INFINITY : f.y);
             }
           }
-          if (!near) {
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-              const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
-              my[i] = fmaxf(my[i], fmaxf(x.x == -INFINITY ? x.x : f.x - x.x, x.y == -INFINITY ? x.y : f.y - x.y));
-            }
-          }
           const float2 a = unpack2(z2[i][0]), b = unpack2(z2[i][1]), c = unpack2(z2[i][2]), d = unpack2(z2[i][3]);
           top[i] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)), fmaxf(fmaxf(c.x, c.y), fmaxf(d.x, d.y)));
         }
@@ -572,7 +579,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           ref[i] = ref_s[lr[i]];
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-          up |= top[i] > ref[i] + kSlackL;
+          up |= top[i] - ref[i] > kTop + kSlackL;
         }
         // raise the references of the rows that need it (what a row gives does not depend on
         // others); a row's two warps agree, the other group's wait for them
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             const float* x = shared + (kParts + 2 * grp) * kLRows + lr[i];
             const float all = fmaxf(x[0], x[kLRows]), other = fminf(x[0], x[kLRows]);
             const float ahead = other > all - kNearL ? kAhead : 0.0f;
-            const float to = all > ref[i] + kSlackL ? floorf(all) + ahead : ref[i];
+            const float to = all - ref[i] > kTop + kSlackL ? floorf(all) + (ahead - kTop) : ref[i];
             a2[i] = to == ref[i] ? 1.0f : fast_exp2(ref[i] - to);
             if (t == 0 && part == 0) ref_s[lr[i]] = to;
             ref[i] = to;
@@ -612,17 +619,26 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         for (int k = 0; k < kPairs; ++k) inv2[k] = lds_f32x2(sc + 8 * kLT + 32 * k);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float rf = kTop - (ref[i] == -INFINITY ? 0.0f : ref[i]);
+          const float rf = ref[i] == -INFINITY ? 0.0f : -ref[i];
           const bool large = __any_sync(0xFFFFFFFFu, top[i] + rf > kE4m3End);  // some x is over 448: E5M2 first
+          const float raise = m[i] == ref[i] ? 0.0f : m[i] - ref[i];  // since the group's last tile
+          m[i] = ref[i];
+#pragma unroll
+          for (int k = 0; k < kPairs; ++k) z2[i][k] = add2(z2[i][k], pack2(rf, rf));
           if (near) {
-            const float a = m[i] == ref[i] ? 1.0f : fast_exp2(m[i] - ref[i]);  // raised since the group's last tile
+            const float a = fast_exp2(raise);
             l2[i] = mul2(l2[i], pack2(a, a));
-            m[i] = ref[i];
           } else {
-            const float to = my[i], zero = to == -INFINITY ? 0.0f : to;
-            const float a = m[i] == -INFINITY ? 1.0f : fast_exp2(m[i] - to);
+            const float o = lds_f32(off + 4 * i) + raise;
+            float to = o;
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+              const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
+              to = fmaxf(to, fmaxf(x.x == -INFINITY ? x.x : f.x - x.x, x.y == -INFINITY ? x.y : f.y - x.y));
+            }
+            const float zero = to == -INFINITY ? 0.0f : to, a = fast_exp2(o - zero);
             l2[i] = mul2(l2[i], pack2(a, a));
-            m[i] = to;
+            sts_f32(off + 4 * i, to);
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) {
               const float2 f = unpack2(z2[i][k]), x = unpack2(x2[k]);
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           uint64_t sum = 0ull;
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            const float2 f = unpack2(add2(z2[i][k], pack2(rf, rf)));
+            const float2 f = unpack2(z2[i][k]);
             const float xa = fast_exp2(f.x), xb = fast_exp2(f.y);
             sum = fma2(pack2(xa, xb), inv2[k], sum);
             const uint32_t h = pack_f16x2(xa, xb);
@@ -647,7 +663,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
             }
             w[i][k] = hi | rest << 16;
           }
-          if (near) l2[i] = fma2(sum, pack2(kTopInv, kTopInv), l2[i]);
+          if (near) l2[i] = add2(sum, l2[i]);
         }
         const uint32_t pb = sb + G::kP + (it & 1) * 2 * kPBytes + (uint32_t)(part * 2048 + 2 * t);
 #pragma unroll
@@ -694,7 +710,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
         __syncwarp();
         if (lane == 0 && !failed) mbar_arrive(bars + 8 * (kLPFull + grp));
       }
-      // the unit's result: O / l, l over the row's parts and for a reference of all
+      // the unit's result: O / l, l over the row's parts and for one offset of all from the
+      // row's last reference
       it0 += (uint32_t)(u.t1 - u.t0);
       if (!failed) failed = !wait(bars + 8 * (kLPvDone + ((it0 - 1) & 1)), ((it0 - 1) >> 1) & 1u);
       if (softmax_or(1, kLSoftmax, failed)) {
@@ -704,6 +721,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
       tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        const float r = ref_s[lr[i]];
+        m[i] = lds_f32(off + 4 * i) + (m[i] == r ? 0.0f : m[i] - r);
         float mq = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
         mq = fmaxf(mq, __shfl_xor_sync(0xFFFFFFFFu, mq, 2));
         if (t == 0) own[kParts * kLRows + lr[i]] = mq;
@@ -728,11 +747,11 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_attn_kernel(const LatentA
           const float* x = shared + lr[i];
           const float r = ref_s[lr[i]];
           const float l = (x[0] + x[kLRows]) + (x[2 * kLRows] + x[3 * kLRows]);
-          const float d = (r == -INFINITY ? 0.0f : r) - kTop - mm[i], h = rintf(0.5f * d);
+          const float d = -mm[i], h = rintf(0.5f * d);
           alpha[lr[i]] = fast_exp2(h);  // two factors: 2^d alone can leave fp32's range
           alpha[kLRows + lr[i]] = l == 0.0f ? 0.0f : fast_exp2(d - h) / l;
           if (!u.whole)
-            p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + lr[i]] = l == 0.0f ? -INFINITY : mm[i] + log2f(l);
+            p.part_lse[((int64_t)blockIdx.x * 2 + u.slot) * kLRows + lr[i]] = l == 0.0f ? -INFINITY : (r == -INFINITY ? 0.0f : r) + (mm[i] + log2f(l));
         }
       }
       named_barrier_sync(1, kLSoftmax);
