@@ -3,7 +3,7 @@
 // cores (tcgen05, accumulators in TMEM), and its C entry point.
 //
 // Mathematics.  Query token i of n sits at position T - n + i and attends 0 .. T - n + i,
-//   y = softmax_scale log2 e (q[:d] . k + q[d:] . k_rope),  P = 2^(y - m),
+//   S = q[:d] . k + q[d:] . k_rope,  P = 2^(f S - m),  f = softmax_scale log2 e,
 //   out = sum P v / sum P.
 // q, k and v enter the products as they are (bf16); P is rounded to bf16, which has
 // fp32's range; sums, maxima and accumulators are fp32.  The reference m of a row is raised
@@ -11,6 +11,9 @@
 // that one that no sum of the unit's P reaches past 1: 8 for the slack and log2 of the
 // positions.  So sum P v stays within fp32's range for every finite v (the largest bf16 values
 // leave no factor at all), at the other end's cost: products under 2^-126 are lost.
+// Where f times that score is over 2^27, m's rounding would stand in P (2^7 in its exponent at
+// 2^31), but neighbouring fp32 scores lie 2^8 in P and more apart: the row takes a power of two
+// for f, for which f S and m, then without the room, are exact.
 //
 // What bounds it: the tensor pipe, 2 (2 d + 64) flop per attended pair and head; a
 // unit's tiles come from L2, 51 KB per 80 positions at d = 128.
@@ -227,8 +230,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
     const uint32_t s_col = tw + G::kSCol + x * kET, p_col = tw + G::kPCol + x * (kET / 2), o_col = tw + x * D;
     const int ntx = x < nx ? tiles_of(x) : 0;
     const int last = first + i, all = first + kERows * x;  // last position of the row, of every row
-    const float count = (float)(32 - __clz(first + rows - 1)), room = count + kSlackE;  // log2 of the positions, rounded up
-    float ref = -INFINITY;
+    const float room = (float)(32 - __clz(first + rows - 1)) + kSlackE;  // (log2 of the positions, rounded up)
+    // the score that set the row's m, the one that a larger one has to pass to raise it, f and m
+    float ref = -INFINITY, past = -INFINITY, f = p.scale_log2, m = room;
     uint64_t l2 = 0ull;
     bool ok = true;
     for (int j = 0; j < ntx && ok; ++j) {
@@ -255,15 +259,22 @@ __global__ void __launch_bounds__(kEThreads, 1)
 #pragma unroll
         for (int k = 0; k < kET / 16; ++k) top = fmaxf(top, __uint_as_float(mx[k]));
       }
-      top *= p.scale_log2;
       // the sums of the tile before: done with O and P
       if (j > 0 && !(ok = wait(bars + 8 * (kEPvDone + x), (j - 1) & 1u))) break;
       tc_fence_after();
-      const bool up = top > ref - count;
+      const bool up = top > past;
       if (__any_sync(0xFFFFFFFFu, up)) {
-        const float to = up ? top + room : ref, a = up ? fast_exp2(ref - to) : 1.0f;
+        float a = 1.0f;
+        if (up) {
+          const float y = fabsf(top * p.scale_log2), old = f, m_old = m;
+          const bool far = y > 134217728.0f;
+          f = far ? __uint_as_float((__float_as_uint(p.scale_log2) + 0x400000u) & 0x7F800000u) : p.scale_log2;
+          m = fmaf(top, f, far ? 0.0f : y > 16384.0f ? room + 4.0f : room);  // (4: half its steps under 2^27)
+          a = ref == -INFINITY ? 0.0f : fast_exp2(fmaf(ref, f, -m) - fmaf(ref, old, -m_old));
+          ref = top;
+          past = __fadd_rd(ref, kSlackE / p.scale_log2);
+        }
         l2 = mul2(l2, pack2(a, a));
-        ref = to;
         if (j > 0) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -275,8 +286,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
           }
         }
       }
-      const float zero = ref == -INFINITY ? 0.0f : -ref;
-      const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), r2 = pack2(zero, zero);
+      const uint64_t c2 = pack2(f, f), r2 = pack2(-m, -m);
 #pragma unroll
       for (int k = 0; k < kET / 16; ++k) {
         uint32_t w[8];
