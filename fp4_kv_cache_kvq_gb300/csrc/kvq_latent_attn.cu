@@ -51,14 +51,15 @@
 // the hand-offs between the groups, are what is left.  The batch of 16 heads stays where
 // it is in each of these: a third of its time is start, change of unit, end and join.
 // Measured (TFLOP/s of the absorbed form, 2 (2 L + R) per pair; L 512, R 64, page 64, L2
-// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.81 ms, 1210; 64 x 8192
-// positions, 16 heads 91 us, 3.7 TB/s; 16 x 32768, 128 heads 151 us, 968.
+// flushed): chunk of 1024 over 8192, 2 sequences, 64 heads 1.77 ms, 1237; 64 x 8192
+// positions, 16 heads 89 us, 3.8 TB/s; 16 x 32768, 128 heads 150 us, 974.
 // From 3.71 ms for the chunk: softmax on eight warps instead of four 3.45; a tile's
 // scales prepared by a warp of their own 3.31; MMAs issued by an elected lane 2.53;
 // scores and sums issued by a warp each 2.46; the references' slack 3 -> 6 (E5M2 first
 // over 448) 2.36; two groups of eight, with waits suspended in the barrier instead of
 // polling, 2.07; a wait that is over looked at once 2.03; references set ahead 1.85;
-// a row's references settled by its own two warps, O rescaled after the weights 1.81.
+// a row's references settled by its own two warps, O rescaled after the weights 1.81;
+// l's form decided by the scales' warp, kTop within the references 1.77.
 // Slower: A kept in the collector for the second MMA of a pair (the second one's B is then
 // read in the first one's type); waits by one lane of a warp (2.79) or by one warp of a group
 // (2.26); polling 64 times before suspending (3.94); four warps a group 2.35; warps

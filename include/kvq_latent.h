@@ -28,6 +28,7 @@
  * value 4, its steps end at 2^-9).  The append sets s to the smallest power of two with
  * max(|c|, |k|) <= 448 s, at least 2^-126.  e = 255 marks a token that held an
  * Inf or NaN (its codes are 0): it reads back as NaN.  Codes are never NaN.
+ * (A latent over 248 2^120, bf16's last 3%, rounds to 2^128, which is Inf in fp32.)
  */
 #ifndef KVQ_LATENT_H
 #define KVQ_LATENT_H
@@ -125,8 +126,10 @@ kvq_status kvq_latent_dequant(const kvq_latent_cache *cache, int32_t batch, cons
  * q enters the products exactly down to 2^-9 of its row's largest element, and
  * off by at most 2^-17 of that below (2^-136 in rows whose largest is under
  * 2^-119).  A weight enters the second product times its token's scale, off by at
- * most 2^-8 of that, or 2^-17 of the largest such product that the row attends.
- * Sums, softmax statistics and their joins are fp32.
+ * most 2^-8 + 2^-11 of that, or 2^-17 of the largest such product that the row attends.
+ * Sums, softmax statistics and their joins are fp32.  So are scores, times
+ * softmax_scale log2 e: they have to lie in its range (softmax_scale times the row's
+ * and a token's largest magnitude under 2^115 is enough).
  * A row that attends a token marked as non-finite, or whose query holds an Inf
  * or NaN, is NaN; no other row is touched by either.
  * Device flags: BAD_LENGTH (n_b outside 0..chunk: the sequence is skipped;
@@ -150,8 +153,9 @@ kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t
  *   head_dim (d)  64 or 128; rope_dim 64.
  *   q            device bf16 [batch][chunk][num_heads][d + rope_dim], contiguous.
  *   k, v         device bf16: d contiguous values per head and token, strides
- *                in elements from head to head and from token to token, tokens
- *                in the order [batch][max_len].
+ *                in elements from head to head (at least d) and from token to
+ *                token (at least a token's heads: head-major keys are refused),
+ *                tokens in the order [batch][max_len].
  *   k_rope       device bf16: rope_dim contiguous values per token,
  *                k_rope_stride elements from token to token.
  *                Strides are multiples of 8, all pointers 16-byte aligned.
@@ -159,11 +163,14 @@ kvq_status kvq_latent_attn(const kvq_latent_cache *cache, int32_t batch, int32_t
  *                are not used.
  *   out          device [batch][chunk][num_heads][d] of out_dtype, 16-byte aligned.
  * q, k and v enter the products as they are; a weight is rounded to bf16, sums and
- * softmax statistics are fp32.  Finite values up to bf16's largest do not overflow a sum;
- * products of a weight and a value that are under fp32's normal range are lost, which is
- * less than T_b^2 2^-117 in a result.  A row that attends a value that is Inf or NaN is
- * not finite in its channel; no Inf or NaN among the keys and values behind a
- * row's position reaches the row.  A row whose scores are all -Inf is NaN.
+ * softmax statistics are fp32; scores have to lie in its range, with softmax_scale log2 e
+ * and without.  Finite values up to bf16's largest do not overflow a sum where the
+ * scores, times softmax_scale log2 e, are under 2^27 (over larger ones, 2^119 / T_b and
+ * less does not).  Products of a weight and a value that are under fp32's normal range
+ * are lost, which is less than T_b^2 2^-117 in a result (T_b^2 2^-109 over scores past
+ * 2^14).  A row that attends a value that is Inf or NaN is not finite in its channel; no
+ * Inf or NaN among the keys and values behind a row's position reaches the row.  A row
+ * whose scores are all -Inf is NaN.
  * Host errors: INVALID_ARGUMENT, UNSUPPORTED (2^30 rows and more, max_len above
  * 2^30).
  * Device flags: BAD_LENGTH (n_b outside 0..chunk, T_b > max_len: the sequence is
